@@ -194,6 +194,29 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
                                w4a16_stream_t stream);
 
 /*
+ * The gate/up projection of a SwiGLU feed-forward for any m >= 1 (a prompt, a
+ * training batch): packed [2n, k/8] and scales [2n, k/group] interleave gate and
+ * up rows as for w4a16_gemv_swiglu, y [m, n] = fp16(SiLU(g) * u) with g, u the
+ * fp32-accumulated products and SiLU(g) = g / (1 + e^-g) in fp32.  `gate_up`
+ * (fp16 [m, 2n], 16-byte aligned, or NULL) receives the products themselves, each
+ * rounded once, g of output i in column 2i and u in column 2i + 1: what
+ * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
+ * m <= 16 without gate_up runs as w4a16_gemv_swiglu, m <= 32 on the
+ * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
+ * Workspace rules as for w4a16_gemm (zero-filled once before its first use; calls
+ * one after another on one stream may share it, also with w4a16_gemm and the
+ * other operators below), its size from w4a16_gemm_swiglu_workspace_bytes.
+ * Errors as w4a16_gemm; k == 0 writes zeros.
+ */
+w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                               uint16_t* gate_up, int64_t m, int64_t n, int64_t k, int32_t group, void* workspace,
+                               size_t workspace_bytes, w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_gemm_swiglu needs (n outputs, i.e. 2n weight
+ * rows) on the current device; 0: none, the pointer may be NULL. */
+size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
  * MoE grouped GEMM (the routed-expert layers of the 35B-A3B MoE model on the
  * LLM170 CUDA/W4A16 page, g32).  x [rows, k] holds one row per (token, expert)
  * pair, sorted by expert; rows offsets[e] .. offsets[e+1]-1 belong to expert e

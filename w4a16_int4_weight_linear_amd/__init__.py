@@ -13,6 +13,7 @@ there is no fallback path of any kind.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -58,6 +59,8 @@ SIGNATURES = {
     "w4a16_grouped_gemm_gather": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32,
                                                  _vp]),
     "w4a16_moe_combine": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _vp]),
+    "w4a16_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "w4a16_gemm_swiglu_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_grouped_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32,
                                                  _vp]),
 }
@@ -303,6 +306,71 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
     return out
 
 
+# ---------------------------------------------------------------------------
+# The feed-forward block for any number of rows, with its backward pass.
+#
+# These calls run on the tensors' own device whichever is current, allocate on
+# the stream they launch on, and keep one workspace per (device, stream).  Under
+# graph capture each call takes a workspace of its own from the graph's pool (its
+# zero fill is part of the graph), so captured graphs share none.
+# ---------------------------------------------------------------------------
+def _launch_on(what, device, stream):
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+_FFN_WORKSPACES = {}
+
+
+def _ffn_workspace(nbytes, device):
+    """A zero-filled workspace (None if none is needed) for a call on the current stream of `device`."""
+    torch = _torch()
+    if nbytes == 0:
+        return None
+    words = (nbytes + 15) // 16 * 4
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(words, dtype=torch.int32, device=device)
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    ws = _FFN_WORKSPACES.get(key)
+    if ws is None or ws.numel() < words:
+        ws = _FFN_WORKSPACES[key] = torch.zeros(words, dtype=torch.int32, device=device)
+    return ws
+
+
+def _ws_args(ws):
+    return (_ptr(ws), ws.numel() * 4 if ws is not None else 0)
+
+
+def _given_workspace(what, workspace):
+    return [] if workspace is None else [("workspace", workspace, "i32", None)]
+
+
+def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace=None, stream=None):
+    """y [m, n] = SiLU(x . Wg^T) * (x . Wu^T) for any m; packed [2n, k/8] interleaves gate/up rows.
+    gate_up (fp16 [m, 2n]), if given, receives the products themselves for gemm_swiglu_backward."""
+    m, n, k, specs = _dense_shapes("gemm_swiglu", x, packed, scales, group, rows_per_out=2)
+    specs = specs + _given_workspace("gemm_swiglu", workspace)
+    if gate_up is not None:
+        specs.append(("gate_up", gate_up, "f16", (m, 2 * n)))
+    if out is not None:
+        specs.append(("out", out, "f16", (m, n)))
+    _check_tensors("gemm_swiglu", specs)
+    with _launch_on("gemm_swiglu", x.device, stream):
+        if out is None:
+            out = _torch().empty((m, n), dtype=x.dtype, device=x.device)
+        if workspace is None:
+            workspace = _ffn_workspace(lib.w4a16_gemm_swiglu_workspace_bytes(m, n, k, group), x.device)
+        _check(lib.w4a16_gemm_swiglu(_ptr(x), _ptr(packed), _ptr(scales), _ptr(out), _ptr(gate_up), m, n, k, group,
+                                     *_ws_args(workspace), _stream(None)), "w4a16_gemm_swiglu")
+    return out
+
+
 def _bank_shapes(what, packed, scales, k, group):
     _require_tensors(what, packed=packed, scales=scales)
     if packed.dim() != 3 or scales.dim() != 3:
@@ -404,4 +472,4 @@ def moe_combine(y_pairs, pair_row, weights, out=None, stream=None):
 __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "unpack", "gemv", "gemm",
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
-           "grouped_gemm_gather", "moe_combine"] + list(SIGNATURES)
+           "grouped_gemm_gather", "moe_combine", "gemm_swiglu"] + list(SIGNATURES)

@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/w4a16.h"
+#include "checks.hpp"
 #include "kernels.hpp"
 
 namespace w4a16 {
@@ -49,13 +50,14 @@ namespace {
 
 using w4a16::DeviceInfo;
 
-bool valid_group(int32_t g) { return g == 32 || g == 128; }
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using w4a16::aligned;
+using w4a16::as_status;
+using w4a16::common_dense_checks;
+using w4a16::kMaxBufferBytes;
+using w4a16::kMaxDim;
+using w4a16::status_of;
+using w4a16::valid_group;
 
-// Activations, packed weights and scales are addressed with 32-bit buffer
-// offsets below 2^31 (an offset of 2^31 marks an out-of-range load).
-constexpr int64_t kMaxBufferBytes = (int64_t)1 << 31;
-constexpr int64_t kMaxDim = (int64_t)1 << 30;
 // Experts the routing kernel counts in LDS (one int per expert beside 4 KB).
 constexpr int32_t kMaxRouteExperts = 32768;
 
@@ -66,24 +68,6 @@ bool bank_fits(int64_t experts, int64_t n, int64_t k) {
   if (per >= kMaxBufferBytes) return false;
   return per == 0 || experts < kMaxBufferBytes / per;
 }
-
-int common_dense_checks(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
-                        int64_t m, int64_t n, int64_t k, int32_t group) {
-  if (!valid_group(group)) return W4A16_ERR_GROUP;
-  if (m < 0 || n < 0 || k < 0 || k % group) return W4A16_ERR_SHAPE;
-  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return W4A16_ERR_SHAPE;
-  if (m == 0 || n == 0) return -1;  // no-op
-  if (!y) return W4A16_ERR_NULL;
-  if (k > 0 && (!x || !packed || !scales)) return W4A16_ERR_NULL;
-  if (!aligned(y, 16) || (k > 0 && (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 2))))
-    return W4A16_ERR_ALIGN;
-  if (n * (k / 2) >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
-  if (2 * m * k >= kMaxBufferBytes || 2 * m * n >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
-  return W4A16_OK;
-}
-
-w4a16_status status_of(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
-w4a16_status as_status(int s) { return static_cast<w4a16_status>(s); }
 
 // Which kernels w4a16_gemm runs: up to 32 rows the product is a weight stream
 // (m <= 4: the decode GEMV kernels while their plan fits; 5..32: the

@@ -1,0 +1,79 @@
+// api_ffn.cpp -- the C ABI of the feed-forward block's training operators:
+// argument validation and dispatch, in the order and with the codes of api.cpp.
+#include <hip/hip_runtime_api.h>
+
+#include <cstdint>
+
+#include "../../include/w4a16.h"
+#include "checks.hpp"
+#include "kernels.hpp"
+
+namespace {
+
+using w4a16::aligned;
+using w4a16::as_status;
+using w4a16::common_dense_checks;
+using w4a16::DeviceInfo;
+using w4a16::kMaxDim;
+using w4a16::status_of;
+using w4a16::valid_group;
+
+// Up to 32 rows the gate/up product is a weight stream: one pass of the
+// weight-streaming kernel per 16 rows, as in w4a16_gemm; beyond, the tiled GEMM.
+constexpr int64_t kSkinnyRows = 32;
+
+bool swiglu_skinny(int64_t m, int64_t n2, int64_t k, const DeviceInfo& dev) {
+  return m <= kSkinnyRows && w4a16::gemm_skinny_fits((int)(m < 16 ? m : 16), (int)n2, (int)k, dev);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
+  if (!valid_group(group) || m <= 0 || n <= 0 || k <= 0 || k % group) return 0;
+  if (m > kMaxDim || n > kMaxDim / 2 || k > kMaxDim) return 0;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return 0;
+  if (swiglu_skinny(m, 2 * n, k, dev)) return 0;
+  return w4a16::gemm_workspace_bytes(m, 2 * n, k, group, dev);
+}
+
+w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                               uint16_t* gate_up, int64_t m, int64_t n, int64_t k, int32_t group, void* workspace,
+                               size_t workspace_bytes, w4a16_stream_t stream) {
+  if (!valid_group(group)) return W4A16_ERR_GROUP;
+  if (n < 0 || n > kMaxDim / 2) return W4A16_ERR_SHAPE;
+  // the weights and the kept products have 2n columns (the size bounds are taken on those)
+  const int c = common_dense_checks(x, packed, scales, y, m, 2 * n, k, group);
+  if (c < 0) return W4A16_OK;
+  if (c != W4A16_OK) return as_status(c);
+  if (!aligned(gate_up, 16) || !aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (k == 0) {   // SiLU(0) * 0
+    const hipError_t e = gate_up ? w4a16::launch_zero_fill(gate_up, (size_t)(2 * m * n), st) : hipSuccess;
+    return status_of(e != hipSuccess ? e : w4a16::launch_zero_fill(y, (size_t)(m * n), st));
+  }
+  // up to 16 rows with nothing kept: the decode product (its kernels for 1-4 rows are faster)
+  if (!gate_up && m <= 16) return w4a16_gemv_swiglu(x, packed, scales, y, m, n, k, group, stream);
+  if (swiglu_skinny(m, 2 * n, k, dev)) {
+    for (int64_t m0 = 0; m0 < m; m0 += 16) {
+      const int mm = (int)(m - m0 < 16 ? m - m0 : 16);
+      const hipError_t e =
+          gate_up ? w4a16::launch_swiglu_skinny_keep(x + m0 * k, packed, scales, y + m0 * n, gate_up + m0 * 2 * n, mm,
+                                                     (int)n, (int)k, group, dev, st)
+                  : w4a16::launch_swiglu_skinny(x + m0 * k, packed, scales, y + m0 * n, mm, (int)n, (int)k, group,
+                                                dev, st);
+      if (e != hipSuccess) return W4A16_ERR_HIP;
+    }
+    return W4A16_OK;
+  }
+  const size_t need = w4a16::gemm_workspace_bytes(m, 2 * n, k, group, dev);
+  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  return status_of(w4a16::launch_gemm_swiglu(x, packed, scales, y, gate_up, (int)m, (int)n, (int)k, group,
+                                             need ? workspace : nullptr, dev, st));
+}
+
+}  // extern "C"

@@ -41,6 +41,13 @@
 //   at the end by their contributors in a fixed order (deterministic).  The
 //   details are at gemm_plan.
 //
+// * The gate/up pair of a SwiGLU feed-forward runs on the same kernel (EPI below):
+//   the weight rows interleave gate and up, so a pair sits in neighbouring lanes
+//   of an accumulator block.  The epilogue swaps one value per lane pair (even
+//   lanes then hold both halves of one row, odd lanes of the next), applies
+//   SiLU(g) u to the fp32 sums and rounds once; the m x 2n intermediate reaches
+//   memory only if the caller keeps it for a backward pass.
+//
 // For integer activations, codes and power-of-two scales every product and
 // partial sum is exact, so such inputs give bit-exact results.
 #include <mutex>
@@ -180,16 +187,33 @@ struct Item {
   bool dp;
 };
 
+// What the epilogue writes: the product; or, with weight rows that interleave
+// SwiGLU gate (even) and up (odd) rows, y [M, N / 2] = SiLU(gate) * up, without
+// or with the product itself (fp16, z [M, N]).
+enum Epilogue { kEpiProduct, kEpiSwiglu, kEpiSwigluKeep };
+
+// Two rows of a (gate, up) column pair.  a0, a1: this lane's column in two
+// accumulator rows.  Lanes 2i and 2i + 1 hold a pair's gate and up columns; after
+// the swap the even lane has both for row 0 and returns its SiLU(g) u, the odd
+// lane those of row 1.
+__device__ inline float swiglu_pair(float a0, float a1, bool odd) {
+  const float send = odd ? a0 : a1;
+  const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                                  0, __builtin_bit_cast(int, send), 0xB1, 0xf, 0xf, false));
+  const float g = odd ? got : a0, u = odd ? a1 : got;
+  return g / (1.0f + __expf(-g)) * u;
+}
+
 // SALIGN: every row's scales start on a 16-byte boundary (K / G a multiple
 // of 8 and a 16-byte aligned scale array), so they come in LDS windows;
 // otherwise with the stages.
-template <int G, bool KTAIL, bool SALIGN>
+template <int G, bool KTAIL, bool SALIGN, int EPI>
 __global__ void __launch_bounds__(kThreads)
 gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
             int M, int N, int K, int tiles_m, int tiles_n, int iters, int rounds, int sk_tiles, int nsk,
             float* __restrict__ partials, uint32_t* __restrict__ flags, uint32_t* __restrict__ counters,
-            uint32_t* __restrict__ status) {
+            uint32_t* __restrict__ status, uint16_t* __restrict__ z) {
   constexpr int kGroups = BK / G;            // scale groups per K step (1 or 4)
   constexpr int kSBytes = SALIGN ? 0 : BN * kGroups * 4;       // per-stage scales (unaligned case)
   constexpr int kStage = kStageBytes + kSBytes;
@@ -501,8 +525,10 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
       static_assert(kWaves * 64 * kPitch <= kStageBytes, "epilogue slabs exceed stage 2");
       uint8_t* ep = stage2 + wave * 64 * kPitch;
       uint8_t* ew = ep + 4 * h * kPitch + li * 2;
+      // the product itself: y, or the kept intermediate z
+      uint16_t* const prod = EPI == kEpiProduct ? y : z;
 #pragma unroll
-      for (int pass = 0; pass < 2; ++pass) {
+      for (int pass = 0; pass < (EPI == kEpiSwiglu ? 0 : 2); ++pass) {
 #pragma unroll
         for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -518,13 +544,46 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
           const u32x4 v = *reinterpret_cast<const u32x4*>(ep + row * kPitch + c * 16);
           const int m = m0 + 64 * pass + row, n = nw + 8 * c;
           if (m < M) {
-            uint16_t* dst = y + (size_t)m * N + n;
+            uint16_t* dst = prod + (size_t)m * N + n;
             if (n + 8 <= N && (N & 7) == 0) {
               *reinterpret_cast<u32x4*>(dst) = v;
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (n + e < N) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+      if constexpr (EPI != kEpiProduct) {
+        // SiLU(gate) up: 16 outputs per row and wave, [row][16 columns] with a
+        // 48-byte row pitch, the wave's 128 rows in one pass
+        constexpr int kHPitch = kWaveN + 16;
+        static_assert(kWaves * 128 * kHPitch <= kStageBytes, "SwiGLU slabs exceed stage 2");
+        const bool odd = li & 1;
+        uint8_t* hp = stage2 + wave * 128 * kHPitch;
+        uint8_t* hw = hp + (4 * h + (odd ? 1 : 0)) * kHPitch + (li >> 1) * 2;
+        const int No = N >> 1;
+        if constexpr (EPI == kEpiSwigluKeep) lds_barrier();   // another wave's z slab overlaps this wave's h slab
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; r += 2)
+            *reinterpret_cast<uint16_t*>(hw + (i * 32 + 8 * (r >> 2) + (r & 3)) * kHPitch) =
+                float_to_half_bits(swiglu_pair(acc[i][0][r], acc[i][0][r + 1], odd));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 32 * j + (lane >> 1), c = lane & 1;
+          const u32x4 v = *reinterpret_cast<const u32x4*>(hp + row * kHPitch + c * 16);
+          const int m = m0 + row, n = (nw >> 1) + 8 * c;
+          if (m < M) {
+            uint16_t* dst = y + (size_t)m * No + n;
+            if (n + 8 <= No && (No & 7) == 0) {
+              *reinterpret_cast<u32x4*>(dst) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (n + e < No) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
             }
           }
         }
@@ -609,7 +668,9 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
     // the contributors' quads are summed in contributor order, 8 loads in flight
     constexpr int kChunks = kMB * kNB * 4 * kThreads;
     const int qs = lwg - c0;
-    const int ch0 = kChunks * qs / parts, ch1 = kChunks * (qs + 1) / parts;
+    // (slices of whole column pairs, so a pair's gate and up are summed by neighbouring lanes)
+    constexpr int kPairMask = EPI == kEpiProduct ? ~0 : ~1;
+    const int ch0 = (kChunks * qs / parts) & kPairMask, ch1 = (kChunks * (qs + 1) / parts) & kPairMask;
     for (int c = ch0 + tid; c < ch1; c += kThreads) {
       auto quad = [&](int l) {
         return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -634,7 +695,17 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int m = m0 + i * 32 + 8 * q + 4 * ch + r;
-          if (m < M) y[(size_t)m * N + n] = failed ? (uint16_t)0x7E00u : float_to_half_bits(v[r]);
+          if (EPI != kEpiSwiglu && m < M)
+            (EPI == kEpiProduct ? y : z)[(size_t)m * N + n] = failed ? (uint16_t)0x7E00u : float_to_half_bits(v[r]);
+        }
+        if constexpr (EPI != kEpiProduct) {
+          const bool odd = n & 1;
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const float o = swiglu_pair(v[r], v[r + 1], odd);
+            const int m = m0 + i * 32 + 8 * q + 4 * ch + r + (odd ? 1 : 0);
+            if (m < M) y[(size_t)m * (N >> 1) + (n >> 1)] = failed ? (uint16_t)0x7E00u : float_to_half_bits(o);
+          }
         }
       }
     }
@@ -699,8 +770,10 @@ size_t gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int, const DeviceIn
   return kWorkspaceHeader + 2 * (size_t)p.wgs * kPartialBytes + 3 * (size_t)p.wgs * sizeof(uint32_t);
 }
 
-hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
-                       int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
+namespace {
+template <int EPI>
+hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
+                      int m, int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const GemmPlan p = gemm_plan(m, n, k, dev);
   float* partials = nullptr;
   uint32_t* flags = nullptr;
@@ -715,12 +788,25 @@ hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t
   }
   const bool tail = k % BK != 0;
   const bool salign = (k / group) % 8 == 0 && (reinterpret_cast<uintptr_t>(scales) & 15) == 0;
-  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true> : gemm_kernel<128, false, false>)
-              : tail       ? gemm_kernel<32, true, false>
-              : salign     ? gemm_kernel<32, false, true>
-                           : gemm_kernel<32, false, false>;
+  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true, EPI> : gemm_kernel<128, false, false, EPI>)
+              : tail       ? gemm_kernel<32, true, false, EPI>
+              : salign     ? gemm_kernel<32, false, true, EPI>
+                           : gemm_kernel<32, false, false, EPI>;
   return launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m,
-                       p.tiles_n, p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status);
+                       p.tiles_n, p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
+}
+}  // namespace
+
+hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                       int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
+  return launch_epi<kEpiProduct>(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream);
+}
+
+hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                              uint16_t* z, int m, int n_out, int k, int group, void* workspace,
+                              const DeviceInfo& dev, hipStream_t stream) {
+  return z ? launch_epi<kEpiSwigluKeep>(x, packed, scales, y, z, m, 2 * n_out, k, group, workspace, dev, stream)
+           : launch_epi<kEpiSwiglu>(x, packed, scales, y, nullptr, m, 2 * n_out, k, group, workspace, dev, stream);
 }
 
 }  // namespace w4a16

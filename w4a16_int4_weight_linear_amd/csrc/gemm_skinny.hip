@@ -56,12 +56,13 @@ static_assert(kWaves * kMaxBlocks * 1024 <= kLds, "the final partial tiles reuse
 
 // SWIGLU: the 2 n weight rows interleave gate (even) and up (odd) rows of n
 // outputs; workgroup ranges are whole pairs and the epilogue writes
-// y[m, i] = SiLU(gate_i) * up_i (fp32, rounded once) instead of both rows.
-template <int G, bool ALIGNED, bool SWIGLU>
+// y[m, i] = SiLU(gate_i) * up_i (fp32, rounded once) instead of both rows.  KEEP:
+// both rows go to z [M, N] as well (the fp16 pre-activations a backward pass reads).
+template <int G, bool ALIGNED, bool SWIGLU, bool KEEP>
 __global__ void __launch_bounds__(kThreads)
 gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
                    const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
-                   int M, int N, int K, int rows_base, int rows_extra) {
+                   int M, int N, int K, int rows_base, int rows_extra, uint16_t* __restrict__ z) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -335,6 +336,10 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
           const float g = t[j];
           const float v = g / (1.0f + __expf(-g)) * t[j + 1];
           y[(size_t)li * (N >> 1) + ((r0 + rr) >> 1)] = float_to_half_bits(v);
+          if constexpr (KEEP) {
+            z[(size_t)li * N + r0 + rr] = float_to_half_bits(g);
+            z[(size_t)li * N + r0 + rr + 1] = float_to_half_bits(t[j + 1]);
+          }
         }
       }
     } else {
@@ -347,11 +352,11 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
   }
 }
 
-template <int G, bool ALIGNED, bool SWIGLU>
-hipError_t launch_ga(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
-                     int k, int blocks, int units, hipStream_t stream) {
-  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU>, dim3(blocks), dim3(kThreads), 0, stream, x, packed,
-                       scales, y, m, n, k, units / blocks, units % blocks);
+template <int G, bool ALIGNED, bool SWIGLU, bool KEEP>
+hipError_t launch_ga(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
+                     int m, int n, int k, int blocks, int units, hipStream_t stream) {
+  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU, KEEP>, dim3(blocks), dim3(kThreads), 0, stream, x,
+                       packed, scales, y, m, n, k, units / blocks, units % blocks, z);
 }
 
 // n weight rows in units of `unit` rows (2: gate/up pairs); returns the grid.
@@ -366,9 +371,9 @@ int skinny_grid(int n, int unit, const DeviceInfo& dev) {
   return g;
 }
 
-template <bool SWIGLU>
-hipError_t launch_s(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
-                    int k, int group, const DeviceInfo& dev, hipStream_t stream) {
+template <bool SWIGLU, bool KEEP>
+hipError_t launch_s(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
+                    int m, int n, int k, int group, const DeviceInfo& dev, hipStream_t stream) {
   const int unit = SWIGLU ? 2 : 1;
   const int g = skinny_grid(n, unit, dev);
   const int units = n / unit;
@@ -376,11 +381,10 @@ hipError_t launch_s(const uint16_t* x, const uint32_t* packed, const uint16_t* s
   // one vector load per row brings a line's scales when every scale row is
   // 16-byte (g32) or 4-byte (g128) aligned in memory
   const uintptr_t sp = reinterpret_cast<uintptr_t>(scales);
-  if (group == 32)
-    return spr % 8 == 0 && (sp & 15) == 0 ? launch_ga<32, true, SWIGLU>(x, packed, scales, y, m, n, k, g, units, stream)
-                                          : launch_ga<32, false, SWIGLU>(x, packed, scales, y, m, n, k, g, units, stream);
-  return spr % 2 == 0 && (sp & 3) == 0 ? launch_ga<128, true, SWIGLU>(x, packed, scales, y, m, n, k, g, units, stream)
-                                       : launch_ga<128, false, SWIGLU>(x, packed, scales, y, m, n, k, g, units, stream);
+  const bool al = group == 32 ? spr % 8 == 0 && (sp & 15) == 0 : spr % 2 == 0 && (sp & 3) == 0;
+  auto launch = group == 32 ? (al ? launch_ga<32, true, SWIGLU, KEEP> : launch_ga<32, false, SWIGLU, KEEP>)
+                            : (al ? launch_ga<128, true, SWIGLU, KEEP> : launch_ga<128, false, SWIGLU, KEEP>);
+  return launch(x, packed, scales, y, z, m, n, k, g, units, stream);
 }
 
 }  // namespace
@@ -392,12 +396,18 @@ bool gemm_skinny_fits(int m, int n, int k, const DeviceInfo& dev) {
 
 hipError_t launch_gemm_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                               int n, int k, int group, const DeviceInfo& dev, hipStream_t stream) {
-  return launch_s<false>(x, packed, scales, y, m, n, k, group, dev, stream);
+  return launch_s<false, false>(x, packed, scales, y, nullptr, m, n, k, group, dev, stream);
 }
 
 hipError_t launch_swiglu_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                 int m, int n_out, int k, int group, const DeviceInfo& dev, hipStream_t stream) {
-  return launch_s<true>(x, packed, scales, y, m, 2 * n_out, k, group, dev, stream);
+  return launch_s<true, false>(x, packed, scales, y, nullptr, m, 2 * n_out, k, group, dev, stream);
+}
+
+hipError_t launch_swiglu_skinny_keep(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                                     uint16_t* z, int m, int n_out, int k, int group, const DeviceInfo& dev,
+                                     hipStream_t stream) {
+  return launch_s<true, true>(x, packed, scales, y, z, m, 2 * n_out, k, group, dev, stream);
 }
 
 }  // namespace w4a16

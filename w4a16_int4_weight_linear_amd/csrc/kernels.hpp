@@ -52,6 +52,11 @@ hipError_t launch_gemm_skinny(const uint16_t* x, const uint32_t* packed, const u
 hipError_t launch_swiglu_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                 int m, int n_out, int k, int group, const DeviceInfo& dev, hipStream_t stream);
 
+// The same, also writing the gate and up products themselves (fp16, z [m, 2 n_out]).
+hipError_t launch_swiglu_skinny_keep(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                                     uint16_t* z, int m, int n_out, int k, int group, const DeviceInfo& dev,
+                                     hipStream_t stream);
+
 // ---- prefill GEMM (gemm.hip) ----
 // The workspace starts with a status word (non-zero after a stream-K fix-up
 // gave up waiting), padded to kWorkspaceHeader bytes; the partial tiles follow.
@@ -65,6 +70,11 @@ size_t gemm_workspace_flags_offset(int64_t m, int64_t n, int64_t k, const Device
 hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                        int m, int n, int k, int group, void* workspace, const DeviceInfo& dev,
                        hipStream_t stream);
+// y [m, n_out] = SiLU(gate) * up, packed/scales holding 2 n_out interleaved rows; with z, the
+// products themselves too (fp16 [m, 2 n_out]).  Workspace as launch_gemm for n = 2 n_out.
+hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                              uint16_t* z, int m, int n_out, int k, int group, void* workspace,
+                              const DeviceInfo& dev, hipStream_t stream);
 
 // ---- MoE grouped GEMM (grouped_gemm.hip) ----
 hipError_t launch_grouped_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales,
