@@ -217,6 +217,27 @@ w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const 
 size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
 
 /*
+ * The product with the other side of the weights, any m >= 1:
+ *
+ *     y[m, k] = sum_n d[m, n] * s[n, k / group] * q[n, k]
+ *
+ * for d [m, n] and y [m, k] fp16: with d the gradient of a product's output, y is
+ * the gradient of its input.  Packed weights and scales are those of the forward
+ * product (there is no second layout).  Weights enter as fp16(s q), sums are fp32,
+ * y is rounded once.  n is any size; n == 0 writes zeros, k == 0 is a no-op.  A
+ * column k whose weights are all zero still carries an infinity or NaN of d, as
+ * the formula does.  The workspace (w4a16_gemm_t_workspace_bytes; 0: none) needs
+ * no initial state, and no call waits for another: calls on several streams may
+ * run at once, each with a workspace of its own.  Errors as w4a16_gemm.
+ */
+w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
+                          int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                          w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_gemm_t needs on the current device. */
+size_t w4a16_gemm_t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
  * MoE grouped GEMM (the routed-expert layers of the 35B-A3B MoE model on the
  * LLM170 CUDA/W4A16 page, g32).  x [rows, k] holds one row per (token, expert)
  * pair, sorted by expert; rows offsets[e] .. offsets[e+1]-1 belong to expert e

@@ -60,6 +60,8 @@ SIGNATURES = {
                                                  _vp]),
     "w4a16_moe_combine": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i32, _i64, _i64, _vp]),
     "w4a16_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "w4a16_gemm_t": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "w4a16_gemm_t_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_gemm_swiglu_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_grouped_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32,
                                                  _vp]),
@@ -371,6 +373,36 @@ def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace
     return out
 
 
+def _transposed_shapes(what, d, packed, scales, group):
+    """(m, n, k, specs) of d [m, n] . deq(packed [n, k/8])."""
+    _require_tensors(what, d=d, packed=packed, scales=scales)
+    if d.dim() != 2 or packed.dim() != 2 or scales.dim() != 2:
+        raise ValueError(f"{what}: d, packed and scales must be 2-D")
+    m, n = d.shape
+    k = packed.shape[1] * 8
+    if group not in (32, 128) or k % group:
+        raise ValueError(f"{what}: k = {k} must be a multiple of the group size 32 or 128 (got {group})")
+    return m, n, k, [("d", d, "f16", None), ("packed", packed, "u32", (n, k // 8)),
+                     ("scales", scales, "f16", (n, k // group))]
+
+
+def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None):
+    """y [m, k] = d [m, n] . deq(packed, scales): the input gradient of gemm / gemv for d = dy, any m."""
+    m, n, k, specs = _transposed_shapes("gemm_t", d, packed, scales, group)
+    specs = specs + _given_workspace("gemm_t", workspace)
+    if out is not None:
+        specs.append(("out", out, "f16", (m, k)))
+    _check_tensors("gemm_t", specs)
+    with _launch_on("gemm_t", d.device, stream):
+        if out is None:
+            out = _torch().empty((m, k), dtype=d.dtype, device=d.device)
+        if workspace is None:
+            workspace = _ffn_workspace(lib.w4a16_gemm_t_workspace_bytes(m, n, k, group), d.device)
+        _check(lib.w4a16_gemm_t(_ptr(d), _ptr(packed), _ptr(scales), _ptr(out), m, n, k, group,
+                                *_ws_args(workspace), _stream(None)), "w4a16_gemm_t")
+    return out
+
+
 def _bank_shapes(what, packed, scales, k, group):
     _require_tensors(what, packed=packed, scales=scales)
     if packed.dim() != 3 or scales.dim() != 3:
@@ -472,4 +504,4 @@ def moe_combine(y_pairs, pair_row, weights, out=None, stream=None):
 __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "unpack", "gemv", "gemm",
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
-           "grouped_gemm_gather", "moe_combine", "gemm_swiglu"] + list(SIGNATURES)
+           "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t"] + list(SIGNATURES)

@@ -14,6 +14,7 @@ using w4a16::aligned;
 using w4a16::as_status;
 using w4a16::common_dense_checks;
 using w4a16::DeviceInfo;
+using w4a16::kMaxBufferBytes;
 using w4a16::kMaxDim;
 using w4a16::status_of;
 using w4a16::valid_group;
@@ -26,9 +27,52 @@ bool swiglu_skinny(int64_t m, int64_t n2, int64_t k, const DeviceInfo& dev) {
   return m <= kSkinnyRows && w4a16::gemm_skinny_fits((int)(m < 16 ? m : 16), (int)n2, (int)k, dev);
 }
 
+// The checks of the products over n (m rows of d, weights [n, k]): W4A16_OK, an
+// error, or -1 when there is no output.  n may be 0 (an empty sum).
+int transposed_checks(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
+                      int64_t n, int64_t k, int32_t group) {
+  if (!valid_group(group)) return W4A16_ERR_GROUP;
+  if (m < 0 || n < 0 || k < 0 || k % group) return W4A16_ERR_SHAPE;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return W4A16_ERR_SHAPE;
+  if (m == 0 || k == 0) return -1;
+  if (!y) return W4A16_ERR_NULL;
+  if (n > 0 && (!d || !packed || !scales)) return W4A16_ERR_NULL;
+  if (!aligned(y, 16) || (n > 0 && (!aligned(d, 16) || !aligned(packed, 16) || !aligned(scales, 2))))
+    return W4A16_ERR_ALIGN;
+  if (n * (k / 2) >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  const int64_t n8 = (n + 7) / 8 * 8;   // rows of d are padded to 8 elements where n is not a multiple
+  if (2 * m * k >= kMaxBufferBytes || 2 * m * n8 >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  return W4A16_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t w4a16_gemm_t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
+  if (!valid_group(group) || m <= 0 || n <= 0 || k <= 0 || k % group) return 0;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return 0;
+  return w4a16::gemm_t_workspace_bytes((int)m, (int)n, (int)k, dev);
+}
+
+w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
+                          int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                          w4a16_stream_t stream) {
+  const int c = transposed_checks(d, packed, scales, y, m, n, k, group);
+  if (c < 0) return W4A16_OK;
+  if (c != W4A16_OK) return as_status(c);
+  if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (n == 0) return status_of(w4a16::launch_zero_fill(y, (size_t)(m * k), st));
+  const size_t need = w4a16::gemm_t_workspace_bytes((int)m, (int)n, (int)k, dev);
+  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  return status_of(w4a16::launch_gemm_t(d, packed, scales, y, (int)m, (int)n, (int)k, group,
+                                        need ? workspace : nullptr, dev, st));
+}
 
 size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
   if (!valid_group(group) || m <= 0 || n <= 0 || k <= 0 || k % group) return 0;

@@ -56,6 +56,7 @@
 #include "kernels.hpp"
 #include "launch.hpp"
 #include "mfma_operands.hpp"
+#include "tile_gemm.hpp"
 
 namespace w4a16 {
 namespace {
@@ -71,7 +72,6 @@ constexpr int kABytes = BM * BK * 2;        // activation tile: 128 rows of 256 
 constexpr int kBBytes = BN * BK / 2;        // packed weight tile: 256 rows of 64 bytes
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kWinBytes = BN * 16;            // one scale window: 256 rows x 8 groups x 2 bytes
-constexpr int kXCD = 8;
 constexpr size_t kPartialBytes = (size_t)BM * BN * 4;
 constexpr uint32_t kSpinLimit = 1u << 24;   // flag polls before the fix-up gives up
 static_assert(3 * kStageBytes + 2 * kWinBytes + 1024 <= 160 * 1024, "LDS use exceeds 160 KB");
@@ -104,7 +104,6 @@ struct GemmPlan {
 // fp32 partials (measured best at 5 on the 512-row up projection; M = 384,
 // 128 and 4096 unchanged)
 constexpr int kMinSKSteps = W4A16_GEMM_MIN_SK_STEPS;
-constexpr int kGroupM = 4;                  // tile rows per group of the tile order
 
 GemmPlan gemm_plan(int m, int n, int k, const DeviceInfo& dev) {
   GemmPlan p;
@@ -126,32 +125,6 @@ GemmPlan gemm_plan(int m, int n, int k, const DeviceInfo& dev) {
   if (nsk > per_xcd) nsk = per_xcd;
   p.nsk = p.sk_tiles ? (int)nsk : 0;
   return p;
-}
-
-__device__ inline int xcd_begin(int xcd, int count) {
-  const int q = count / kXCD, r = count % kXCD;
-  return xcd * q + (xcd < r ? xcd : r);
-}
-
-// Tile order: groups of kGroupM tile rows; inside a group, column by column.
-__device__ inline void tile_coords(int tau, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int per_group = kGroupM * tiles_n;
-  const int grp = tau / per_group;
-  const int first_m = grp * kGroupM;
-  const int gsize = tiles_m - first_m < kGroupM ? tiles_m - first_m : kGroupM;
-  const int r = tau - grp * per_group;
-  tm = first_m + r % gsize;
-  tn = r / gsize;
-}
-
-#define W4A16_LDS(p) ((__attribute__((address_space(3))) void*)(p))
-
-// Barrier that publishes LDS: this thread's LDS reads and global-to-LDS
-// loads are complete before it, and no LDS access moves across it.
-__device__ inline void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Order of one MFMA sub-step's instructions: each of its 4 MFMAs is

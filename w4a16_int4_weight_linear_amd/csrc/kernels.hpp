@@ -76,6 +76,14 @@ hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const u
                               uint16_t* z, int m, int n_out, int k, int group, void* workspace,
                               const DeviceInfo& dev, hipStream_t stream);
 
+// ---- the product with the weights' other side, tiled (gemm_t.hip) ----
+// y [m, k] = d [m, n] . deq(W), W [n, k].  The workspace needs no initial state (0 bytes: none).
+size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev);
+hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
+                         int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
+// d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row.
+hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
+
 // ---- MoE grouped GEMM (grouped_gemm.hip) ----
 hipError_t launch_grouped_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales,
                                const int32_t* offsets, uint16_t* y, int experts, int rows, int n, int k,

@@ -1,0 +1,149 @@
+// tile_gemm.hpp -- what the tiled kernels share: the LDS barrier, the tile order,
+// and the work split of tiles over persistent workgroups.
+//
+// Work split.  T output tiles, I steps each along the sum, W persistent workgroups
+// (a multiple of the 8 XCDs; workgroup g runs on XCD g % 8):
+// * data-parallel rounds: the first floor(T / W) * W tiles are computed whole, W at a
+//   time; in each round the workgroups of an XCD take consecutive tiles of the tile
+//   order, so they share rows and columns in the XCD's L2;
+// * the leftover tiles are dealt to the XCDs in contiguous ranges, and an XCD's
+//   (tile, step) iterations are split evenly over nsk of its workgroups, which compute
+//   them first and store fp32 partial tiles.  A workgroup's range is no longer than
+//   one tile, so it touches at most two tiles (slots 2 g and 2 g + 1).
+#pragma once
+
+#include <type_traits>
+
+#include "device.hpp"
+#include "kernels.hpp"
+
+namespace w4a16 {
+
+constexpr int kXCD = 8;
+constexpr int kGroupM = 4;                  // tile rows per group of the tile order
+
+#define W4A16_LDS(p) ((__attribute__((address_space(3))) void*)(p))
+
+// Barrier that publishes LDS: this thread's LDS reads and global-to-LDS
+// loads are complete before it, and no LDS access moves across it.
+__device__ inline void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+struct SplitPlan {
+  int tiles_m, tiles_n, iters;              // iters: steps per tile
+  int wgs, rounds, sk_tiles, nsk;           // nsk: stream-K workgroups per XCD
+};
+
+inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, const DeviceInfo& dev) {
+  SplitPlan p;
+  p.tiles_m = tiles_m;
+  p.tiles_n = tiles_n;
+  p.iters = iters;
+  int per_xcd = dev.num_cu / kXCD;
+  if (per_xcd < 1) per_xcd = 1;
+  p.wgs = per_xcd * kXCD;
+  const long long tiles = (long long)tiles_m * tiles_n;
+  p.rounds = (int)(tiles / p.wgs);
+  p.sk_tiles = (int)(tiles - (long long)p.rounds * p.wgs);
+  // stream-K workgroups per XCD, from the busiest XCD's ceil(R / 8) tiles;
+  // at least one per tile, so no range is longer than a tile
+  const int cnt_max = (p.sk_tiles + kXCD - 1) / kXCD;
+  long long nsk = (long long)cnt_max * iters / min_steps;
+  if (nsk < cnt_max) nsk = cnt_max;
+  if (nsk > per_xcd) nsk = per_xcd;
+  p.nsk = p.sk_tiles ? (int)nsk : 0;
+  return p;
+}
+
+__device__ inline int xcd_begin(int xcd, int count) {
+  const int q = count / kXCD, r = count % kXCD;
+  return xcd * q + (xcd < r ? xcd : r);
+}
+
+// Tile order: groups of kGroupM tile rows; inside a group, column by column.
+__device__ inline void tile_coords(int tau, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per_group = kGroupM * tiles_n;
+  const int grp = tau / per_group;
+  const int first_m = grp * kGroupM;
+  const int gsize = tiles_m - first_m < kGroupM ? tiles_m - first_m : kGroupM;
+  const int r = tau - grp * per_group;
+  tm = first_m + r % gsize;
+  tn = r / gsize;
+}
+
+// One work item: steps [a, b) of the tile whose first output row and column are r0 and c0.
+struct TileItem {
+  int a, b, r0, c0;
+};
+
+// Iterations [sk_begin(l), sk_begin(l + 1)) of an XCD with `cnt` leftover tiles belong to its workgroup l.
+__device__ inline long long sk_begin(const SplitPlan& p, int cnt, int l) {
+  return (long long)cnt * p.iters * l / p.nsk;
+}
+
+// The items of workgroup `wg`: its stream-K segments (n_seg of them: 0, 1 or 2), then one whole tile per round.
+struct WorkRange {
+  int wg, xcd, lwg, sk_lo, n_seg, j_first;
+  long long s, e;
+  __device__ inline WorkRange(const SplitPlan& p, int wg_) : wg(wg_) {
+    xcd = wg % kXCD;
+    lwg = wg / kXCD;
+    sk_lo = xcd_begin(xcd, p.sk_tiles);
+    const int cnt = xcd_begin(xcd + 1, p.sk_tiles) - sk_lo;
+    const bool in = lwg < p.nsk && cnt > 0;
+    s = in ? sk_begin(p, cnt, lwg) : 0;
+    e = in ? sk_begin(p, cnt, lwg + 1) : 0;
+    n_seg = e > s ? (int)((e - 1) / p.iters - s / p.iters) + 1 : 0;
+    j_first = (int)(s / p.iters);
+  }
+  __device__ inline TileItem item(const SplitPlan& p, int i, int tile_rows, int tile_cols) const {
+    TileItem it;
+    int tau;
+    if (i < n_seg) {
+      const long long lo = (long long)(j_first + i) * p.iters;
+      it.a = (int)((s > lo ? s : lo) - lo);
+      it.b = (int)((e < lo + p.iters ? e : lo + p.iters) - lo);
+      tau = p.rounds * p.wgs + sk_lo + j_first + i;
+    } else {
+      it.a = 0;
+      it.b = p.iters;
+      tau = (i - n_seg) * p.wgs + xcd * (p.wgs / kXCD) + lwg;
+    }
+    int tm, tn;
+    tile_coords(tau, p.tiles_m, p.tiles_n, tm, tn);
+    it.r0 = tm * tile_rows;
+    it.c0 = tn * tile_cols;
+    return it;
+  }
+};
+
+// The workgroups [first, last] of an XCD that hold parts of leftover tile `tile` (0 .. sk_tiles - 1), in order.
+struct Contributors {
+  int xcd, first, last, cnt;
+  long long lo;
+  __device__ inline Contributors(const SplitPlan& p, int tile) {
+    for (xcd = 0; xcd_begin(xcd + 1, p.sk_tiles) <= tile; ++xcd) {}
+    const int sk_lo = xcd_begin(xcd, p.sk_tiles);
+    cnt = xcd_begin(xcd + 1, p.sk_tiles) - sk_lo;
+    lo = (long long)(tile - sk_lo) * p.iters;
+    // workgroup l holds iteration i iff sk_begin(l) <= i < sk_begin(l + 1)
+    const long long total = (long long)cnt * p.iters;
+    auto owner = [&](long long i) {
+      int l = (int)(i * p.nsk / total);
+      while (l + 1 < p.nsk && sk_begin(p, cnt, l + 1) <= i) ++l;
+      while (l > 0 && sk_begin(p, cnt, l) > i) --l;
+      return l;
+    };
+    first = owner(lo);
+    last = owner(lo + p.iters - 1);
+  }
+  // partial slot of contributor l: its second segment if its range began in the tile before
+  __device__ inline int slot(const SplitPlan& p, int l) const {
+    return 2 * (l * kXCD + xcd) + (sk_begin(p, cnt, l) < lo ? 1 : 0);
+  }
+};
+
+}  // namespace w4a16
