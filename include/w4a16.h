@@ -238,6 +238,45 @@ w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint1
 size_t w4a16_gemm_t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
 
 /*
+ * Backward pass of w4a16_gemm_swiglu.  dy [m, n] is the gradient of its output,
+ * gate_up [m, 2n] the products it kept (g in even, u in odd columns), packed and
+ * scales its weights.  Writes dgate_up [m, 2n], the gradient of the products,
+ *
+ *     dg = dy u sig (1 + g (1 - sig)),  du = dy g sig,  sig = 1 / (1 + e^-g)
+ *
+ * in fp32 with one rounding to fp16, and dx [m, k] = dgate_up . deq(W) (the product
+ * of that fp16 output, as w4a16_gemm_t).  All fp16, 16-byte aligned; gradients that
+ * need more range are scaled by the caller.  n == 0 writes zeros to dx, k == 0 only
+ * dgate_up.  Workspace (w4a16_gemm_swiglu_backward_workspace_bytes) and errors as
+ * w4a16_gemm_t.
+ */
+w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate_up, const uint32_t* packed,
+                                        const uint16_t* scales, uint16_t* dgate_up, uint16_t* dx, int64_t m, int64_t n,
+                                        int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                                        w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_gemm_swiglu_backward needs (n outputs) on the current device. */
+size_t w4a16_gemm_swiglu_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
+ * Gradient of the scales of y = x . deq(W)^T, for d = dy:
+ *
+ *     dscales[n, j] = sum over k in group j of q[n, k] * sum_m d[m, n] x[m, k]
+ *
+ * d [m, n], x [m, k] fp16, packed [n, k/8]; dscales fp32 [n, k/group], 16-byte
+ * aligned.  fp32 sums in a fixed order (results do not depend on timing); the n x k
+ * weight gradient is not stored.  For the gate/up pair, d is dgate_up and n counts
+ * its 2n rows.  m == 0 writes zeros; n == 0 or k == 0 is a no-op.  Workspace
+ * (w4a16_gemm_dscales_workspace_bytes) and errors as w4a16_gemm_t.
+ */
+w4a16_status w4a16_gemm_dscales(const uint16_t* d, const uint16_t* x, const uint32_t* packed, float* dscales, int64_t m,
+                                int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                                w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_gemm_dscales needs on the current device. */
+size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
  * MoE grouped GEMM (the routed-expert layers of the 35B-A3B MoE model on the
  * LLM170 CUDA/W4A16 page, g32).  x [rows, k] holds one row per (token, expert)
  * pair, sorted by expert; rows offsets[e] .. offsets[e+1]-1 belong to expert e

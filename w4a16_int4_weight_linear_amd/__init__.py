@@ -62,6 +62,11 @@ SIGNATURES = {
     "w4a16_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
     "w4a16_gemm_t": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
     "w4a16_gemm_t_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "w4a16_gemm_swiglu_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz,
+                                                  _vp]),
+    "w4a16_gemm_swiglu_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "w4a16_gemm_dscales": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "w4a16_gemm_dscales_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_gemm_swiglu_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_grouped_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32,
                                                  _vp]),
@@ -403,6 +408,57 @@ def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None)
     return out
 
 
+def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgate_up=None, workspace=None,
+                         stream=None):
+    """(dx [m, k], dgate_up [m, 2n]) from dy [m, n] and the products gate_up [m, 2n] that gemm_swiglu kept."""
+    _require_tensors("gemm_swiglu_backward", dy=dy, gate_up=gate_up)
+    m, n2, k, specs = _transposed_shapes("gemm_swiglu_backward", gate_up, packed, scales, group)
+    if n2 % 2:
+        raise ValueError("gemm_swiglu_backward: gate_up must have an even number of columns")
+    specs[0] = ("gate_up", gate_up, "f16", None)
+    specs = specs + [("dy", dy, "f16", (m, n2 // 2))] + _given_workspace("gemm_swiglu_backward", workspace)
+    if out is not None:
+        specs.append(("out", out, "f16", (m, k)))
+    if dgate_up is not None:
+        specs.append(("dgate_up", dgate_up, "f16", (m, n2)))
+    _check_tensors("gemm_swiglu_backward", specs)
+    with _launch_on("gemm_swiglu_backward", dy.device, stream):
+        if out is None:
+            out = _torch().empty((m, k), dtype=dy.dtype, device=dy.device)
+        if dgate_up is None:
+            dgate_up = _torch().empty((m, n2), dtype=dy.dtype, device=dy.device)
+        if workspace is None:
+            workspace = _ffn_workspace(lib.w4a16_gemm_swiglu_backward_workspace_bytes(m, n2 // 2, k, group), dy.device)
+        _check(lib.w4a16_gemm_swiglu_backward(_ptr(dy), _ptr(gate_up), _ptr(packed), _ptr(scales), _ptr(dgate_up),
+                                              _ptr(out), m, n2 // 2, k, group, *_ws_args(workspace), _stream(None)),
+               "w4a16_gemm_swiglu_backward")
+    return out, dgate_up
+
+
+def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None):
+    """Gradient fp32 [n, k/group] of the scales of y = x . deq(W)^T, for d = dy [m, n] and x [m, k]."""
+    _require_tensors("gemm_dscales", d=d, x=x, packed=packed)
+    if d.dim() != 2 or x.dim() != 2 or packed.dim() != 2:
+        raise ValueError("gemm_dscales: d, x and packed must be 2-D")
+    m, n = d.shape
+    k = x.shape[1]
+    if group not in (32, 128) or k % group:
+        raise ValueError(f"gemm_dscales: k = {k} must be a multiple of the group size 32 or 128 (got {group})")
+    specs = [("d", d, "f16", None), ("x", x, "f16", (m, k)), ("packed", packed, "u32", (n, k // 8))]
+    specs = specs + _given_workspace("gemm_dscales", workspace)
+    if out is not None:
+        specs.append(("out", out, "f32", (n, k // group)))
+    _check_tensors("gemm_dscales", specs)
+    with _launch_on("gemm_dscales", d.device, stream):
+        if out is None:
+            out = _torch().empty((n, k // group), dtype=_torch().float32, device=d.device)
+        if workspace is None:
+            workspace = _ffn_workspace(lib.w4a16_gemm_dscales_workspace_bytes(m, n, k, group), d.device)
+        _check(lib.w4a16_gemm_dscales(_ptr(d), _ptr(x), _ptr(packed), _ptr(out), m, n, k, group, *_ws_args(workspace),
+                                      _stream(None)), "w4a16_gemm_dscales")
+    return out
+
+
 def _bank_shapes(what, packed, scales, k, group):
     _require_tensors(what, packed=packed, scales=scales)
     if packed.dim() != 3 or scales.dim() != 3:
@@ -504,4 +560,5 @@ def moe_combine(y_pairs, pair_row, weights, out=None, stream=None):
 __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "unpack", "gemv", "gemm",
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
-           "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t"] + list(SIGNATURES)
+           "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t",
+           "gemm_swiglu_backward", "gemm_dscales"] + list(SIGNATURES)

@@ -120,4 +120,74 @@ w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const 
                                              need ? workspace : nullptr, dev, st));
 }
 
+size_t w4a16_gemm_swiglu_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
+  if (n > kMaxDim / 2) return 0;
+  return w4a16_gemm_t_workspace_bytes(m, n < 0 ? n : 2 * n, k, group);
+}
+
+w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate_up, const uint32_t* packed,
+                                        const uint16_t* scales, uint16_t* dgate_up, uint16_t* dx, int64_t m, int64_t n,
+                                        int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                                        w4a16_stream_t stream) {
+  if (!valid_group(group)) return W4A16_ERR_GROUP;
+  if (n < 0 || n > kMaxDim / 2) return W4A16_ERR_SHAPE;
+  // the product's sizes and buffers, with the pairs' gradient as its left side; k == 0 leaves
+  // the pairs' gradient to write
+  int c = transposed_checks(dgate_up, packed, scales, dx, m, 2 * n, k, group);
+  if (c > 0) return as_status(c);
+  if (m == 0 || (n == 0 && k == 0)) return W4A16_OK;
+  if (n > 0) {
+    if (!dy || !gate_up || !dgate_up) return W4A16_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(gate_up, 16) || !aligned(dgate_up, 16)) return W4A16_ERR_ALIGN;
+    if (m > kMaxDim || 4 * m * n >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  }
+  if (!aligned(workspace, 16)) return W4A16_ERR_ALIGN;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const bool product = n > 0 && k > 0;
+  const size_t need = product ? w4a16::gemm_t_workspace_bytes((int)m, (int)(2 * n), (int)k, dev) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (n > 0) {
+    const hipError_t e = w4a16::launch_swiglu_grad(dy, gate_up, dgate_up, (size_t)(m * n), st);
+    if (e != hipSuccess) return W4A16_ERR_HIP;
+  }
+  if (!product) return k > 0 ? status_of(w4a16::launch_zero_fill(dx, (size_t)(m * k), st)) : W4A16_OK;
+  return status_of(w4a16::launch_gemm_t(dgate_up, packed, scales, dx, (int)m, (int)(2 * n), (int)k, group,
+                                        need ? workspace : nullptr, dev, st));
+}
+
+size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
+  if (!valid_group(group) || m <= 0 || n <= 0 || k <= 0 || k % group) return 0;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return 0;
+  return w4a16::dscales_workspace_bytes((int)m, (int)n, (int)k, group, dev);
+}
+
+w4a16_status w4a16_gemm_dscales(const uint16_t* d, const uint16_t* x, const uint32_t* packed, float* dscales, int64_t m,
+                                int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
+                                w4a16_stream_t stream) {
+  if (!valid_group(group)) return W4A16_ERR_GROUP;
+  if (m < 0 || n < 0 || k < 0 || k % group) return W4A16_ERR_SHAPE;
+  if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return W4A16_ERR_SHAPE;
+  if (n == 0 || k == 0) return W4A16_OK;
+  if (!dscales || (m > 0 && (!d || !x || !packed))) return W4A16_ERR_NULL;
+  if (!aligned(dscales, 16) || !aligned(workspace, 16) ||
+      (m > 0 && (!aligned(d, 16) || !aligned(x, 16) || !aligned(packed, 16))))
+    return W4A16_ERR_ALIGN;
+  const int64_t n8 = (n + 7) / 8 * 8;
+  if (n * (k / 2) >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  if (2 * m * k >= kMaxBufferBytes || 2 * m * n8 >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  DeviceInfo dev;
+  if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (m == 0)   // the empty sum (two 16-bit zeros per value)
+    return status_of(w4a16::launch_zero_fill(reinterpret_cast<uint16_t*>(dscales), (size_t)(2 * n * (k / group)), st));
+  const size_t need = w4a16::dscales_workspace_bytes((int)m, (int)n, (int)k, group, dev);
+  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  return status_of(w4a16::launch_dscales(d, x, packed, dscales, (int)m, (int)n, (int)k, group,
+                                         need ? workspace : nullptr, dev, st));
+}
+
 }  // extern "C"

@@ -84,6 +84,16 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
 // d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row.
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
 
+// ---- gradient of SiLU(g) u (swiglu_grad.hip): count outputs, interleaved pairs ----
+hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, size_t count,
+                              hipStream_t stream);
+
+// ---- gradient of the scales (dscales.hip) ----
+// ds [n, k / group] fp32 from d [m, n] and x [m, k].  The workspace needs no initial state.
+size_t dscales_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev);
+hipError_t launch_dscales(const uint16_t* d, const uint16_t* x, const uint32_t* packed, float* ds, int m, int n, int k,
+                          int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
+
 // ---- MoE grouped GEMM (grouped_gemm.hip) ----
 hipError_t launch_grouped_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales,
                                const int32_t* offsets, uint16_t* y, int experts, int rows, int n, int k,

@@ -1,0 +1,59 @@
+// swiglu_grad.hip -- gradient of h = SiLU(g) u with respect to g and u, elementwise on gfx950.
+//
+// With sig = 1 / (1 + e^-g): dg = dh u sig (1 + g (1 - sig)), du = dh g sig, computed in
+// fp32 and rounded once to fp16 (the gradient is an output, and the fp16 operand of the
+// products that follow).  gate_up and dgate_up interleave the pairs, so output i of the
+// flattened [m, n] owns elements 2 i and 2 i + 1 and rows need no alignment of their own.
+//
+// Bound by memory: 10 bytes per output.  A thread takes eight outputs (one 16-byte load
+// of dh, two of gate_up, two stores).
+#include "device.hpp"
+#include "kernels.hpp"
+#include "launch.hpp"
+
+namespace w4a16 {
+namespace {
+
+__device__ inline f16x2 grad_pair(_Float16 g16, _Float16 u16, _Float16 dh16) {
+  const float g = (float)g16, u = (float)u16, dh = (float)dh16;
+  const float sig = 1.0f / (1.0f + __expf(-g));
+  return f16x2{(_Float16)(dh * u * sig * (1.0f + g * (1.0f - sig))), (_Float16)(dh * g * sig)};
+}
+
+__global__ void __launch_bounds__(256)
+swiglu_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gate_up,
+                   uint16_t* __restrict__ dgate_up, size_t count) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (i + 8 <= count) {
+    const f16x8 d = *reinterpret_cast<const f16x8*>(dh + i);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const f16x8 z = *reinterpret_cast<const f16x8*>(gate_up + 2 * i + 8 * p);
+      f16x8 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f16x2 r = grad_pair(z[2 * e], z[2 * e + 1], d[4 * p + e]);
+        o[2 * e] = r[0];
+        o[2 * e + 1] = r[1];
+      }
+      *reinterpret_cast<f16x8*>(dgate_up + 2 * i + 8 * p) = o;
+    }
+  } else {
+    for (size_t e = i; e < count; ++e) {
+      const f16x2 r = grad_pair(__builtin_bit_cast(_Float16, gate_up[2 * e]),
+                                __builtin_bit_cast(_Float16, gate_up[2 * e + 1]), __builtin_bit_cast(_Float16, dh[e]));
+      dgate_up[2 * e] = __builtin_bit_cast(uint16_t, (_Float16)r[0]);
+      dgate_up[2 * e + 1] = __builtin_bit_cast(uint16_t, (_Float16)r[1]);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, size_t count,
+                              hipStream_t stream) {
+  return launch_kernel(swiglu_grad_kernel, dim3((unsigned)((count + 2047) / 2048)), dim3(256), 0, stream, dh, gate_up,
+                       dgate_up, count);
+}
+
+}  // namespace w4a16
