@@ -203,10 +203,11 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
  * m <= 16 without gate_up runs as w4a16_gemv_swiglu, m <= 32 on the
  * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
- * Workspace rules as for w4a16_gemm (zero-filled once before its first use; calls
- * one after another on one stream may share it, also with w4a16_gemm and the
- * other operators below), its size from w4a16_gemm_swiglu_workspace_bytes.
- * Errors as w4a16_gemm; k == 0 writes zeros.
+ * The workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none) needs no initial
+ * state and calls one after another on one stream may share it, also with the
+ * three operators below (not with w4a16_gemm, whose workspace holds state).  No
+ * call waits for another: calls on several streams may run at once, each with a
+ * workspace of its own.  Errors as w4a16_gemm; k == 0 writes zeros.
  */
 w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                uint16_t* gate_up, int64_t m, int64_t n, int64_t k, int32_t group, void* workspace,
@@ -226,9 +227,8 @@ size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_
  * product (there is no second layout).  Weights enter as fp16(s q), sums are fp32,
  * y is rounded once.  n is any size; n == 0 writes zeros, k == 0 is a no-op.  A
  * column k whose weights are all zero still carries an infinity or NaN of d, as
- * the formula does.  The workspace (w4a16_gemm_t_workspace_bytes; 0: none) needs
- * no initial state, and no call waits for another: calls on several streams may
- * run at once, each with a workspace of its own.  Errors as w4a16_gemm.
+ * the formula does.  Workspace (w4a16_gemm_t_workspace_bytes) as for
+ * w4a16_gemm_swiglu, errors as w4a16_gemm.
  */
 w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
                           int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,

@@ -80,7 +80,7 @@ size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_
   DeviceInfo dev;
   if (w4a16::current_device_info(&dev) != hipSuccess) return 0;
   if (swiglu_skinny(m, 2 * n, k, dev)) return 0;
-  return w4a16::gemm_workspace_bytes(m, 2 * n, k, group, dev);
+  return w4a16::gemm_swiglu_workspace_bytes((int)m, (int)n, (int)k, dev);
 }
 
 w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
@@ -114,7 +114,7 @@ w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const 
     }
     return W4A16_OK;
   }
-  const size_t need = w4a16::gemm_workspace_bytes(m, 2 * n, k, group, dev);
+  const size_t need = w4a16::gemm_swiglu_workspace_bytes((int)m, (int)n, (int)k, dev);
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   return status_of(w4a16::launch_gemm_swiglu(x, packed, scales, y, gate_up, (int)m, (int)n, (int)k, group,
                                              need ? workspace : nullptr, dev, st));

@@ -46,7 +46,10 @@
 //   of an accumulator block.  The epilogue swaps one value per lane pair (even
 //   lanes then hold both halves of one row, odd lanes of the next), applies
 //   SiLU(g) u to the fp32 sums and rounds once; the m x 2n intermediate reaches
-//   memory only if the caller keeps it for a backward pass.
+//   memory only if the caller keeps it for a backward pass.  Its split tiles are
+//   joined by a second, small kernel instead of the in-kernel fix-up: no workgroup
+//   waits for another (calls on several streams cannot hold each other up) and the
+//   workspace holds no state.
 //
 // For integer activations, codes and power-of-two scales every product and
 // partial sum is exact, so such inputs give bit-exact results.
@@ -561,6 +564,15 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
           }
         }
       }
+    } else if constexpr (EPI != kEpiProduct) {
+      // the partial (slot 2 wg + item), for the join kernel
+      uint8_t* slot = reinterpret_cast<uint8_t*>(partials) + (size_t)(2 * wg + item) * kPartialBytes;
+#pragma unroll
+      for (int i = 0; i < kMB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4*>(slot + ((i * 4 + q) * kThreads + tid) * 16) =
+              f32x4{acc[i][0][4 * q], acc[i][0][4 * q + 1], acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]};
     } else {
       // Publish the partial (slot 2 wg + item) for the fix-up: device-scope
       // stores, all complete (s_waitcnt) before the flag is raised.
@@ -583,7 +595,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   }
 
   // ---- fix-up: each contributor of a stream-K tile reduces one slice of it.
-  if (n_seg == 0) return;
+  if (EPI != kEpiProduct || n_seg == 0) return;
   // Wave 0 builds the table of this workgroup's one or two stream-K tiles:
   // lane l describes the XCD's workgroup l (nsk <= 64) and polls its flag.
   __shared__ uint32_t fix_slot[2][64];       // partial slot of each contributor
@@ -641,9 +653,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
     // the contributors' quads are summed in contributor order, 8 loads in flight
     constexpr int kChunks = kMB * kNB * 4 * kThreads;
     const int qs = lwg - c0;
-    // (slices of whole column pairs, so a pair's gate and up are summed by neighbouring lanes)
-    constexpr int kPairMask = EPI == kEpiProduct ? ~0 : ~1;
-    const int ch0 = (kChunks * qs / parts) & kPairMask, ch1 = (kChunks * (qs + 1) / parts) & kPairMask;
+    const int ch0 = kChunks * qs / parts, ch1 = kChunks * (qs + 1) / parts;
     for (int c = ch0 + tid; c < ch1; c += kThreads) {
       auto quad = [&](int l) {
         return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
@@ -668,17 +678,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int m = m0 + i * 32 + 8 * q + 4 * ch + r;
-          if (EPI != kEpiSwiglu && m < M)
-            (EPI == kEpiProduct ? y : z)[(size_t)m * N + n] = failed ? (uint16_t)0x7E00u : float_to_half_bits(v[r]);
-        }
-        if constexpr (EPI != kEpiProduct) {
-          const bool odd = n & 1;
-#pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const float o = swiglu_pair(v[r], v[r + 1], odd);
-            const int m = m0 + i * 32 + 8 * q + 4 * ch + r + (odd ? 1 : 0);
-            if (m < M) y[(size_t)m * (N >> 1) + (n >> 1)] = failed ? (uint16_t)0x7E00u : float_to_half_bits(o);
-          }
+          if (m < M) y[(size_t)m * N + n] = failed ? (uint16_t)0x7E00u : float_to_half_bits(v[r]);
         }
       }
     }
@@ -693,6 +693,38 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
         __hip_atomic_store(counters + xcd * per_xcd + j, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
+  }
+}
+
+// Joins the split tiles of the SwiGLU product: one thread per 16-byte quad (four rows of
+// a column), the parts added in contributor order, gate and up in neighbouring lanes.
+constexpr int kQuads = kMB * kNB * 4 * kThreads;
+__global__ void __launch_bounds__(256)
+swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, uint16_t* __restrict__ z, int M, int N,
+                   SplitPlan plan) {
+  const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
+  const Contributors cs(plan, tile);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
+  f32x4 v = f32x4{};
+  for (int l = cs.first; l <= cs.last; ++l)
+    v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(plan, l) * kPartialBytes);
+  int tm, tn;
+  tile_coords(plan.rounds * plan.wgs + tile, plan.tiles_m, plan.tiles_n, tm, tn);
+  const int t = c % kThreads, bq = c / kThreads, i = bq >> 2, q = bq & 3;
+  const int n = tn * BN + (t >> 6) * kWaveN + (t & 31);
+  const int m0 = tm * BM + 32 * i + 8 * q + 4 * ((t >> 5) & 1);
+  const bool odd = n & 1;
+  const float o[2] = {swiglu_pair(v[0], v[1], odd), swiglu_pair(v[2], v[3], odd)};
+  if (n >= N) return;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int m = m0 + 2 * r + (odd ? 1 : 0);
+    if (m < M) y[(size_t)m * (N >> 1) + (n >> 1)] = float_to_half_bits(o[r]);
+  }
+  if (z) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (m0 + r < M) z[(size_t)(m0 + r) * N + n] = float_to_half_bits(v[r]);
   }
 }
 
@@ -752,7 +784,9 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
   uint32_t* flags = nullptr;
   uint32_t* counters = nullptr;
   uint32_t* status = nullptr;
-  if (workspace) {
+  if (EPI != kEpiProduct) {
+    partials = static_cast<float*>(workspace);
+  } else if (workspace) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     status = reinterpret_cast<uint32_t*>(ws);
     partials = reinterpret_cast<float*>(ws + kWorkspaceHeader);
@@ -765,14 +799,24 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
               : tail       ? gemm_kernel<32, true, false, EPI>
               : salign     ? gemm_kernel<32, false, true, EPI>
                            : gemm_kernel<32, false, false, EPI>;
-  return launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m,
-                       p.tiles_n, p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
+  const hipError_t e =
+      launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m, p.tiles_n,
+                    p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
+  if (EPI == kEpiProduct || e != hipSuccess || p.sk_tiles == 0) return e;
+  const SplitPlan sp = {p.tiles_m, p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
+  return launch_kernel(swiglu_join_kernel, dim3((unsigned)p.sk_tiles * (kQuads / 256)), dim3(256), 0, stream, partials,
+                       y, z, m, n, sp);
 }
 }  // namespace
 
 hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                        int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   return launch_epi<kEpiProduct>(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream);
+}
+
+size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev) {
+  const GemmPlan p = gemm_plan(m, 2 * n_out, k, dev);
+  return p.sk_tiles ? 2 * (size_t)p.wgs * kPartialBytes : 0;
 }
 
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,

@@ -71,7 +71,8 @@ hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t
                        int m, int n, int k, int group, void* workspace, const DeviceInfo& dev,
                        hipStream_t stream);
 // y [m, n_out] = SiLU(gate) * up, packed/scales holding 2 n_out interleaved rows; with z, the
-// products themselves too (fp16 [m, 2 n_out]).  Workspace as launch_gemm for n = 2 n_out.
+// products themselves too (fp16 [m, 2 n_out]).  The workspace needs no initial state.
+size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev);
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                               uint16_t* z, int m, int n_out, int k, int group, void* workspace,
                               const DeviceInfo& dev, hipStream_t stream);
