@@ -31,7 +31,8 @@ def reference(d, q, s, group):
 # a step, k below, at and past a tile, one step and many.
 CASES = [(1, 1, 32, 32), (1, 1000, 1024, 128), (2, 63, 384, 128), (5, 300, 96, 32), (16, 129, 1056, 32),
          (17, 2048, 256, 128), (33, 513, 2080, 32), (64, 72, 4096, 128), (65, 1001, 640, 128), (130, 64, 160, 32),
-         (257, 2003, 2080, 32), (300, 1016, 768, 128), (1000, 4104, 512, 128), (2050, 200, 8448, 128)]
+         (257, 2003, 2080, 32), (300, 1016, 768, 128), (1000, 4104, 512, 128), (2050, 200, 8448, 128), (3, 17408, 5120, 128), (31, 5120, 1760, 32), (50, 2500, 8192, 32),
+         (8, 40, 70016, 128)]
 
 
 @pytest.mark.parametrize("m,n,k,group", CASES)

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -317,145 +318,208 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # The feed-forward block for any number of rows, with its backward pass.
 #
 # These calls run on the tensors' own device whichever is current, allocate on
-# the stream they launch on, and keep one workspace per (device, stream).  Under
-# graph capture each call takes a workspace of its own from the graph's pool (its
-# zero fill is part of the graph), so captured graphs share none.
+# the stream they launch on, and keep one workspace per (device, stream), grown to
+# the largest size asked for.  The workspaces hold no state between calls.  Under
+# graph capture each call takes one from the graph's own pool, so captured graphs
+# share none.  A smallest call is bound by what the host does before it launches,
+# so the checks here walk the arguments once.
 # ---------------------------------------------------------------------------
+def _check_ffn(what, specs):
+    """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""
+    tensor = _torch_preload.Tensor
+    for name, t, dtypes, shape in specs:
+        if not isinstance(t, tensor):
+            raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{what}: {name} has dtype {t.dtype}, expected {dtypes[0]}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    device = specs[0][1].device
+    for name, t, _, _ in specs:
+        if not t.is_cuda:
+            raise ValueError(f"{what}: {name} is on {t.device}; every tensor must be on the HIP device")
+        if t.device != device:
+            raise ValueError(f"{what}: tensors are on different devices {device}, {t.device}")
+    return device
+
+
+def _matrices(what, group, **tensors):
+    """Tensors, 2-D, and a known group size: what reading the shapes needs."""
+    tensor = _torch_preload.Tensor
+    for name, t in tensors.items():
+        if not isinstance(t, tensor):
+            raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
+        if t.dim() != 2:
+            raise ValueError(f"{what}: {name} must be 2-D")
+    if group not in (32, 128):
+        raise ValueError(f"{what}: the group size must be 32 or 128 (got {group}): k must be a multiple of it")
+
+
+def _check_k(what, k, group):
+    if k % group:
+        raise ValueError(f"{what}: k = {k} must be a multiple of the group size {group}")
+
+
+if _torch_preload is not None:
+    _F16 = (_torch_preload.float16,)
+    _F32 = (_torch_preload.float32,)
+    _I32 = (_torch_preload.int32,)
+    _U32 = tuple(d for d in (_torch_preload.int32, getattr(_torch_preload, "uint32", None)) if d is not None)
+
+
+@contextlib.contextmanager
+def _on_stream(stream):
+    with _torch_preload.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+@contextlib.contextmanager
+def _on_device(device):
+    with _torch_preload.cuda.device(device):
+        yield _torch_preload.cuda.current_stream(device).cuda_stream
+
+
 def _launch_on(what, device, stream):
-    torch = _torch()
+    """A context in which `device` and `stream` (None: the device's current one) are current; gives the handle."""
+    cuda = _torch_preload.cuda
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+        return _on_stream(stream)
+    if device.index != cuda.current_device():
+        return _on_device(device)
+    return contextlib.nullcontext(cuda.current_stream(device.index).cuda_stream)
 
 
 _FFN_WORKSPACES = {}
 
 
-def _ffn_workspace(nbytes, device):
-    """A zero-filled workspace (None if none is needed) for a call on the current stream of `device`."""
-    torch = _torch()
+@functools.lru_cache(maxsize=1024)
+def _ffn_workspace_bytes(entry, m, n, k, group, device_index):
+    """The size query of entry point `entry` on the current device, whose index is device_index."""
+    return getattr(lib, entry + "_workspace_bytes")(m, n, k, group)
+
+
+def _ffn_workspace(entry, m, n, k, group, device, handle, given):
+    """(pointer, bytes) of the given workspace, or of one for a call on stream `handle` of the current device."""
+    if given is not None:
+        return given.data_ptr(), given.numel() * 4
+    nbytes = _ffn_workspace_bytes(entry, m, n, k, group, device.index)
     if nbytes == 0:
-        return None
-    words = (nbytes + 15) // 16 * 4
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(words, dtype=torch.int32, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+        return 0, 0
+    if _torch_preload.cuda.is_current_stream_capturing():
+        ws = _torch_preload.empty(nbytes, dtype=_torch_preload.uint8, device=device)
+        return ws.data_ptr(), nbytes     # freed to the graph's pool, whose later work is ordered behind this call
+    key = (device.index, handle)
     ws = _FFN_WORKSPACES.get(key)
-    if ws is None or ws.numel() < words:
-        ws = _FFN_WORKSPACES[key] = torch.zeros(words, dtype=torch.int32, device=device)
-    return ws
-
-
-def _ws_args(ws):
-    return (_ptr(ws), ws.numel() * 4 if ws is not None else 0)
-
-
-def _given_workspace(what, workspace):
-    return [] if workspace is None else [("workspace", workspace, "i32", None)]
+    if ws is None or ws.numel() < nbytes:
+        ws = _FFN_WORKSPACES[key] = _torch_preload.empty(nbytes, dtype=_torch_preload.uint8, device=device)
+    return ws.data_ptr(), ws.numel()
 
 
 def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace=None, stream=None):
     """y [m, n] = SiLU(x . Wg^T) * (x . Wu^T) for any m; packed [2n, k/8] interleaves gate/up rows.
     gate_up (fp16 [m, 2n]), if given, receives the products themselves for gemm_swiglu_backward."""
-    m, n, k, specs = _dense_shapes("gemm_swiglu", x, packed, scales, group, rows_per_out=2)
-    specs = specs + _given_workspace("gemm_swiglu", workspace)
+    what = "gemm_swiglu"
+    _matrices(what, group, x=x, packed=packed, scales=scales)
+    (m, k), n2 = x.shape, packed.shape[0]
+    _check_k(what, k, group)
+    if n2 % 2:
+        raise ValueError(f"{what}: packed must have a multiple of 2 rows")
+    n = n2 // 2
+    specs = [("x", x, _F16, None), ("packed", packed, _U32, (n2, k // 8)), ("scales", scales, _F16, (n2, k // group))]
     if gate_up is not None:
-        specs.append(("gate_up", gate_up, "f16", (m, 2 * n)))
+        specs.append(("gate_up", gate_up, _F16, (m, n2)))
     if out is not None:
-        specs.append(("out", out, "f16", (m, n)))
-    _check_tensors("gemm_swiglu", specs)
-    with _launch_on("gemm_swiglu", x.device, stream):
+        specs.append(("out", out, _F16, (m, n)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+    with _launch_on(what, device, stream) as handle:
         if out is None:
-            out = _torch().empty((m, n), dtype=x.dtype, device=x.device)
-        if workspace is None:
-            workspace = _ffn_workspace(lib.w4a16_gemm_swiglu_workspace_bytes(m, n, k, group), x.device)
-        _check(lib.w4a16_gemm_swiglu(_ptr(x), _ptr(packed), _ptr(scales), _ptr(out), _ptr(gate_up), m, n, k, group,
-                                     *_ws_args(workspace), _stream(None)), "w4a16_gemm_swiglu")
+            out = _torch_preload.empty((m, n), dtype=x.dtype, device=device)
+        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu", m, n, k, group, device, handle,
+                                    workspace)
+        _check(lib.w4a16_gemm_swiglu(x.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(),
+                                     0 if gate_up is None else gate_up.data_ptr(), m, n, k, group, ws, nbytes, handle),
+               "w4a16_gemm_swiglu")
     return out
-
-
-def _transposed_shapes(what, d, packed, scales, group):
-    """(m, n, k, specs) of d [m, n] . deq(packed [n, k/8])."""
-    _require_tensors(what, d=d, packed=packed, scales=scales)
-    if d.dim() != 2 or packed.dim() != 2 or scales.dim() != 2:
-        raise ValueError(f"{what}: d, packed and scales must be 2-D")
-    m, n = d.shape
-    k = packed.shape[1] * 8
-    if group not in (32, 128) or k % group:
-        raise ValueError(f"{what}: k = {k} must be a multiple of the group size 32 or 128 (got {group})")
-    return m, n, k, [("d", d, "f16", None), ("packed", packed, "u32", (n, k // 8)),
-                     ("scales", scales, "f16", (n, k // group))]
 
 
 def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None):
     """y [m, k] = d [m, n] . deq(packed, scales): the input gradient of gemm / gemv for d = dy, any m."""
-    m, n, k, specs = _transposed_shapes("gemm_t", d, packed, scales, group)
-    specs = specs + _given_workspace("gemm_t", workspace)
+    what = "gemm_t"
+    _matrices(what, group, d=d, packed=packed, scales=scales)
+    (m, n), k = d.shape, packed.shape[1] * 8
+    _check_k(what, k, group)
+    specs = [("d", d, _F16, None), ("packed", packed, _U32, (n, k // 8)), ("scales", scales, _F16, (n, k // group))]
     if out is not None:
-        specs.append(("out", out, "f16", (m, k)))
-    _check_tensors("gemm_t", specs)
-    with _launch_on("gemm_t", d.device, stream):
+        specs.append(("out", out, _F16, (m, k)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+    with _launch_on(what, device, stream) as handle:
         if out is None:
-            out = _torch().empty((m, k), dtype=d.dtype, device=d.device)
-        if workspace is None:
-            workspace = _ffn_workspace(lib.w4a16_gemm_t_workspace_bytes(m, n, k, group), d.device)
-        _check(lib.w4a16_gemm_t(_ptr(d), _ptr(packed), _ptr(scales), _ptr(out), m, n, k, group,
-                                *_ws_args(workspace), _stream(None)), "w4a16_gemm_t")
+            out = _torch_preload.empty((m, k), dtype=d.dtype, device=device)
+        ws, nbytes = _ffn_workspace("w4a16_gemm_t", m, n, k, group, device, handle, workspace)
+        _check(lib.w4a16_gemm_t(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(), m, n, k, group,
+                                ws, nbytes, handle), "w4a16_gemm_t")
     return out
 
 
 def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgate_up=None, workspace=None,
                          stream=None):
     """(dx [m, k], dgate_up [m, 2n]) from dy [m, n] and the products gate_up [m, 2n] that gemm_swiglu kept."""
-    _require_tensors("gemm_swiglu_backward", dy=dy, gate_up=gate_up)
-    m, n2, k, specs = _transposed_shapes("gemm_swiglu_backward", gate_up, packed, scales, group)
+    what = "gemm_swiglu_backward"
+    _matrices(what, group, dy=dy, gate_up=gate_up, packed=packed, scales=scales)
+    (m, n2), k = gate_up.shape, packed.shape[1] * 8
+    _check_k(what, k, group)
     if n2 % 2:
-        raise ValueError("gemm_swiglu_backward: gate_up must have an even number of columns")
-    specs[0] = ("gate_up", gate_up, "f16", None)
-    specs = specs + [("dy", dy, "f16", (m, n2 // 2))] + _given_workspace("gemm_swiglu_backward", workspace)
+        raise ValueError(f"{what}: gate_up must have an even number of columns")
+    n = n2 // 2
+    specs = [("gate_up", gate_up, _F16, None), ("dy", dy, _F16, (m, n)), ("packed", packed, _U32, (n2, k // 8)),
+             ("scales", scales, _F16, (n2, k // group))]
     if out is not None:
-        specs.append(("out", out, "f16", (m, k)))
+        specs.append(("out", out, _F16, (m, k)))
     if dgate_up is not None:
-        specs.append(("dgate_up", dgate_up, "f16", (m, n2)))
-    _check_tensors("gemm_swiglu_backward", specs)
-    with _launch_on("gemm_swiglu_backward", dy.device, stream):
+        specs.append(("dgate_up", dgate_up, _F16, (m, n2)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+    with _launch_on(what, device, stream) as handle:
         if out is None:
-            out = _torch().empty((m, k), dtype=dy.dtype, device=dy.device)
+            out = _torch_preload.empty((m, k), dtype=dy.dtype, device=device)
         if dgate_up is None:
-            dgate_up = _torch().empty((m, n2), dtype=dy.dtype, device=dy.device)
-        if workspace is None:
-            workspace = _ffn_workspace(lib.w4a16_gemm_swiglu_backward_workspace_bytes(m, n2 // 2, k, group), dy.device)
-        _check(lib.w4a16_gemm_swiglu_backward(_ptr(dy), _ptr(gate_up), _ptr(packed), _ptr(scales), _ptr(dgate_up),
-                                              _ptr(out), m, n2 // 2, k, group, *_ws_args(workspace), _stream(None)),
-               "w4a16_gemm_swiglu_backward")
+            dgate_up = _torch_preload.empty((m, n2), dtype=dy.dtype, device=device)
+        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu_backward", m, n, k, group, device,
+                                    handle, workspace)
+        _check(lib.w4a16_gemm_swiglu_backward(dy.data_ptr(), gate_up.data_ptr(), packed.data_ptr(), scales.data_ptr(),
+                                              dgate_up.data_ptr(), out.data_ptr(), m, n, k, group, ws, nbytes,
+                                              handle), "w4a16_gemm_swiglu_backward")
     return out, dgate_up
 
 
 def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None):
     """Gradient fp32 [n, k/group] of the scales of y = x . deq(W)^T, for d = dy [m, n] and x [m, k]."""
-    _require_tensors("gemm_dscales", d=d, x=x, packed=packed)
-    if d.dim() != 2 or x.dim() != 2 or packed.dim() != 2:
-        raise ValueError("gemm_dscales: d, x and packed must be 2-D")
-    m, n = d.shape
-    k = x.shape[1]
-    if group not in (32, 128) or k % group:
-        raise ValueError(f"gemm_dscales: k = {k} must be a multiple of the group size 32 or 128 (got {group})")
-    specs = [("d", d, "f16", None), ("x", x, "f16", (m, k)), ("packed", packed, "u32", (n, k // 8))]
-    specs = specs + _given_workspace("gemm_dscales", workspace)
+    what = "gemm_dscales"
+    _matrices(what, group, d=d, x=x, packed=packed)
+    (m, n), k = d.shape, x.shape[1]
+    _check_k(what, k, group)
+    specs = [("d", d, _F16, None), ("x", x, _F16, (m, k)), ("packed", packed, _U32, (n, k // 8))]
     if out is not None:
-        specs.append(("out", out, "f32", (n, k // group)))
-    _check_tensors("gemm_dscales", specs)
-    with _launch_on("gemm_dscales", d.device, stream):
+        specs.append(("out", out, _F32, (n, k // group)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+    with _launch_on(what, device, stream) as handle:
         if out is None:
-            out = _torch().empty((n, k // group), dtype=_torch().float32, device=d.device)
-        if workspace is None:
-            workspace = _ffn_workspace(lib.w4a16_gemm_dscales_workspace_bytes(m, n, k, group), d.device)
-        _check(lib.w4a16_gemm_dscales(_ptr(d), _ptr(x), _ptr(packed), _ptr(out), m, n, k, group, *_ws_args(workspace),
-                                      _stream(None)), "w4a16_gemm_dscales")
+            out = _torch_preload.empty((n, k // group), dtype=_torch_preload.float32, device=device)
+        ws, nbytes = _ffn_workspace("w4a16_gemm_dscales", m, n, k, group, device, handle,
+                                    workspace)
+        _check(lib.w4a16_gemm_dscales(d.data_ptr(), x.data_ptr(), packed.data_ptr(), out.data_ptr(), m, n, k, group,
+                                      ws, nbytes, handle), "w4a16_gemm_dscales")
     return out
 
 

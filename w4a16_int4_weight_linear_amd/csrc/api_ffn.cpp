@@ -27,6 +27,24 @@ bool swiglu_skinny(int64_t m, int64_t n2, int64_t k, const DeviceInfo& dev) {
   return m <= kSkinnyRows && w4a16::gemm_skinny_fits((int)(m < 16 ? m : 16), (int)n2, (int)k, dev);
 }
 
+// The product over n of checked arguments (m, n, k > 0): up to kSkinnyTRows rows on the
+// weight-streaming kernel, beyond on the tiles.
+bool t_skinny(int64_t m, int64_t n, int64_t k, int32_t group, const DeviceInfo& dev) {
+  return m <= w4a16::kSkinnyTRows && w4a16::gemm_t_skinny_fits((int)m, (int)n, (int)k, group, dev);
+}
+
+size_t t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group, const DeviceInfo& dev) {
+  return t_skinny(m, n, k, group, dev)
+             ? w4a16::gemm_t_skinny_workspace_bytes((int)m, (int)n, (int)k, group, dev)
+             : w4a16::gemm_t_workspace_bytes((int)m, (int)n, (int)k, dev);
+}
+
+hipError_t launch_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m, int64_t n,
+                    int64_t k, int32_t group, void* workspace, const DeviceInfo& dev, hipStream_t st) {
+  auto launch = t_skinny(m, n, k, group, dev) ? w4a16::launch_gemm_t_skinny : w4a16::launch_gemm_t;
+  return launch(d, packed, scales, y, (int)m, (int)n, (int)k, group, workspace, dev, st);
+}
+
 // The checks of the products over n (m rows of d, weights [n, k]): W4A16_OK, an
 // error, or -1 when there is no output.  n may be 0 (an empty sum).
 int transposed_checks(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
@@ -54,7 +72,7 @@ size_t w4a16_gemm_t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t gro
   if (m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
   DeviceInfo dev;
   if (w4a16::current_device_info(&dev) != hipSuccess) return 0;
-  return w4a16::gemm_t_workspace_bytes((int)m, (int)n, (int)k, dev);
+  return t_workspace_bytes(m, n, k, group, dev);
 }
 
 w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
@@ -68,10 +86,9 @@ w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint1
   if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (n == 0) return status_of(w4a16::launch_zero_fill(y, (size_t)(m * k), st));
-  const size_t need = w4a16::gemm_t_workspace_bytes((int)m, (int)n, (int)k, dev);
+  const size_t need = t_workspace_bytes(m, n, k, group, dev);
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
-  return status_of(w4a16::launch_gemm_t(d, packed, scales, y, (int)m, (int)n, (int)k, group,
-                                        need ? workspace : nullptr, dev, st));
+  return status_of(launch_t(d, packed, scales, y, m, n, k, group, need ? workspace : nullptr, dev, st));
 }
 
 size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {
@@ -146,15 +163,14 @@ w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate
   if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const bool product = n > 0 && k > 0;
-  const size_t need = product ? w4a16::gemm_t_workspace_bytes((int)m, (int)(2 * n), (int)k, dev) : 0;
+  const size_t need = product ? t_workspace_bytes(m, 2 * n, k, group, dev) : 0;
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   if (n > 0) {
     const hipError_t e = w4a16::launch_swiglu_grad(dy, gate_up, dgate_up, (size_t)(m * n), st);
     if (e != hipSuccess) return W4A16_ERR_HIP;
   }
   if (!product) return k > 0 ? status_of(w4a16::launch_zero_fill(dx, (size_t)(m * k), st)) : W4A16_OK;
-  return status_of(w4a16::launch_gemm_t(dgate_up, packed, scales, dx, (int)m, (int)(2 * n), (int)k, group,
-                                        need ? workspace : nullptr, dev, st));
+  return status_of(launch_t(dgate_up, packed, scales, dx, m, 2 * n, k, group, need ? workspace : nullptr, dev, st));
 }
 
 size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {

@@ -1,0 +1,294 @@
+// gemm_t_skinny.hip -- the product with the other side of the int4 weights for few rows
+// (weight-streaming): y[m, k] = sum_n d[m, n] * s[n, k / g] * q[n, k], m <= 64 per pass.
+//
+// With few rows the product is one pass over the packed weights, bound by HBM (0.53 bytes
+// per 2 m operations).  The packed words run along k, the output side, so every
+// word holds eight output columns of one n:
+//
+// * A workgroup owns a strip of CW columns and a range of n; its eight waves take the
+//   range's units of 32 n in turn, each for the whole strip.  Lane (lq, li) of a unit loads
+//   CW / 128 words of each of the rows 8 lq .. 8 lq + 7: sixteen lanes read CW / 2
+//   contiguous bytes of a row (a whole 128-byte line for 256 columns).
+// * Two words of neighbouring n give their nibble pairs by one byte permute per four
+//   columns; an AND-OR makes fp16 1024 + u or 64 + u of a pair, a packed subtraction the
+//   code and a packed multiplication by the two rows' scales the operand q s (rounded
+//   once, as in the GEMM).  Eight n of a column are exactly a lane's slice of
+//   v_mfma_f32_16x16x32_f16, so a unit is CW / 16 such operands, each used by the MB
+//   blocks of sixteen rows of d.
+// * The rows of d and the scales of the workgroup's range are staged in LDS once (scales
+//   turned to [group][n]).  Rows of d go to MFMA rows (r, lq) -> 4 lq + r, so that up to
+//   four rows of d occupy one accumulator register per column.
+// * The waves' sums are added in wave order in LDS; ranges of n are joined by a second
+//   small kernel in range order (fixed order, no atomics, no state in the workspace).
+#include "device.hpp"
+#include "kernels.hpp"
+#include "launch.hpp"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / 64;
+constexpr int kUnit = 32;                       // n per unit
+
+struct SkinnyPlan {
+  int strips, splits, units, range;             // strips of CW columns, ranges of n, units of 32 n, n per range
+  int xpitch;                                   // bytes of a staged row of d
+  uint32_t lds;
+};
+
+// Eight operand values of column f of a lane's words w[0..7] (eight n), scales sc.
+__device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
+  return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
+}
+
+template <int G, int MB, int CW>
+__global__ void __launch_bounds__(kThreads)
+gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
+                     const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
+                     SkinnyPlan plan, float* __restrict__ partials) {
+  constexpr int kWords = CW / 128;              // words per lane and row (1 or 2)
+  constexpr int kF = CW / 16;                   // operands (columns) per lane and unit
+  constexpr int kGroups = CW / G;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lq = lane >> 4, li = lane & 15;
+
+  const int strip = blockIdx.x % plan.strips, split = blockIdx.x / plan.strips;
+  const int c0 = strip * CW;
+  const int n_lo = split * plan.range;
+  const int n_cnt = min(plan.range, N - n_lo);                 // at least 1
+  const int units = (n_cnt + kUnit - 1) / kUnit;
+
+  const uint32_t wrow = (uint32_t)K >> 1;
+  const int spr = K / G;
+  const __amdgpu_buffer_rsrc_t wres = make_rsrc(packed, (uint32_t)N * wrow);
+
+  // ---- weight stream: unit u's rows n_lo + 32 u + 8 lq + j ----
+  const uint32_t w_v = (uint32_t)(8 * lq) * wrow + (uint32_t)(4 * kWords * li);
+  auto load_unit = [&](int u, uint32_t (&w)[8][kWords]) {
+    const bool live = u < units;                                // wave-uniform; else no memory access
+    const uint32_t off = live ? w_v : kOutOfRange;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t so = live ? (uint32_t)(n_lo + kUnit * u + j) * wrow + (uint32_t)(c0 >> 1) : 0u;
+      if constexpr (kWords == 2) {
+        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wres, off, so, kStream));
+        w[j][0] = v[0];
+        w[j][1] = v[1];
+      } else {
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(wres, off, so, kStream);
+      }
+    }
+  };
+
+  // ---- staging: rows of d (zeros past N; rows past M feed nothing), scales [group][n] ----
+  uint8_t* xs = smem;
+  uint8_t* ss = smem + (size_t)MB * 16 * plan.xpitch;
+  const int rng = units * kUnit;                                // staged n (a multiple of 32)
+  if (N % 8 == 0) {
+    const int pieces = rng / 8;
+    for (int i = tid; i < M * pieces; i += kThreads) {
+      const int r = i / pieces, c = i - r * pieces;
+      const int n = n_lo + 8 * c;
+      u32x4 v = u32x4{};
+      if (n < N) v = *reinterpret_cast<const u32x4*>(d + (size_t)r * N + n);
+      *reinterpret_cast<u32x4*>(xs + r * plan.xpitch + 16 * c) = v;
+    }
+  } else {
+    for (int i = tid; i < M * rng; i += kThreads) {
+      const int r = i / rng, c = i - r * rng;
+      const int n = n_lo + c;
+      *reinterpret_cast<uint16_t*>(xs + r * plan.xpitch + 2 * c) = n < N ? d[(size_t)r * N + n] : (uint16_t)0;
+    }
+  }
+  for (int i = tid; i < rng * kGroups; i += kThreads) {
+    const int n = i / kGroups, g = i % kGroups;
+    const bool ok = n_lo + n < N && c0 / G + g < spr;
+    *reinterpret_cast<uint16_t*>(ss + (g * plan.range + n) * 2) =
+        ok ? scales[(size_t)(n_lo + n) * spr + c0 / G + g] : (uint16_t)0;
+  }
+  __syncthreads();
+
+  f32x4 acc[MB][kF];
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int f = 0; f < kF; ++f) acc[b][f] = f32x4{};
+
+  const uint32_t m_lo = __builtin_amdgcn_readfirstlane(0x000F000Fu), m_hi = __builtin_amdgcn_readfirstlane(0x00F000F0u);
+  uint32_t e_lo = 0x64006400u, e_hi = 0x54005400u;     // fp16 1024 and 64, both halves
+  asm volatile("" : "+v"(e_lo), "+v"(e_hi));
+  const f16x2 b_lo = {(_Float16)-1032.f, (_Float16)-1032.f}, b_hi = {(_Float16)-72.f, (_Float16)-72.f};
+
+  // operand row li of d: row 4 (li % 4) + li / 4 of its block
+  const uint8_t* xrow = xs + ((li & 3) * 4 + (li >> 2)) * plan.xpitch + 16 * lq;
+  const uint8_t* srow = ss + ((kF * li) / G) * plan.range * 2 + 16 * lq;
+
+  auto use_unit = [&](int u, const uint32_t (&w)[8][kWords]) {
+    const f16x8 sc = *reinterpret_cast<const f16x8*>(srow + u * (kUnit * 2));
+    f16x8 xv[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+      xv[b] = *reinterpret_cast<const f16x8*>(xrow + b * 16 * plan.xpitch + u * (kUnit * 2));
+#pragma unroll
+    for (int wd = 0; wd < kWords; ++wd)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t p[4], p8[4];
+#pragma unroll
+        for (int jp = 0; jp < 4; ++jp) {
+          p[jp] = pair_perm(w[2 * jp][wd], w[2 * jp + 1][wd], hh);
+          p8[jp] = p[jp] >> 8;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f16x8 op;
+#pragma unroll
+          for (int jp = 0; jp < 4; ++jp) {
+            const uint32_t src = c < 2 ? p[jp] : p8[jp];
+            const uint32_t t = (c & 1) ? ((src & m_hi) | e_hi) : ((src & m_lo) | e_lo);
+            const f16x2 v = (__builtin_bit_cast(f16x2, t) + ((c & 1) ? b_hi : b_lo)) * f16x2{sc[2 * jp], sc[2 * jp + 1]};
+            op[2 * jp] = v[0];
+            op[2 * jp + 1] = v[1];
+          }
+          const int f = 8 * wd + 4 * hh + c;
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+            acc[b][f] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xv[b], op, acc[b][f], 0, 0, 0);
+        }
+      }
+  };
+
+  // two units in flight per wave
+  uint32_t wa[8][kWords], wb[8][kWords];
+  load_unit(wave, wa);
+  load_unit(wave + kWaves, wb);
+  for (int u = wave; u < units; u += 2 * kWaves) {
+    use_unit(u, wa);
+    load_unit(u + 2 * kWaves, wa);
+    if (u + kWaves < units) {
+      use_unit(u + kWaves, wb);
+      load_unit(u + 3 * kWaves, wb);
+    }
+  }
+
+  // ---- sums over the waves, four rows of d at a time: buffer [wave][lq][CW columns] fp32,
+  // columns kF li + f; 16-byte chunk j of a lane's columns at j ^ (li / 2 % 4) (bank spread).
+  // Accumulator r of lane (lq, li) is row 4 r + lq of its block.
+  float* red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row0 = 16 * b + 4 * r;
+      if (row0 >= M) break;
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kF / 4; ++j) {
+        const f32x4 v = {acc[b][4 * j][r], acc[b][4 * j + 1][r], acc[b][4 * j + 2][r], acc[b][4 * j + 3][r]};
+        *reinterpret_cast<f32x4*>(red + (wave * 4 + lq) * CW + kF * li + 4 * (j ^ ((li >> 1) & (kF / 4 - 1)))) = v;
+      }
+      __syncthreads();
+      for (int o = tid; o < 4 * CW / 2; o += kThreads) {
+        const int q = o / (CW / 2), c = (o % (CW / 2)) * 2;
+        const int l = c / kF, f = c % kF;
+        const float* src = red + q * CW + kF * l + 4 * ((f >> 2) ^ ((l >> 1) & (kF / 4 - 1))) + (f & 3);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(src + w * 4 * CW);
+          s0 += v.x;
+          s1 += v.y;
+        }
+        const int m = row0 + q, k = c0 + c;
+        if (m < M && k < K) {
+          if (plan.splits == 1)
+            *reinterpret_cast<uint32_t*>(y + (size_t)m * K + k) =
+                (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
+          else
+            *reinterpret_cast<float2*>(partials + ((size_t)split * M + m) * K + k) = make_float2(s0, s1);
+        }
+      }
+    }
+}
+
+// y = the ranges' sums [splits][m k] added in order; four outputs per thread.
+__global__ void __launch_bounds__(256)
+gemm_t_skinny_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, int count, int splits) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;          // count is a multiple of 32
+  if (i >= count) return;
+  f32x4 s = f32x4{};
+  for (int p = 0; p < splits; ++p) s += *reinterpret_cast<const f32x4*>(partials + (size_t)p * count + i);
+  u32x2 o;
+  o[0] = (uint32_t)float_to_half_bits(s[0]) | ((uint32_t)float_to_half_bits(s[1]) << 16);
+  o[1] = (uint32_t)float_to_half_bits(s[2]) | ((uint32_t)float_to_half_bits(s[3]) << 16);
+  *reinterpret_cast<u32x2*>(y + i) = o;
+}
+
+constexpr size_t kMaxSums = (size_t)256 << 20;   // bytes of the ranges' sums, at most
+
+int blocks_of(int m) { return m <= 16 ? 1 : (m <= 32 ? 2 : 4); }
+int strip_of(int mb) { return mb == 4 ? 128 : 256; }
+
+SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
+  const int mb = blocks_of(m), cw = strip_of(mb);
+  SkinnyPlan p;
+  p.strips = (k + cw - 1) / cw;
+  p.units = (n + kUnit - 1) / kUnit;
+  // workgroups: one or two per CU
+  const int slots = dev.num_cu * (mb == 1 ? 2 : 1);
+  int splits = slots / p.strips;
+  const int max_range = mb == 1 ? 1024 : (mb == 2 ? 1024 : 768);   // what fits in LDS
+  const int lo = (n + max_range - 1) / max_range;
+  if (splits > (p.units + kWaves - 1) / kWaves) splits = (p.units + kWaves - 1) / kWaves;
+  if (splits < lo) splits = lo;
+  if (splits < 1) splits = 1;
+  p.range = ((p.units + splits - 1) / splits) * kUnit;
+  p.splits = (n + p.range - 1) / p.range;
+  p.xpitch = p.range * 2 + 16;
+  const uint32_t stage = (uint32_t)(mb * 16 * p.xpitch + (cw / group) * p.range * 2);
+  const uint32_t red = (uint32_t)(kWaves * 4 * cw * 4);
+  p.lds = stage > red ? stage : red;
+  return p;
+}
+
+template <int G>
+hipError_t launch_g(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n, int k,
+                    const SkinnyPlan& p, float* partials, hipStream_t stream) {
+  const int mb = blocks_of(m);
+  auto kern = mb == 1 ? gemm_t_skinny_kernel<G, 1, 256>
+                      : (mb == 2 ? gemm_t_skinny_kernel<G, 2, 256> : gemm_t_skinny_kernel<G, 4, 128>);
+  return launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d, packed, scales, y,
+                       m, n, k, p, partials);
+}
+
+}  // namespace
+
+size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
+  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
+  return p.splits > 1 ? (size_t)p.splits * m * k * 4 : 0;
+}
+
+bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
+  if (m > kSkinnyTRows) return false;
+  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
+  // (a range is limited by LDS: a very large product would need many ranges, and their sums room)
+  return p.lds <= dev.max_lds && (p.splits == 1 || (size_t)p.splits * m * k * 4 <= kMaxSums);
+}
+
+hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                                int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
+  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
+  float* partials = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  const hipError_t e = group == 128 ? launch_g<128>(d, packed, scales, y, m, n, k, p, partials, stream)
+                                    : launch_g<32>(d, packed, scales, y, m, n, k, p, partials, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int count = m * k;
+  return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, stream,
+                       partials, y, count, p.splits);
+}
+
+}  // namespace w4a16

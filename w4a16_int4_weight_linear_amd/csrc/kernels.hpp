@@ -85,6 +85,13 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
 // d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row.
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
 
+// ---- the same product for few rows, weight-streaming (gemm_t_skinny.hip) ----
+constexpr int kSkinnyTRows = 64;             // rows per pass
+bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev);
+size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev);
+hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                                int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
+
 // ---- gradient of SiLU(g) u (swiglu_grad.hip): count outputs, interleaved pairs ----
 hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, size_t count,
                               hipStream_t stream);
