@@ -84,19 +84,66 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     }
   };
 
-  // ---- staging: rows of d (zeros past N; rows past M feed nothing), scales [group][n] ----
+  // ---- staging: rows of d (zeros past N; rows past M feed nothing), scales [group][n].
+  // The first loads go out before the first weight loads (loads return in order: waiting for
+  // them then does not wait for the weights), the rest, if any, after them.
   uint8_t* xs = smem;
   uint8_t* ss = smem + (size_t)MB * 16 * plan.xpitch;
   const int rng = units * kUnit;                                // staged n (a multiple of 32)
-  if (N % 8 == 0) {
-    const int pieces = rng / 8;
-    for (int i = tid; i < M * pieces; i += kThreads) {
-      const int r = i / pieces, c = i - r * pieces;
-      const int n = n_lo + 8 * c;
-      u32x4 v = u32x4{};
-      if (n < N) v = *reinterpret_cast<const u32x4*>(d + (size_t)r * N + n);
-      *reinterpret_cast<u32x4*>(xs + r * plan.xpitch + 16 * c) = v;
+  const __amdgpu_buffer_rsrc_t dres = make_rsrc(d, (uint32_t)M * (uint32_t)N * 2u);
+  const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * (uint32_t)spr * 2u);
+  const bool vec = N % 8 == 0;                                  // rows of d 16-byte aligned: 16-byte pieces
+  const int pieces = vec ? rng / 8 : 0, xtotal = M * pieces;
+  auto load_x = [&](int r, int c, bool ok) -> u32x4 {
+    const int n = n_lo + 8 * c;
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                         dres, ok && n < N ? ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u : kOutOfRange, 0, 0));
+  };
+  auto store_x = [&](int r, int c, const u32x4& v) { *reinterpret_cast<u32x4*>(xs + r * plan.xpitch + 16 * c) = v; };
+  auto load_s = [&](int i) -> uint16_t {
+    const int n = n_lo + i / kGroups, g = c0 / G + i % kGroups;
+    const bool ok = i < rng * kGroups && n < N && g < spr;
+    return __builtin_amdgcn_raw_buffer_load_b16(sres, ok ? ((uint32_t)n * (uint32_t)spr + (uint32_t)g) * 2u : kOutOfRange, 0, 0);
+  };
+  auto store_s = [&](int i, uint16_t v) {
+    *reinterpret_cast<uint16_t*>(ss + ((i % kGroups) * plan.range + i / kGroups) * 2) = v;
+  };
+  constexpr int kX0 = MB == 1 ? 4 : 6, kS0 = kGroups == 2 ? 4 : 8;   // loads per thread ahead of the weights
+  const int xstep_r = vec ? kThreads / pieces : 0, xstep_c = vec ? kThreads - xstep_r * pieces : 0;
+  int xr = vec ? tid / pieces : 0, xc = vec ? tid - xr * pieces : 0;
+  u32x4 x0[kX0];
+  uint16_t s0[kS0];
+#pragma unroll
+  for (int j = 0; j < kX0; ++j) {
+    x0[j] = load_x(xr, xc, tid + j * kThreads < xtotal);
+    xr += xstep_r;
+    xc += xstep_c;
+    if (xc >= pieces && vec) {
+      xc -= pieces;
+      ++xr;
     }
+  }
+#pragma unroll
+  for (int j = 0; j < kS0; ++j) s0[j] = load_s(tid + j * kThreads);
+
+  // two units in flight per wave
+  uint32_t wa[8][kWords], wb[8][kWords];
+  load_unit(wave, wa);
+  load_unit(wave + kWaves, wb);
+
+  if (vec) {
+    int r = tid / pieces, c = tid - r * pieces;
+#pragma unroll
+    for (int j = 0; j < kX0; ++j) {
+      if (tid + j * kThreads < xtotal) store_x(r, c, x0[j]);
+      r += xstep_r;
+      c += xstep_c;
+      if (c >= pieces) {
+        c -= pieces;
+        ++r;
+      }
+    }
+    for (int i = tid + kX0 * kThreads; i < xtotal; i += kThreads) store_x(i / pieces, i % pieces, load_x(i / pieces, i % pieces, true));
   } else {
     for (int i = tid; i < M * rng; i += kThreads) {
       const int r = i / rng, c = i - r * rng;
@@ -104,12 +151,10 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
       *reinterpret_cast<uint16_t*>(xs + r * plan.xpitch + 2 * c) = n < N ? d[(size_t)r * N + n] : (uint16_t)0;
     }
   }
-  for (int i = tid; i < rng * kGroups; i += kThreads) {
-    const int n = i / kGroups, g = i % kGroups;
-    const bool ok = n_lo + n < N && c0 / G + g < spr;
-    *reinterpret_cast<uint16_t*>(ss + (g * plan.range + n) * 2) =
-        ok ? scales[(size_t)(n_lo + n) * spr + c0 / G + g] : (uint16_t)0;
-  }
+#pragma unroll
+  for (int j = 0; j < kS0; ++j)
+    if (tid + j * kThreads < rng * kGroups) store_s(tid + j * kThreads, s0[j]);
+  for (int i = tid + kS0 * kThreads; i < rng * kGroups; i += kThreads) store_s(i, load_s(i));
   __syncthreads();
 
   f32x4 acc[MB][kF];
@@ -162,10 +207,6 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
       }
   };
 
-  // two units in flight per wave
-  uint32_t wa[8][kWords], wb[8][kWords];
-  load_unit(wave, wa);
-  load_unit(wave + kWaves, wb);
   for (int u = wave; u < units; u += 2 * kWaves) {
     use_unit(u, wa);
     load_unit(u + 2 * kWaves, wa);
@@ -215,17 +256,26 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     }
 }
 
-// y = the ranges' sums [splits][m k] added in order; four outputs per thread.
-__global__ void __launch_bounds__(256)
+// y = the ranges' sums [splits][m k] added in order: two outputs per thread, sixteen loads in flight.
+__global__ void __launch_bounds__(64)
 gemm_t_skinny_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, int count, int splits) {
-  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;          // count is a multiple of 32
+  const int i = (blockIdx.x * 64 + threadIdx.x) * 2;           // count is a multiple of 32
   if (i >= count) return;
-  f32x4 s = f32x4{};
-  for (int p = 0; p < splits; ++p) s += *reinterpret_cast<const f32x4*>(partials + (size_t)p * count + i);
-  u32x2 o;
-  o[0] = (uint32_t)float_to_half_bits(s[0]) | ((uint32_t)float_to_half_bits(s[1]) << 16);
-  o[1] = (uint32_t)float_to_half_bits(s[2]) | ((uint32_t)float_to_half_bits(s[3]) << 16);
-  *reinterpret_cast<u32x2*>(y + i) = o;
+  float s0 = 0.f, s1 = 0.f;
+  for (int p0 = 0; p0 < splits; p0 += 16) {
+    float2 v[16];
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+      const int q = p0 + p < splits ? p0 + p : p0;
+      v[p] = *reinterpret_cast<const float2*>(partials + (size_t)q * count + i);
+    }
+#pragma unroll
+    for (int p = 0; p < 16; ++p) {
+      s0 += p0 + p < splits ? v[p].x : 0.f;
+      s1 += p0 + p < splits ? v[p].y : 0.f;
+    }
+  }
+  *reinterpret_cast<uint32_t*>(y + i) = (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
 }
 
 constexpr size_t kMaxSums = (size_t)256 << 20;   // bytes of the ranges' sums, at most
@@ -287,7 +337,7 @@ hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const
                                     : launch_g<32>(d, packed, scales, y, m, n, k, p, partials, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   const int count = m * k;
-  return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 4 + 255) / 256)), dim3(256), 0, stream,
+  return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 2 + 63) / 64)), dim3(64), 0, stream,
                        partials, y, count, p.splits);
 }
 
