@@ -13,7 +13,6 @@ there is no fallback path of any kind.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -369,28 +368,24 @@ if _torch_preload is not None:
     _U32 = tuple(d for d in (_torch_preload.int32, getattr(_torch_preload, "uint32", None)) if d is not None)
 
 
-@contextlib.contextmanager
-def _on_stream(stream):
-    with _torch_preload.cuda.stream(stream):
-        yield stream.cuda_stream
-
-
-@contextlib.contextmanager
-def _on_device(device):
-    with _torch_preload.cuda.device(device):
-        yield _torch_preload.cuda.current_stream(device).cuda_stream
-
-
-def _launch_on(what, device, stream):
-    """A context in which `device` and `stream` (None: the device's current one) are current; gives the handle."""
+def _launch_on(what, device, stream, call):
+    """call(handle) with `device` and `stream` (None: the device's current one) current."""
     cuda = _torch_preload.cuda
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
-        return _on_stream(stream)
-    if device.index != cuda.current_device():
-        return _on_device(device)
-    return contextlib.nullcontext(cuda.current_stream(device.index).cuda_stream)
+    if stream is None:
+        if device.index == cuda.current_device():
+            return call(_current_handle(device.index))
+        with cuda.device(device):
+            return call(_current_handle(device.index))
+    if stream.device != device:
+        raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+    with cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _current_handle(index):
+    """Handle of a device's current stream (torch's raw getter, where it has one, builds no Stream object)."""
+    raw = getattr(_torch_preload._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else _torch_preload.cuda.current_stream(index).cuda_stream
 
 
 _FFN_WORKSPACES = {}
@@ -437,14 +432,17 @@ def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace
     if workspace is not None:
         specs.append(("workspace", workspace, _I32, None))
     device = _check_ffn(what, specs)
-    with _launch_on(what, device, stream) as handle:
+
+    def call(handle):
+        nonlocal out
         if out is None:
             out = _torch_preload.empty((m, n), dtype=x.dtype, device=device)
-        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu", m, n, k, group, device, handle,
-                                    workspace)
+        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu", m, n, k, group, device, handle, workspace)
         _check(lib.w4a16_gemm_swiglu(x.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(),
                                      0 if gate_up is None else gate_up.data_ptr(), m, n, k, group, ws, nbytes, handle),
                "w4a16_gemm_swiglu")
+
+    _launch_on(what, device, stream, call)
     return out
 
 
@@ -460,12 +458,16 @@ def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None)
     if workspace is not None:
         specs.append(("workspace", workspace, _I32, None))
     device = _check_ffn(what, specs)
-    with _launch_on(what, device, stream) as handle:
+
+    def call(handle):
+        nonlocal out
         if out is None:
             out = _torch_preload.empty((m, k), dtype=d.dtype, device=device)
         ws, nbytes = _ffn_workspace("w4a16_gemm_t", m, n, k, group, device, handle, workspace)
         _check(lib.w4a16_gemm_t(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(), m, n, k, group,
                                 ws, nbytes, handle), "w4a16_gemm_t")
+
+    _launch_on(what, device, stream, call)
     return out
 
 
@@ -488,7 +490,9 @@ def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgat
     if workspace is not None:
         specs.append(("workspace", workspace, _I32, None))
     device = _check_ffn(what, specs)
-    with _launch_on(what, device, stream) as handle:
+
+    def call(handle):
+        nonlocal out, dgate_up
         if out is None:
             out = _torch_preload.empty((m, k), dtype=dy.dtype, device=device)
         if dgate_up is None:
@@ -498,6 +502,8 @@ def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgat
         _check(lib.w4a16_gemm_swiglu_backward(dy.data_ptr(), gate_up.data_ptr(), packed.data_ptr(), scales.data_ptr(),
                                               dgate_up.data_ptr(), out.data_ptr(), m, n, k, group, ws, nbytes,
                                               handle), "w4a16_gemm_swiglu_backward")
+
+    _launch_on(what, device, stream, call)
     return out, dgate_up
 
 
@@ -513,13 +519,17 @@ def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None
     if workspace is not None:
         specs.append(("workspace", workspace, _I32, None))
     device = _check_ffn(what, specs)
-    with _launch_on(what, device, stream) as handle:
+
+    def call(handle):
+        nonlocal out
         if out is None:
             out = _torch_preload.empty((n, k // group), dtype=_torch_preload.float32, device=device)
         ws, nbytes = _ffn_workspace("w4a16_gemm_dscales", m, n, k, group, device, handle,
                                     workspace)
         _check(lib.w4a16_gemm_dscales(d.data_ptr(), x.data_ptr(), packed.data_ptr(), out.data_ptr(), m, n, k, group,
                                       ws, nbytes, handle), "w4a16_gemm_dscales")
+
+    _launch_on(what, device, stream, call)
     return out
 
 

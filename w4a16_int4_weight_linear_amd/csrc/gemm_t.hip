@@ -223,6 +223,33 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
   for (int item = 0; item < n_items; ++item) {
     const bool dp = item >= wr.n_seg;
     const int nsteps = cur.b - cur.a;
+    // 32-row blocks of this wave with rows below M.  A wave without any (the second half of a
+    // last tile) only loads its share: its SIMD's other wave has the matrix core to itself.
+    const int live = min(kMB, (M - cur.r0 - 128 * wm + 31) >> 5);
+    if (live <= 0) {
+      store_scale(0, sreg[0]);
+      store_scale(1, sreg[1]);
+      lds_barrier();
+      auto idle_step = [&](int st, int r) {
+        store_scale(st, sreg[2]);
+        sreg[2] = load_scale(cur, clamp_of(cur, r + 3));
+        for (int p = 0; p < 5; ++p) load_part(cur, clamp_of(cur, r + 2), st, p);
+        lds_barrier();
+      };
+      for (int r = 0;;) {
+        idle_step(2, r);
+        if (++r == nsteps) break;
+        idle_step(0, r);
+        if (++r == nsteps) break;
+        idle_step(1, r);
+        if (++r == nsteps) break;
+      }
+      if (item + 1 < n_items) {
+        cur = wr.item(plan, item + 1, BM, BC);
+        prologue_loads(cur);
+      }
+      continue;
+    }
 
     f32x16 acc[kMB][kNB];
 #pragma unroll
@@ -319,7 +346,8 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
       // ((4 blk + q) 512 + t) 16, so every store covers 1 KB contiguously
       uint8_t* slot = reinterpret_cast<uint8_t*>(partials) + (size_t)(2 * blockIdx.x + item) * kPartialBytes;
 #pragma unroll
-      for (int i = 0; i < kMB; ++i)
+      for (int i = 0; i < kMB; ++i) {
+        if (i >= live) break;
 #pragma unroll
         for (int nb = 0; nb < kNB; ++nb)
 #pragma unroll
@@ -327,6 +355,7 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
             const f32x4 v = {acc[i][nb][4 * q], acc[i][nb][4 * q + 1], acc[i][nb][4 * q + 2], acc[i][nb][4 * q + 3]};
             *reinterpret_cast<f32x4*>(slot + (size_t)(((i * kNB + nb) * 4 + q) * kThreads + tid) * 16) = v;
           }
+      }
     }
   }
 }
@@ -337,22 +366,28 @@ constexpr int kQuads = kMB * kNB * 4 * kThreads;
 __global__ void __launch_bounds__(256)
 gemm_t_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, int M, int K, SplitPlan plan) {
   const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
-  const Contributors cs(plan, tile);
-  const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
-  f32x4 v = f32x4{};
-  for (int l = cs.first; l <= cs.last; ++l)
-    v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(plan, l) * kPartialBytes);
   int tm, tn;
   tile_coords(plan.rounds * plan.wgs + tile, plan.tiles_m, plan.tiles_n, tm, tn);
   const int t = c % kThreads, bq = c / kThreads, blk = bq >> 2, q = bq & 3;
   const int wave = t >> 6, h = (t >> 5) & 1, li = t & 31;
   const int k = tn * BC + 64 * (wave & 3) + 32 * (blk % kNB) + li;
   const int m0 = tm * BM + 128 * (wave >> 2) + 32 * (blk / kNB) + 8 * q + 4 * h;
-  if (k < K) {
+  if (k >= K || m0 >= M) return;
+  const Contributors cs(plan, tile);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
+  f32x4 v = f32x4{};
+  for (int l = cs.first; l <= cs.last; l += 4) {       // four loads in flight
+    f32x4 p[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (m0 + r < M) y[(size_t)(m0 + r) * K + k] = float_to_half_bits(v[r]);
+    for (int u = 0; u < 4; ++u)
+      p[u] = *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(plan, min(l + u, cs.last)) * kPartialBytes);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (l + u <= cs.last) v += p[u];
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (m0 + r < M) y[(size_t)(m0 + r) * K + k] = float_to_half_bits(v[r]);
 }
 
 // d [m, n] copied with the row pitch padded to 8 elements (zeros), for an n that is no multiple of 8.

@@ -1,19 +1,19 @@
 // gemm_t_skinny.hip -- the product with the other side of the int4 weights for few rows
-// (weight-streaming): y[m, k] = sum_n d[m, n] * s[n, k / g] * q[n, k], m <= 64 per pass.
+// (weight-streaming): y[m, k] = sum_n d[m, n] * s[n, k / g] * q[n, k], m <= 32.
 //
 // With few rows the product is one pass over the packed weights, bound by HBM (0.53 bytes
 // per 2 m operations).  The packed words run along k, the output side, so every
 // word holds eight output columns of one n:
 //
-// * A workgroup owns a strip of CW columns and a range of n; its eight waves take the
+// * A workgroup owns a strip of 256 columns and a range of n; its eight waves take the
 //   range's units of 32 n in turn, each for the whole strip.  Lane (lq, li) of a unit loads
-//   CW / 128 words of each of the rows 8 lq .. 8 lq + 7: sixteen lanes read CW / 2
-//   contiguous bytes of a row (a whole 128-byte line for 256 columns).
+//   two words of each of the rows 8 lq .. 8 lq + 7: sixteen lanes read 128 contiguous
+//   bytes of a row, a whole line.
 // * Two words of neighbouring n give their nibble pairs by one byte permute per four
 //   columns; an AND-OR makes fp16 1024 + u or 64 + u of a pair, a packed subtraction the
 //   code and a packed multiplication by the two rows' scales the operand q s (rounded
 //   once, as in the GEMM).  Eight n of a column are exactly a lane's slice of
-//   v_mfma_f32_16x16x32_f16, so a unit is CW / 16 such operands, each used by the MB
+//   v_mfma_f32_16x16x32_f16, so a unit is 16 such operands, each used by the one or two
 //   blocks of sixteen rows of d.
 // * The rows of d and the scales of the workgroup's range are staged in LDS once (scales
 //   turned to [group][n]).  Rows of d go to MFMA rows (r, lq) -> 4 lq + r, so that up to
@@ -30,6 +30,9 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kUnit = 32;                       // n per unit
+constexpr int CW = 256;                         // columns per strip
+constexpr int kWords = CW / 128;                // words per lane and row
+constexpr int kF = CW / 16;                     // operands (columns) per lane and unit
 
 struct SkinnyPlan {
   int strips, splits, units, range;             // strips of CW columns, ranges of n, units of 32 n, n per range
@@ -37,18 +40,24 @@ struct SkinnyPlan {
   uint32_t lds;
 };
 
-// Eight operand values of column f of a lane's words w[0..7] (eight n), scales sc.
+// Rows of d summed over the waves at a time: 64 KB for one block (two workgroups share a
+// CU's LDS), 128 KB for two.
+__host__ __device__ constexpr int red_rows(int mb) { return mb == 1 ? 8 : 16; }
+// floats of one wave's sums in that buffer (whole quads of rows)
+__host__ __device__ constexpr int red_stride(int m, int mb) {
+  return (m < red_rows(mb) ? (m + 3) / 4 * 4 : red_rows(mb)) * CW;
+}
+
+// The same four columns of two neighbouring n.
 __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
   return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
 }
 
-template <int G, int MB, int CW>
+template <int G, int MB>
 __global__ void __launch_bounds__(kThreads)
 gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
                      const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
                      SkinnyPlan plan, float* __restrict__ partials) {
-  constexpr int kWords = CW / 128;              // words per lane and row (1 or 2)
-  constexpr int kF = CW / 16;                   // operands (columns) per lane and unit
   constexpr int kGroups = CW / G;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x;
@@ -74,13 +83,9 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t so = live ? (uint32_t)(n_lo + kUnit * u + j) * wrow + (uint32_t)(c0 >> 1) : 0u;
-      if constexpr (kWords == 2) {
-        const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wres, off, so, kStream));
-        w[j][0] = v[0];
-        w[j][1] = v[1];
-      } else {
-        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(wres, off, so, kStream);
-      }
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wres, off, so, kStream));
+      w[j][0] = v[0];
+      w[j][1] = v[1];
     }
   };
 
@@ -216,31 +221,40 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     }
   }
 
-  // ---- sums over the waves, four rows of d at a time: buffer [wave][lq][CW columns] fp32,
-  // columns kF li + f; 16-byte chunk j of a lane's columns at j ^ (li / 2 % 4) (bank spread).
-  // Accumulator r of lane (lq, li) is row 4 r + lq of its block.
+  // ---- sums over the waves, 4 kR rows of d at a time: buffer [wave][4 kR rows][256 columns]
+  // fp32, columns 16 li + f; 16-byte chunk j of a lane's columns at j ^ (li / 2 % 4) (bank
+  // spread).  Accumulator r of lane (lq, li) is row 4 r + lq of its block.
   float* red = reinterpret_cast<float*>(smem);
+  constexpr int kR = red_rows(MB) / 4;
+  const int wstride = red_stride(M, MB);
 #pragma unroll
   for (int b = 0; b < MB; ++b)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row0 = 16 * b + 4 * r;
+    for (int r0 = 0; r0 < 4; r0 += kR) {
+      const int row0 = 16 * b + 4 * r0;
       if (row0 >= M) break;
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kF / 4; ++j) {
-        const f32x4 v = {acc[b][4 * j][r], acc[b][4 * j + 1][r], acc[b][4 * j + 2][r], acc[b][4 * j + 3][r]};
-        *reinterpret_cast<f32x4*>(red + (wave * 4 + lq) * CW + kF * li + 4 * (j ^ ((li >> 1) & (kF / 4 - 1)))) = v;
+      for (int r = 0; r < kR; ++r) {
+        if (row0 + 4 * r >= M) break;
+#pragma unroll
+        for (int j = 0; j < kF / 4; ++j) {
+          const f32x4 v = {acc[b][4 * j][r0 + r], acc[b][4 * j + 1][r0 + r], acc[b][4 * j + 2][r0 + r],
+                           acc[b][4 * j + 3][r0 + r]};
+          *reinterpret_cast<f32x4*>(red + wave * wstride + (4 * r + lq) * CW + kF * li + 4 * (j ^ ((li >> 1) & 3))) = v;
+        }
       }
       __syncthreads();
-      for (int o = tid; o < 4 * CW / 2; o += kThreads) {
+#pragma unroll
+      for (int o = tid; o < 4 * kR * CW / 2; o += kThreads) {
         const int q = o / (CW / 2), c = (o % (CW / 2)) * 2;
+        if (row0 + q >= M) break;
         const int l = c / kF, f = c % kF;
-        const float* src = red + q * CW + kF * l + 4 * ((f >> 2) ^ ((l >> 1) & (kF / 4 - 1))) + (f & 3);
+        const float* src = red + q * CW + kF * l + 4 * ((f >> 2) ^ ((l >> 1) & 3)) + (f & 3);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(src + w * 4 * CW);
+          const float2 v = *reinterpret_cast<const float2*>(src + w * wstride);
           s0 += v.x;
           s1 += v.y;
         }
@@ -280,27 +294,26 @@ gemm_t_skinny_join_kernel(const float* __restrict__ partials, uint16_t* __restri
 
 constexpr size_t kMaxSums = (size_t)256 << 20;   // bytes of the ranges' sums, at most
 
-int blocks_of(int m) { return m <= 16 ? 1 : (m <= 32 ? 2 : 4); }
-int strip_of(int mb) { return mb == 4 ? 128 : 256; }
+int blocks_of(int m) { return m <= 16 ? 1 : 2; }
 
 SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
-  const int mb = blocks_of(m), cw = strip_of(mb);
+  const int mb = blocks_of(m);
   SkinnyPlan p;
-  p.strips = (k + cw - 1) / cw;
+  p.strips = (k + CW - 1) / CW;
   p.units = (n + kUnit - 1) / kUnit;
   // workgroups: one or two per CU
   const int slots = dev.num_cu * (mb == 1 ? 2 : 1);
   int splits = slots / p.strips;
-  const int max_range = mb == 1 ? 1024 : (mb == 2 ? 1024 : 768);   // what fits in LDS
-  const int lo = (n + max_range - 1) / max_range;
+  constexpr int kMaxRange = 1024;             // what fits in LDS
+  const int lo = (n + kMaxRange - 1) / kMaxRange;
   if (splits > (p.units + kWaves - 1) / kWaves) splits = (p.units + kWaves - 1) / kWaves;
   if (splits < lo) splits = lo;
   if (splits < 1) splits = 1;
   p.range = ((p.units + splits - 1) / splits) * kUnit;
   p.splits = (n + p.range - 1) / p.range;
   p.xpitch = p.range * 2 + 16;
-  const uint32_t stage = (uint32_t)(mb * 16 * p.xpitch + (cw / group) * p.range * 2);
-  const uint32_t red = (uint32_t)(kWaves * 4 * cw * 4);
+  const uint32_t stage = (uint32_t)(mb * 16 * p.xpitch + (CW / group) * p.range * 2);
+  const uint32_t red = (uint32_t)(kWaves * red_stride(m, mb) * 4);
   p.lds = stage > red ? stage : red;
   return p;
 }
@@ -309,8 +322,7 @@ template <int G>
 hipError_t launch_g(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n, int k,
                     const SkinnyPlan& p, float* partials, hipStream_t stream) {
   const int mb = blocks_of(m);
-  auto kern = mb == 1 ? gemm_t_skinny_kernel<G, 1, 256>
-                      : (mb == 2 ? gemm_t_skinny_kernel<G, 2, 256> : gemm_t_skinny_kernel<G, 4, 128>);
+  auto kern = mb == 1 ? gemm_t_skinny_kernel<G, 1> : gemm_t_skinny_kernel<G, 2>;
   return launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d, packed, scales, y,
                        m, n, k, p, partials);
 }

@@ -86,7 +86,7 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
 
 // ---- the same product for few rows, weight-streaming (gemm_t_skinny.hip) ----
-constexpr int kSkinnyTRows = 64;             // rows per pass
+constexpr int kSkinnyTRows = 32;
 bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev);
 size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev);
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,

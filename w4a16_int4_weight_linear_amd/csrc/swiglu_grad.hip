@@ -25,10 +25,14 @@ swiglu_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__
                    uint16_t* __restrict__ dgate_up, size_t count) {
   const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (i + 8 <= count) {
-    const f16x8 d = *reinterpret_cast<const f16x8*>(dh + i);
+    // (both inputs are read once: non-temporal)
+    const f16x8 d = __builtin_nontemporal_load(reinterpret_cast<const f16x8*>(dh + i));
+    f16x8 zv[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) zv[p] = __builtin_nontemporal_load(reinterpret_cast<const f16x8*>(gate_up + 2 * i + 8 * p));
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const f16x8 z = *reinterpret_cast<const f16x8*>(gate_up + 2 * i + 8 * p);
+      const f16x8 z = zv[p];
       f16x8 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
