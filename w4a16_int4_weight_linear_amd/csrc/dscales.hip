@@ -36,15 +36,27 @@ constexpr int kMB = 4, kNB = 2;                  // 32 x 32 blocks per wave
 constexpr int kTileBytes = BR * 512;             // one operand's tile of a step
 constexpr int kStage = 2 * kTileBytes;
 constexpr int kMinSKSteps = 4;                   // steps per split segment, at least
+constexpr int kStepLoads = 4;                    // vector loads of a wave per step
 
 __device__ inline void schedule_substep() {
 #pragma unroll
   for (int i = 0; i < kMB * kNB; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // MFMA
     __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);             // LDS reads
-    if (i < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // global load
+    if (i < kStepLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // global load
     __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);             // VALU
   }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Barrier inside a step: every LDS access of this wave is complete, and of its vector memory
+// accesses all but (at most) the newest kStepLoads, one step's loads.
+__device__ inline void step_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(kStepLoads | (7 << 4));       // vmcnt(kStepLoads) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
@@ -105,11 +117,14 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
   const WorkRange wr(plan, blockIdx.x);
   const int n_items = wr.n_seg + plan.rounds;
 
-  // Part p of step kt into stage st: d (p = 0, 1), x (p = 2, 3).  Rows past M go outside the
-  // buffers (zeros); chunks past a row's end only feed outputs that are not stored.
-  auto load_part = [&](const TileItem& it, int kt, int st, int p) {
+  // Part p of step r of an item into stage st: d (p = 0, 1), x (p = 2, 3).  Rows past M, and
+  // steps past the item's last, go outside the buffers (no memory access, zeros); chunks past
+  // a row's end only feed outputs that are not stored.
+  auto load_part = [&](const TileItem& it, int r, int st, int p) {
     const int row = l_row + 16 * (p & 1);
-    const bool ok = kt * BR + row < M;
+    const bool in = r < it.b - it.a;
+    const int kt = in ? it.a + r : it.a;
+    const bool ok = in && kt * BR + row < M;
     uint8_t* dst = stage(st) + (p < 2 ? 0 : kTileBytes) + (2 * wave + 16 * (p & 1)) * 512;
     if (p < 2)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(dres, W4A16_LDS(dst), 16,
@@ -120,9 +135,9 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
                                                ok ? (uint32_t)row * xpitch + (uint32_t)l_chunk * 16u : kOutOfRange,
                                                (uint32_t)kt * BR * xpitch + (uint32_t)it.c0 * 2u, 0, 0);
   };
-  auto load_stage = [&](const TileItem& it, int kt, int st) {
+  auto load_step = [&](const TileItem& it, int r, int st) {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) load_part(it, kt, st, p);
+    for (int p = 0; p < 4; ++p) load_part(it, r, st, p);
   };
   auto load_codes = [&](const TileItem& it) {
 #pragma unroll
@@ -133,7 +148,6 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
           n < N ? (uint32_t)n * wrow + (uint32_t)(it.c0 >> 1) + (uint32_t)c_chunk * 16u : kOutOfRange, 0, 0, 0);
     }
   };
-  auto clamp_of = [&](const TileItem& it, int r) { return it.a + (r < it.b - it.a ? r : it.b - it.a - 1); };
 
   typedef short i16x4 __attribute__((ext_vector_type(4)));
   typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -153,8 +167,7 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
   TileItem cur{};
   if (n_items > 0) {
     cur = wr.item(plan, 0, BN, BC);
-    load_stage(cur, clamp_of(cur, 0), 0);
-    load_stage(cur, clamp_of(cur, 1), 1);
+    for (int r = 0; r < 3; ++r) load_step(cur, r, r);
   }
   for (int item = 0; item < n_items; ++item) {
     const bool dp = item >= wr.n_seg;
@@ -166,18 +179,24 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
       for (int nb = 0; nb < kNB; ++nb) acc[i][nb] = f32x16{};
     f16x8 aop[2][kMB], bop[2][kNB];
     lds_barrier();
-    load_codes(cur);             // read after the loop's barriers
+    load_codes(cur);
     read_ops(0, 0, aop[0], bop[0]);
 
+    // One step r (stage r % 3 == U).  Its second sub-step's operands are read in the first; the
+    // barrier between them frees the stage, which takes the loads of step r + 3, and publishes
+    // step r + 1, whose loads were issued two steps ago.
     auto step = [&](auto u_tag, int r) {
       constexpr int U = decltype(u_tag)::value;
-      constexpr int st_cur = U, st_nxt = (U + 1) % 3, st_ld = (U + 2) % 3;
+      constexpr int st_cur = U, st_nxt = (U + 1) % 3;
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
-        load_part(cur, clamp_of(cur, r + 2), st_ld, 2 * s);
-        load_part(cur, clamp_of(cur, r + 2), st_ld, 2 * s + 1);
-        if (s + 1 < kSub) read_ops(st_cur, s + 1, aop[(s + 1) & 1], bop[(s + 1) & 1]);
-        else read_ops(st_nxt, 0, aop[(s + 1) & 1], bop[(s + 1) & 1]);
+        if (s + 1 < kSub) {
+          read_ops(st_cur, s + 1, aop[(s + 1) & 1], bop[(s + 1) & 1]);
+        } else {
+          step_barrier();
+          read_ops(st_nxt, 0, aop[(s + 1) & 1], bop[(s + 1) & 1]);
+          load_step(cur, r + 3, st_cur);
+        }
 #pragma unroll
         for (int i = 0; i < kMB; ++i)
 #pragma unroll
@@ -185,7 +204,6 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
             acc[i][nb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(aop[s & 1][i], bop[s & 1][nb], acc[i][nb], 0, 0, 0);
         schedule_substep();
       }
-      lds_barrier();
     };
     for (int r = 0;;) {
       step(std::integral_constant<int, 0>{}, r);
@@ -195,11 +213,13 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
       step(std::integral_constant<int, 2>{}, r);
       if (++r == nsteps) break;
     }
+    lds_barrier();               // every wave's codes have arrived (the only loads left to wait for)
     const TileItem done = cur;
     if (item + 1 < n_items) {
       cur = wr.item(plan, item + 1, BN, BC);
-      load_stage(cur, clamp_of(cur, 0), 0);
-      load_stage(cur, clamp_of(cur, 1), 1);
+      // (every stage is free: needed reads end before a step's barrier, and a wave's loads into
+      // one place land in order)
+      for (int r = 0; r < 3; ++r) load_step(cur, r, r);
     }
 
     // ---- codes, then the sum over the 32 columns of each block.  v[b][16 i + r]: accumulator r

@@ -68,7 +68,7 @@ __device__ inline void schedule_substep() {
   for (int i = 0; i < kMB * kNB; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // MFMA
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);             // LDS read
-    if (i < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // global load
+    if (i < 6) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // global load
     __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);             // VALU
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -100,10 +100,11 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
   const __amdgpu_buffer_rsrc_t wres = make_rsrc(packed, (uint32_t)N * wrow);
   const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * spr * 2u);
 
-  // ---- gradient tile: row r of 128 bytes, 16-byte chunk c (8 n) stored at c ^ (r % 8).
+  // ---- gradient tile: row r of 128 bytes, 16-byte chunk c (8 n) stored at c ^ (r / 2 % 8): the
+  // sixteen lanes of a read phase cover 256 bytes (two rows share a place, in either 128-byte half).
   // Load j of wave w fills rows 64 j + 8 w .. + 7 (lane i: row + i / 8, stored chunk i % 8).
   const int a_row = tid >> 3;                                        // + 64 j
-  const int a_chunk = (tid & 7) ^ (a_row & 7);
+  const int a_chunk = (tid & 7) ^ ((a_row >> 1) & 7);
   // per item: the byte offset of the thread's chunk in each of its four rows, outside the
   // buffer for rows past M (the step's offset, at most a row, goes into the scalar offset)
   uint32_t a_v[4];
@@ -116,7 +117,7 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
   uint32_t a_r[kSub];
 #pragma unroll
   for (int s = 0; s < kSub; ++s)
-    a_r[s] = (uint32_t)(128 * wm + li) * 128u + (uint32_t)(((4 * h + s) ^ (li & 7)) << 4);
+    a_r[s] = (uint32_t)(128 * wm + li) * 128u + (uint32_t)(((4 * h + s) ^ ((li >> 1) & 7)) << 4);
 
   // ---- packed tile: row n of 128 bytes, chunk c (32 columns) stored at c ^ ((n / 2) % 8), so
   // that the sixteen rows of a transpose read fall on distinct banks (two rows share a chunk
@@ -282,8 +283,9 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
       sreg[2] = load_scale(cur, clamp_of(cur, r + 3));
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
-        load_part(cur, clamp_of(cur, r + 2), st_ld, s);
-        if (s == 0) load_part(cur, clamp_of(cur, r + 2), st_ld, 4);
+        // (all of them in the first sub-step: the barrier at the step's end waits for them)
+        if (s == 0)
+          for (int p = 0; p < 5; ++p) load_part(cur, clamp_of(cur, r + 2), st_ld, p);
         // operands of sub-step s + 1, scales of s + 2, words of the pair after next
         if (s + 1 < kSub) read_a(st_cur, s + 1, aop[(s + 1) & 1]);
         else read_a(st_nxt, 0, aop[(s + 1) & 1]);
