@@ -302,7 +302,7 @@ dscales_join_kernel(const float* __restrict__ partials, float* __restrict__ ds, 
   const int tile = blockIdx.x / groups, c = (blockIdx.x % groups) * 256 + threadIdx.x;
   const Contributors cs(plan, tile);
   float s = 0.f;
-  for (int l = cs.first; l <= cs.last; ++l) s += partials[(size_t)cs.slot(plan, l) * (BN * groups) + c];
+  for (int l = cs.first; l <= cs.last; ++l) s += partials[(size_t)cs.slot(l) * (BN * groups) + c];
   int tm, tn;
   tile_coords(plan.rounds * plan.wgs + tile, plan.tiles_m, plan.tiles_n, tm, tn);
   const int n = tm * BN + c / groups, g = tn * groups + c % groups;

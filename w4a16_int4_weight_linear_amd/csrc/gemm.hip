@@ -707,7 +707,7 @@ swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y,
   const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
   f32x4 v = f32x4{};
   for (int l = cs.first; l <= cs.last; ++l)
-    v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(plan, l) * kPartialBytes);
+    v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(l) * kPartialBytes);
   int tm, tn;
   tile_coords(plan.rounds * plan.wgs + tile, plan.tiles_m, plan.tiles_n, tm, tn);
   const int t = c % kThreads, bq = c / kThreads, i = bq >> 2, q = bq & 3;

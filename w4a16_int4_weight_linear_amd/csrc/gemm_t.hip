@@ -382,7 +382,7 @@ gemm_t_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y,
     f32x4 p[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      p[u] = *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(plan, min(l + u, cs.last)) * kPartialBytes);
+      p[u] = *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(min(l + u, cs.last)) * kPartialBytes);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       if (l + u <= cs.last) v += p[u];

@@ -44,6 +44,7 @@ inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, 
   p.iters = iters;
   int per_xcd = dev.num_cu / kXCD;
   if (per_xcd < 1) per_xcd = 1;
+  if (per_xcd > 32) per_xcd = 32;           // (32-bit iteration counts, see sk_begin)
   p.wgs = per_xcd * kXCD;
   const long long tiles = (long long)tiles_m * tiles_n;
   p.rounds = (int)(tiles / p.wgs);
@@ -54,6 +55,10 @@ inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, 
   long long nsk = (long long)cnt_max * iters / min_steps;
   if (nsk < cnt_max) nsk = cnt_max;
   if (nsk > per_xcd) nsk = per_xcd;
+  // no empty ranges on an XCD with fewer leftover tiles (a join takes every workgroup between
+  // a tile's first and last contributor); for one step per tile a range may then be two tiles
+  const long long least = (long long)(p.sk_tiles >= kXCD ? p.sk_tiles / kXCD : 1) * iters;
+  if (nsk > least) nsk = least;
   p.nsk = p.sk_tiles ? (int)nsk : 0;
   return p;
 }
@@ -79,33 +84,35 @@ struct TileItem {
   int a, b, r0, c0;
 };
 
-// Iterations [sk_begin(l), sk_begin(l + 1)) of an XCD with `cnt` leftover tiles belong to its workgroup l.
-__device__ inline long long sk_begin(const SplitPlan& p, int cnt, int l) {
-  return (long long)cnt * p.iters * l / p.nsk;
+// Iterations [sk_begin(l), sk_begin(l + 1)) of an XCD with `cnt` leftover tiles belong to its
+// workgroup l.  32 bits hold the product: at most 32 leftover tiles and 32 workgroups per
+// XCD, and fewer than 2^21 steps (a packed weight tensor stays below 2 GiB).
+__device__ inline uint32_t sk_begin(const SplitPlan& p, int cnt, int l) {
+  return (uint32_t)cnt * (uint32_t)p.iters * (uint32_t)l / (uint32_t)p.nsk;
 }
 
 // The items of workgroup `wg`: its stream-K segments (n_seg of them: 0, 1 or 2), then one whole tile per round.
 struct WorkRange {
   int wg, xcd, lwg, sk_lo, n_seg, j_first;
-  long long s, e;
+  int s, e;
   __device__ inline WorkRange(const SplitPlan& p, int wg_) : wg(wg_) {
     xcd = wg % kXCD;
     lwg = wg / kXCD;
     sk_lo = xcd_begin(xcd, p.sk_tiles);
     const int cnt = xcd_begin(xcd + 1, p.sk_tiles) - sk_lo;
     const bool in = lwg < p.nsk && cnt > 0;
-    s = in ? sk_begin(p, cnt, lwg) : 0;
-    e = in ? sk_begin(p, cnt, lwg + 1) : 0;
-    n_seg = e > s ? (int)((e - 1) / p.iters - s / p.iters) + 1 : 0;
-    j_first = (int)(s / p.iters);
+    s = in ? (int)sk_begin(p, cnt, lwg) : 0;
+    e = in ? (int)sk_begin(p, cnt, lwg + 1) : 0;
+    j_first = s / p.iters;
+    n_seg = e > s ? (e > (j_first + 1) * p.iters ? 2 : 1) : 0;
   }
   __device__ inline TileItem item(const SplitPlan& p, int i, int tile_rows, int tile_cols) const {
     TileItem it;
     int tau;
     if (i < n_seg) {
-      const long long lo = (long long)(j_first + i) * p.iters;
-      it.a = (int)((s > lo ? s : lo) - lo);
-      it.b = (int)((e < lo + p.iters ? e : lo + p.iters) - lo);
+      const int lo = (j_first + i) * p.iters;
+      it.a = (s > lo ? s : lo) - lo;
+      it.b = (e < lo + p.iters ? e : lo + p.iters) - lo;
       tau = p.rounds * p.wgs + sk_lo + j_first + i;
     } else {
       it.a = 0;
@@ -122,28 +129,21 @@ struct WorkRange {
 
 // The workgroups [first, last] of an XCD that hold parts of leftover tile `tile` (0 .. sk_tiles - 1), in order.
 struct Contributors {
-  int xcd, first, last, cnt;
-  long long lo;
+  int xcd, first, last;
+  bool first_cut;            // the first one's range began in the tile before
   __device__ inline Contributors(const SplitPlan& p, int tile) {
-    for (xcd = 0; xcd_begin(xcd + 1, p.sk_tiles) <= tile; ++xcd) {}
+    const int q = p.sk_tiles / kXCD, r = p.sk_tiles % kXCD;
+    xcd = tile < r * (q + 1) ? tile / (q + 1) : r + (tile - r * (q + 1)) / (q > 0 ? q : 1);
     const int sk_lo = xcd_begin(xcd, p.sk_tiles);
-    cnt = xcd_begin(xcd + 1, p.sk_tiles) - sk_lo;
-    lo = (long long)(tile - sk_lo) * p.iters;
-    // workgroup l holds iteration i iff sk_begin(l) <= i < sk_begin(l + 1)
-    const long long total = (long long)cnt * p.iters;
-    auto owner = [&](long long i) {
-      int l = (int)(i * p.nsk / total);
-      while (l + 1 < p.nsk && sk_begin(p, cnt, l + 1) <= i) ++l;
-      while (l > 0 && sk_begin(p, cnt, l) > i) --l;
-      return l;
-    };
-    first = owner(lo);
-    last = owner(lo + p.iters - 1);
+    const int cnt = xcd_begin(xcd + 1, p.sk_tiles) - sk_lo;
+    const uint32_t total = (uint32_t)cnt * (uint32_t)p.iters, lo = (uint32_t)(tile - sk_lo) * (uint32_t)p.iters;
+    // the largest l with floor(total l / nsk) <= i, i.e. l < (i + 1) nsk / total
+    first = (int)(((lo + 1) * (uint32_t)p.nsk - 1) / total);
+    last = (int)(((lo + (uint32_t)p.iters) * (uint32_t)p.nsk - 1) / total);
+    first_cut = sk_begin(p, cnt, first) < lo;
   }
   // partial slot of contributor l: its second segment if its range began in the tile before
-  __device__ inline int slot(const SplitPlan& p, int l) const {
-    return 2 * (l * kXCD + xcd) + (sk_begin(p, cnt, l) < lo ? 1 : 0);
-  }
+  __device__ inline int slot(int l) const { return 2 * (l * kXCD + xcd) + (l == first && first_cut ? 1 : 0); }
 };
 
 }  // namespace w4a16
