@@ -203,11 +203,13 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
  * m <= 16 without gate_up runs as w4a16_gemv_swiglu, m <= 32 on the
  * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
- * The workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none) needs no initial
- * state and calls one after another on one stream may share it, also with the
- * three operators below (not with w4a16_gemm, whose workspace holds state).  No
- * call waits for another: calls on several streams may run at once, each with a
- * workspace of its own.  Errors as w4a16_gemm; k == 0 writes zeros.
+ * Workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none, the pointer may be NULL):
+ * a fresh one must be zero-filled once before its first use, and every call leaves
+ * it ready for the next.  Calls one after another on one stream may share one,
+ * also with the three operators below (not with w4a16_gemm, whose workspace is
+ * laid out differently).  No call waits for another: calls on several streams
+ * may run at once, each with a workspace of its own.  Errors as w4a16_gemm;
+ * k == 0 writes zeros.
  */
 w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                uint16_t* gate_up, int64_t m, int64_t n, int64_t k, int32_t group, void* workspace,

@@ -318,9 +318,9 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 #
 # These calls run on the tensors' own device whichever is current, allocate on
 # the stream they launch on, and keep one workspace per (device, stream), grown to
-# the largest size asked for.  The workspaces hold no state between calls.  Under
-# graph capture each call takes one from the graph's own pool, so captured graphs
-# share none.  A smallest call is bound by what the host does before it launches,
+# the largest size asked for.  A workspace begins with counters that are 0 between
+# calls.  Under graph capture each call takes one from the graph's own pool and
+# clears its counters in the graph, so captured graphs share none.  A smallest call is bound by what the host does before it launches,
 # so the checks here walk the arguments once.
 # ---------------------------------------------------------------------------
 def _check_ffn(what, specs):
@@ -405,13 +405,34 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
     if nbytes == 0:
         return 0, 0
     if _torch_preload.cuda.is_current_stream_capturing():
-        ws = _torch_preload.empty(nbytes, dtype=_torch_preload.uint8, device=device)
+        ws = _new_workspace(nbytes, device)
         return ws.data_ptr(), nbytes     # freed to the graph's pool, whose later work is ordered behind this call
     key = (device.index, handle)
     ws = _FFN_WORKSPACES.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _FFN_WORKSPACES[key] = _torch_preload.empty(nbytes, dtype=_torch_preload.uint8, device=device)
-    return ws.data_ptr(), ws.numel()
+    if ws is None or ws.numel() * 4 < nbytes:
+        ws = _FFN_WORKSPACES[key] = _new_workspace(nbytes, device)
+    return ws.data_ptr(), ws.numel() * 4
+
+
+_COUNTER_WORDS = 4096        # the counters a workspace begins with
+
+
+def _new_workspace(nbytes, device):
+    ws = _torch_preload.empty((nbytes + 3) // 4, dtype=_torch_preload.int32, device=device)
+    ws[:_COUNTER_WORDS].zero_()
+    return ws
+
+
+def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None):
+    """A workspace tensor for gemm_swiglu, gemm_swiglu_backward, gemm_t or gemm_dscales (`call` by name)
+    of these sizes (n as in the C ABI: outputs of the gated calls, else weight rows); None if none is needed."""
+    if call not in ("gemm_swiglu", "gemm_swiglu_backward", "gemm_t", "gemm_dscales"):
+        raise ValueError(f"ffn_workspace: no workspace for {call!r}")
+    device = _torch_preload.device("cuda", _torch_preload.cuda.current_device()) if device is None \
+        else _torch_preload.device(device)
+    with _torch_preload.cuda.device(device):
+        nbytes = getattr(lib, f"w4a16_{call}_workspace_bytes")(m, n, k, group)
+        return _new_workspace(nbytes, device) if nbytes else None
 
 
 def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace=None, stream=None):
@@ -635,4 +656,4 @@ __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "u
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
            "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t",
-           "gemm_swiglu_backward", "gemm_dscales"] + list(SIGNATURES)
+           "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace"] + list(SIGNATURES)

@@ -19,8 +19,10 @@
 //   two rows and keeps one per lane: 2.4 operations per accumulator instead of 10),
 //   which leaves lane l rows 2 l and 2 l + 1 of the wave's 64 per half.
 // * Leftover tiles are split along m as in tile_gemm.hpp; a part is 256 x groups fp32
-//   (2 or 8 KB), and a second kernel adds the parts in order.  Sums are fp32
-//   throughout, products of fp16 pairs exact; results do not depend on timing.
+//   (2 or 8 KB), and a second kernel adds the parts in order (adding them in the last
+//   contributor instead measured 6 us slower at 133 rows: its stores, its arrival and its
+//   loads each pay the device-scope latency in turn).  Sums are fp32 throughout, products
+//   of fp16 pairs exact; results do not depend on timing.
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -319,13 +321,14 @@ size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) 
 
 size_t dscales_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  return pad_bytes(m, n) + (p.sk_tiles ? 2 * (size_t)p.wgs * BN * (BC / group) * 4 : 0);
+  const size_t bytes = pad_bytes(m, n) + (p.sk_tiles ? 2 * (size_t)p.wgs * BN * (BC / group) * 4 : 0);
+  return bytes ? kCounterBytes + bytes : 0;
 }
 
 hipError_t launch_dscales(const uint16_t* d, const uint16_t* x, const uint32_t* packed, float* ds, int m, int n, int k,
                           int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = workspace ? behind_counters(workspace) : nullptr;
   uint32_t pitch = (uint32_t)n * 2u;
   if (n % 8) {
     const hipError_t e = launch_pad_rows(d, reinterpret_cast<uint16_t*>(ws), m, n, stream);

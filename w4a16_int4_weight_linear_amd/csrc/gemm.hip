@@ -785,7 +785,7 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
   uint32_t* counters = nullptr;
   uint32_t* status = nullptr;
   if (EPI != kEpiProduct) {
-    partials = static_cast<float*>(workspace);
+    partials = workspace ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
   } else if (workspace) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     status = reinterpret_cast<uint32_t*>(ws);
@@ -816,7 +816,7 @@ hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t
 
 size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev) {
   const GemmPlan p = gemm_plan(m, 2 * n_out, k, dev);
-  return p.sk_tiles ? 2 * (size_t)p.wgs * kPartialBytes : 0;
+  return p.sk_tiles ? kCounterBytes + 2 * (size_t)p.wgs * kPartialBytes : 0;
 }
 
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,

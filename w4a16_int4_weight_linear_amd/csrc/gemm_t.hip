@@ -411,7 +411,8 @@ size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) 
 
 size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  return pad_bytes(m, n) + (p.sk_tiles ? 2 * (size_t)p.wgs * kPartialBytes : 0);
+  const size_t bytes = pad_bytes(m, n) + (p.sk_tiles ? 2 * (size_t)p.wgs * kPartialBytes : 0);
+  return bytes ? kCounterBytes + bytes : 0;
 }
 
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream) {
@@ -429,7 +430,7 @@ hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipSt
 hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
                          int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = workspace ? behind_counters(workspace) : nullptr;
   uint32_t pitch = (uint32_t)n * 2u;
   if (n % 8) {
     const hipError_t e = launch_pad_rows(d, reinterpret_cast<uint16_t*>(ws), m, n, stream);

@@ -18,8 +18,10 @@
 // * The rows of d and the scales of the workgroup's range are staged in LDS once (scales
 //   turned to [group][n]).  Rows of d go to MFMA rows (r, lq) -> 4 lq + r, so that up to
 //   four rows of d occupy one accumulator register per column.
-// * The waves' sums are added in wave order in LDS; ranges of n are joined by a second
-//   small kernel in range order (fixed order, no atomics, no state in the workspace).
+// * The waves' sums are added in wave order in LDS; the ranges' sums of a strip by
+//   its last workgroup, in range order (one launch; no workgroup waits for another), or,
+//   where that workgroup would have more than kJoinRows rows to add, by a second kernel on
+//   the whole device.  Results do not depend on timing.
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -38,7 +40,15 @@ struct SkinnyPlan {
   int strips, splits, units, range;             // strips of CW columns, ranges of n, units of 32 n, n per range
   int xpitch;                                   // bytes of a staged row of d
   uint32_t lds;
+  bool fused;                                   // the strips' last workgroups add the ranges' sums
 };
+
+// Rows (ranges x rows of d, 1 KB each) that a strip's last workgroup adds at most.  Measured,
+// last workgroup against second kernel, device time: 1 row 1024 -> 1024 (4 rows) 6.8 / 7.4 us,
+// 1 row through a 1024 x 2048 pair (4) 9.1 / 9.6, 1 row 17408 -> 5120 (25) 19.0 / 18.3, 19 rows
+// through the pair (76) 14.3 / 12.3, 16 rows 17408 -> 5120 (400) 27.3 / 21.3; the second launch
+// also takes 2.3 us of the host's time per call, which is what bounds the small ones.
+constexpr int kJoinRows = 16;
 
 // Rows of d summed over the waves at a time: 64 KB for one block (two workgroups share a
 // CU's LDS), 128 KB for two.
@@ -57,9 +67,10 @@ template <int G, int MB>
 __global__ void __launch_bounds__(kThreads)
 gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
                      const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
-                     SkinnyPlan plan, float* __restrict__ partials) {
+                     SkinnyPlan plan, float* __restrict__ partials, uint32_t* __restrict__ counters) {
   constexpr int kGroups = CW / G;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ uint32_t arrived;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -224,6 +235,8 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   // ---- sums over the waves, 4 kR rows of d at a time: buffer [wave][4 kR rows][256 columns]
   // fp32, columns 16 li + f; 16-byte chunk j of a lane's columns at j ^ (li / 2 % 4) (bank
   // spread).  Accumulator r of lane (lq, li) is row 4 r + lq of its block.
+  const __amdgpu_buffer_rsrc_t pres =
+      make_rsrc(partials, plan.splits > 1 ? (uint32_t)plan.splits * (uint32_t)(M * K) * 4u : 0u);
   float* red = reinterpret_cast<float*>(smem);
   constexpr int kR = red_rows(MB) / 4;
   const int wstride = red_stride(M, MB);
@@ -264,10 +277,39 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
             *reinterpret_cast<uint32_t*>(y + (size_t)m * K + k) =
                 (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
           else
-            *reinterpret_cast<float2*>(partials + ((size_t)split * M + m) * K + k) = make_float2(s0, s1);
+            __builtin_amdgcn_raw_buffer_store_b64(
+                u32x2{__builtin_bit_cast(uint32_t, s0), __builtin_bit_cast(uint32_t, s1)}, pres,
+                (uint32_t)(m * K + k) * 4u, (uint32_t)split * (uint32_t)(M * K) * 4u, kDeviceScope);
         }
       }
     }
+
+  // ---- ranges of n: the strip's last workgroup adds the ranges' sums in range order ----
+  if (plan.splits == 1 || !plan.fused || !arrive_last(counters + strip, (uint32_t)plan.splits, &arrived)) return;
+  const int cols = min(CW, K - c0) / 2;                        // column pairs of the strip
+  for (int o = tid; o < M * (CW / 2); o += kThreads) {
+    const int m = o / (CW / 2), c = o % (CW / 2);
+    if (c >= cols) continue;
+    const uint32_t at = (uint32_t)(m * K + c0 + 2 * c) * 4u;
+    float s0 = 0.f, s1 = 0.f;
+    for (int p0 = 0; p0 < plan.splits; p0 += 8) {              // eight loads in flight
+      u32x2 v[8];
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        v[p] = __builtin_bit_cast(
+            u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                       pres, at, (uint32_t)min(p0 + p, plan.splits - 1) * (uint32_t)(M * K) * 4u, kDeviceScope));
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p0 + p < plan.splits) {
+          const uint32_t lo = v[p][0], hi = v[p][1];
+          s0 += __builtin_bit_cast(float, lo);
+          s1 += __builtin_bit_cast(float, hi);
+        }
+    }
+    *reinterpret_cast<uint32_t*>(y + (size_t)m * K + c0 + 2 * c) =
+        (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
+  }
 }
 
 // y = the ranges' sums [splits][m k] added in order: two outputs per thread, sixteen loads in flight.
@@ -284,10 +326,11 @@ gemm_t_skinny_join_kernel(const float* __restrict__ partials, uint16_t* __restri
       v[p] = *reinterpret_cast<const float2*>(partials + (size_t)q * count + i);
     }
 #pragma unroll
-    for (int p = 0; p < 16; ++p) {
-      s0 += p0 + p < splits ? v[p].x : 0.f;
-      s1 += p0 + p < splits ? v[p].y : 0.f;
-    }
+    for (int p = 0; p < 16; ++p)
+      if (p0 + p < splits) {
+        s0 += v[p].x;
+        s1 += v[p].y;
+      }
   }
   *reinterpret_cast<uint32_t*>(y + i) = (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
 }
@@ -311,6 +354,7 @@ SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
   if (splits < 1) splits = 1;
   p.range = ((p.units + splits - 1) / splits) * kUnit;
   p.splits = (n + p.range - 1) / p.range;
+  p.fused = p.splits > 1 && p.splits * m <= kJoinRows && p.strips <= kCounters;
   p.xpitch = p.range * 2 + 16;
   const uint32_t stage = (uint32_t)(mb * 16 * p.xpitch + (CW / group) * p.range * 2);
   const uint32_t red = (uint32_t)(kWaves * red_stride(m, mb) * 4);
@@ -319,19 +363,15 @@ SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
 }
 
 template <int G>
-hipError_t launch_g(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n, int k,
-                    const SkinnyPlan& p, float* partials, hipStream_t stream) {
-  const int mb = blocks_of(m);
-  auto kern = mb == 1 ? gemm_t_skinny_kernel<G, 1> : gemm_t_skinny_kernel<G, 2>;
-  return launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d, packed, scales, y,
-                       m, n, k, p, partials);
+auto kernel_of(int m) {
+  return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1> : gemm_t_skinny_kernel<G, 2>;
 }
 
 }  // namespace
 
 size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
   const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  return p.splits > 1 ? (size_t)p.splits * m * k * 4 : 0;
+  return p.splits > 1 ? kCounterBytes + (size_t)p.splits * m * k * 4 : 0;
 }
 
 bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
@@ -344,10 +384,12 @@ bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                                 int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  float* partials = p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  const hipError_t e = group == 128 ? launch_g<128>(d, packed, scales, y, m, n, k, p, partials, stream)
-                                    : launch_g<32>(d, packed, scales, y, m, n, k, p, partials, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
+  float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
+  uint32_t* counters = static_cast<uint32_t*>(workspace);
+  auto kern = group == 128 ? kernel_of<128>(m) : kernel_of<32>(m);
+  const hipError_t e = launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d,
+                                     packed, scales, y, m, n, k, p, partials, counters);
+  if (e != hipSuccess || p.splits == 1 || p.fused) return e;
   const int count = m * k;
   return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 2 + 63) / 64)), dim3(64), 0, stream,
                        partials, y, count, p.splits);

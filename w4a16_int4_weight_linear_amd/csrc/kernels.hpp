@@ -77,8 +77,15 @@ hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const u
                               uint16_t* z, int m, int n_out, int k, int group, void* workspace,
                               const DeviceInfo& dev, hipStream_t stream);
 
+// ---- workspaces of the feed-forward block's operators ----
+// A workspace begins with arrival counters, all 0 between calls (zero-filled once by the
+// caller); the sizes below include them.  Everything behind holds nothing between calls.
+constexpr int kCounters = 4096;
+constexpr size_t kCounterBytes = kCounters * sizeof(uint32_t);
+inline uint8_t* behind_counters(void* workspace) { return static_cast<uint8_t*>(workspace) + kCounterBytes; }
+
 // ---- the product with the weights' other side, tiled (gemm_t.hip) ----
-// y [m, k] = d [m, n] . deq(W), W [n, k].  The workspace needs no initial state (0 bytes: none).
+// y [m, k] = d [m, n] . deq(W), W [n, k].
 size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev);
 hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
                          int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
