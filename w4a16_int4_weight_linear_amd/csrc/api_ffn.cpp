@@ -19,8 +19,8 @@ using w4a16::kMaxDim;
 using w4a16::status_of;
 using w4a16::valid_group;
 
-// Up to 32 rows the gate/up product is a weight stream: one pass of the
-// weight-streaming kernel per 16 rows, as in w4a16_gemm; beyond, the tiled GEMM.
+// Up to 32 rows the gate/up product is a weight stream: the weight-streaming kernel, its
+// blocks of 16 rows side by side in one launch; beyond, the tiled GEMM.
 constexpr int64_t kSkinnyRows = 32;
 
 bool swiglu_skinny(int64_t m, int64_t n2, int64_t k, const DeviceInfo& dev) {
@@ -120,16 +120,9 @@ w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const 
   // up to 16 rows with nothing kept: the decode product (its kernels for 1-4 rows are faster)
   if (!gate_up && m <= 16) return w4a16_gemv_swiglu(x, packed, scales, y, m, n, k, group, stream);
   if (swiglu_skinny(m, 2 * n, k, dev)) {
-    for (int64_t m0 = 0; m0 < m; m0 += 16) {
-      const int mm = (int)(m - m0 < 16 ? m - m0 : 16);
-      const hipError_t e =
-          gate_up ? w4a16::launch_swiglu_skinny_keep(x + m0 * k, packed, scales, y + m0 * n, gate_up + m0 * 2 * n, mm,
-                                                     (int)n, (int)k, group, dev, st)
-                  : w4a16::launch_swiglu_skinny(x + m0 * k, packed, scales, y + m0 * n, mm, (int)n, (int)k, group,
-                                                dev, st);
-      if (e != hipSuccess) return W4A16_ERR_HIP;
-    }
-    return W4A16_OK;
+    return status_of(gate_up ? w4a16::launch_swiglu_skinny_keep(x, packed, scales, y, gate_up, (int)m, (int)n, (int)k,
+                                                                group, dev, st)
+                             : w4a16::launch_swiglu_skinny(x, packed, scales, y, (int)m, (int)n, (int)k, group, dev, st));
   }
   const size_t need = w4a16::gemm_swiglu_workspace_bytes((int)m, (int)n, (int)k, dev);
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
@@ -165,12 +158,15 @@ w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate
   const bool product = n > 0 && k > 0;
   const size_t need = product ? t_workspace_bytes(m, 2 * n, k, group, dev) : 0;
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  // (the tiled product's padded copy of its left side, where it needs one, is filled on the way)
+  uint16_t* padded = product && !t_skinny(m, 2 * n, k, group, dev) ? w4a16::gemm_t_padded((int)(2 * n), workspace) : nullptr;
   if (n > 0) {
-    const hipError_t e = w4a16::launch_swiglu_grad(dy, gate_up, dgate_up, (size_t)(m * n), st);
+    const hipError_t e = w4a16::launch_swiglu_grad(dy, gate_up, dgate_up, padded, (int)m, (int)n, st);
     if (e != hipSuccess) return W4A16_ERR_HIP;
   }
   if (!product) return k > 0 ? status_of(w4a16::launch_zero_fill(dx, (size_t)(m * k), st)) : W4A16_OK;
-  return status_of(launch_t(dgate_up, packed, scales, dx, m, 2 * n, k, group, need ? workspace : nullptr, dev, st));
+  return status_of(launch_t(padded ? nullptr : dgate_up, packed, scales, dx, m, 2 * n, k, group,
+                            need ? workspace : nullptr, dev, st));
 }
 
 size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group) {

@@ -64,6 +64,14 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
                    const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
                    int M, int N, int K, int rows_base, int rows_extra, uint16_t* __restrict__ z) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  // grid row p: rows 16 p .. 16 p + 15 (the SwiGLU product of up to 32 rows is one launch)
+  if (const int p = blockIdx.y; p > 0) {
+    x += (size_t)16 * p * K;
+    y += (size_t)16 * p * (SWIGLU ? N >> 1 : N);
+    if constexpr (KEEP) z += (size_t)16 * p * N;
+    M -= 16 * p;
+  }
+  M = min(M, 16);
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -355,7 +363,7 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
 template <int G, bool ALIGNED, bool SWIGLU, bool KEEP>
 hipError_t launch_ga(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
                      int m, int n, int k, int blocks, int units, hipStream_t stream) {
-  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU, KEEP>, dim3(blocks), dim3(kThreads), 0, stream, x,
+  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU, KEEP>, dim3(blocks, (m + 15) / 16), dim3(kThreads), 0, stream, x,
                        packed, scales, y, m, n, k, units / blocks, units % blocks, z);
 }
 

@@ -48,7 +48,8 @@ hipError_t launch_gemv_mfma(const uint16_t* x, const uint32_t* packed, const uin
 bool gemm_skinny_fits(int m, int n, int k, const DeviceInfo& dev);
 hipError_t launch_gemm_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                               int n, int k, int group, const DeviceInfo& dev, hipStream_t stream);
-// y [m, n_out] = SiLU(gate) * up, packed/scales holding 2 n_out interleaved rows (1 <= m <= 16).
+// y [m, n_out] = SiLU(gate) * up, packed/scales holding 2 n_out interleaved rows; blocks of 16
+// rows side by side in one launch.
 hipError_t launch_swiglu_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                 int m, int n_out, int k, int group, const DeviceInfo& dev, hipStream_t stream);
 
@@ -89,6 +90,9 @@ inline uint8_t* behind_counters(void* workspace) { return static_cast<uint8_t*>(
 size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev);
 hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m, int n,
                          int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
+// Where launch_gemm_t keeps d with rows padded to 8 elements (null: n is a multiple of 8 and d
+// is read in place).  A caller that has filled it passes d = null.
+uint16_t* gemm_t_padded(int n, void* workspace);
 // d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row.
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
 
@@ -99,9 +103,10 @@ size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const Devic
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                                 int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
 
-// ---- gradient of SiLU(g) u (swiglu_grad.hip): count outputs, interleaved pairs ----
-hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, size_t count,
-                              hipStream_t stream);
+// ---- gradient of SiLU(g) u (swiglu_grad.hip): m x n outputs, interleaved pairs ----
+// padded, if not null, receives dgate_up too, rows padded with zeros to a multiple of 8 elements.
+hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, uint16_t* padded, int m,
+                              int n, hipStream_t stream);
 
 // ---- gradient of the scales (dscales.hip) ----
 // ds [n, k / group] fp32 from d [m, n] and x [m, k].  The workspace needs no initial state.

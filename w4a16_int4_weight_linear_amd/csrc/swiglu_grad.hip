@@ -52,10 +52,36 @@ swiglu_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__
   }
 }
 
+// The same for rows of 2 n elements that are no multiple of 8: one output per thread, written
+// to dgate_up and to the padded copy that the product reads (np: its pairs per row).
+__global__ void __launch_bounds__(256)
+swiglu_grad_padded_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gate_up,
+                          uint16_t* __restrict__ dgate_up, uint16_t* __restrict__ padded, int n, int np, size_t count) {
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;     // over m x np
+  if (i >= count) return;
+  const size_t m = i / (uint32_t)np;
+  const int c = (int)(i - m * (uint32_t)np);
+  f16x2 r = {};
+  if (c < n) {
+    const size_t at = m * (size_t)n + c;
+    const f16x2 z = *reinterpret_cast<const f16x2*>(gate_up + 2 * at);
+    r = grad_pair(z[0], z[1], __builtin_bit_cast(_Float16, dh[at]));
+    *reinterpret_cast<f16x2*>(dgate_up + 2 * at) = r;
+  }
+  *reinterpret_cast<f16x2*>(padded + 2 * i) = r;
+}
+
 }  // namespace
 
-hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, size_t count,
-                              hipStream_t stream) {
+hipError_t launch_swiglu_grad(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up, uint16_t* padded, int m,
+                              int n, hipStream_t stream) {
+  if (padded) {
+    const int np = (2 * n + 7) / 8 * 4;
+    const size_t count = (size_t)m * np;
+    return launch_kernel(swiglu_grad_padded_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, stream, dh,
+                         gate_up, dgate_up, padded, n, np, count);
+  }
+  const size_t count = (size_t)m * n;
   return launch_kernel(swiglu_grad_kernel, dim3((unsigned)((count + 2047) / 2048)), dim3(256), 0, stream, dh, gate_up,
                        dgate_up, count);
 }
