@@ -15,9 +15,12 @@
 //   once, as in the GEMM).  Eight n of a column are exactly a lane's slice of
 //   v_mfma_f32_16x16x32_f16, so a unit is 16 such operands, each used by the one or two
 //   blocks of sixteen rows of d.
-// * The rows of d and the scales of the workgroup's range are staged in LDS once (scales
-//   turned to [group][n]).  Rows of d go to MFMA rows (r, lq) -> 4 lq + r, so that up to
-//   four rows of d occupy one accumulator register per column.
+// * A wave loads what a unit needs, weights, operands of d (already in MFMA layout) and
+//   scales, straight to registers; only the scales cross lanes, through 128
+//   or 512 bytes of LDS of the wave's own.  No workgroup barrier precedes the sums: staging d
+//   and the scales per workgroup instead kept the first unit waiting until 3.5 us after the
+//   start (4.3 us to its end, of 8.6; 32 rows 17408 -> 5120: 35.4 us against 22.6).  Rows of d go to MFMA rows (r, lq) -> 4 lq + r, so
+//   that up to four rows of d occupy one accumulator register per column.
 // * The waves' sums are added in wave order in LDS; the ranges' sums of a strip by
 //   its last workgroup, in range order (one launch; no workgroup waits for another), or,
 //   where that workgroup would have more than kJoinRows rows to add, by a second kernel on
@@ -38,7 +41,6 @@ constexpr int kF = CW / 16;                     // operands (columns) per lane a
 
 struct SkinnyPlan {
   int strips, splits, units, range;             // strips of CW columns, ranges of n, units of 32 n, n per range
-  int xpitch;                                   // bytes of a staged row of d
   uint32_t lds;
   bool fused;                                   // the strips' last workgroups add the ranges' sums
 };
@@ -50,9 +52,8 @@ struct SkinnyPlan {
 // also takes 2.3 us of the host's time per call, which is what bounds the small ones.
 constexpr int kJoinRows = 16;
 
-// Rows of d summed over the waves at a time: 64 KB for one block (two workgroups share a
-// CU's LDS), 128 KB for two.
-__host__ __device__ constexpr int red_rows(int mb) { return mb == 1 ? 8 : 16; }
+// Rows of d summed over the waves at a time: 128 KB of LDS.
+__host__ __device__ constexpr int red_rows(int) { return 16; }
 // floats of one wave's sums in that buffer (whole quads of rows)
 __host__ __device__ constexpr int red_stride(int m, int mb) {
   return (m < red_rows(mb) ? (m + 3) / 4 * 4 : red_rows(mb)) * CW;
@@ -63,13 +64,15 @@ __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
   return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
 }
 
-template <int G, int MB>
-__global__ void __launch_bounds__(kThreads)
+// VEC: rows of d are 16-byte aligned (N a multiple of 8); otherwise d comes in 2-byte loads.
+template <int G, int MB, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2)   // (two waves per SIMD: one workgroup per CU)
 gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
                      const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
                      SkinnyPlan plan, float* __restrict__ partials, uint32_t* __restrict__ counters) {
   constexpr int kGroups = CW / G;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ __attribute__((aligned(16))) uint8_t scale_tile[kWaves * kGroups * kUnit * 2];
   __shared__ uint32_t arrived;
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -86,92 +89,55 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   const int spr = K / G;
   const __amdgpu_buffer_rsrc_t wres = make_rsrc(packed, (uint32_t)N * wrow);
 
-  // ---- weight stream: unit u's rows n_lo + 32 u + 8 lq + j ----
+  // ---- loads of unit u, all straight to registers: its rows n = n_lo + 32 u + 8 lq + j of the
+  // weights, the lane's operand of d (row 4 (li % 4) + li / 4 of each block, eight n; zeros past
+  // N; rows past M feed nothing) and the unit's scales, kS per lane.  Past the wave's last unit
+  // every offset lies outside the buffers (no memory access).
+  constexpr int kS = kGroups / 2;               // lane: row lane / 2, groups kS (lane % 2) ..
+  const __amdgpu_buffer_rsrc_t dres = make_rsrc(d, (uint32_t)M * (uint32_t)N * 2u);
+  const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * (uint32_t)spr * 2u);
   const uint32_t w_v = (uint32_t)(8 * lq) * wrow + (uint32_t)(4 * kWords * li);
-  auto load_unit = [&](int u, uint32_t (&w)[8][kWords]) {
-    const bool live = u < units;                                // wave-uniform; else no memory access
+  const int x_row = (li & 3) * 4 + (li >> 2);
+  const int s_n = lane >> 1, s_g = kS * (lane & 1);
+  struct Unit {
+    uint32_t w[8][kWords];
+    u32x4 x[MB];
+    uint16_t s[kS];
+  };
+  auto load_unit = [&](int u, Unit& t) {
+    const bool live = u < units;                                // wave-uniform
+    const int n0 = n_lo + kUnit * u;
+#pragma unroll
+    for (int g = 0; g < kS; ++g) {
+      const int n = n0 + s_n, gg = c0 / G + s_g + g;
+      t.s[g] = __builtin_amdgcn_raw_buffer_load_b16(
+          sres, live && n < N && gg < spr ? ((uint32_t)n * (uint32_t)spr + (uint32_t)gg) * 2u : kOutOfRange, 0, 0);
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      const int r = x_row + 16 * b, n = n0 + 8 * lq;
+      const bool ok = live && r < M;
+      const uint32_t at = ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u;
+      if constexpr (VEC) {
+        t.x[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(dres, ok && n < N ? at : kOutOfRange, 0, 0));
+      } else {
+        uint16_t e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          e[j] = __builtin_amdgcn_raw_buffer_load_b16(dres, ok && n + j < N ? at + 2u * j : kOutOfRange, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t.x[b][j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+      }
+    }
     const uint32_t off = live ? w_v : kOutOfRange;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t so = live ? (uint32_t)(n_lo + kUnit * u + j) * wrow + (uint32_t)(c0 >> 1) : 0u;
+      const uint32_t so = live ? (uint32_t)(n0 + j) * wrow + (uint32_t)(c0 >> 1) : 0u;
       const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(wres, off, so, kStream));
-      w[j][0] = v[0];
-      w[j][1] = v[1];
+      t.w[j][0] = v[0];
+      t.w[j][1] = v[1];
     }
   };
-
-  // ---- staging: rows of d (zeros past N; rows past M feed nothing), scales [group][n].
-  // The first loads go out before the first weight loads (loads return in order: waiting for
-  // them then does not wait for the weights), the rest, if any, after them.
-  uint8_t* xs = smem;
-  uint8_t* ss = smem + (size_t)MB * 16 * plan.xpitch;
-  const int rng = units * kUnit;                                // staged n (a multiple of 32)
-  const __amdgpu_buffer_rsrc_t dres = make_rsrc(d, (uint32_t)M * (uint32_t)N * 2u);
-  const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * (uint32_t)spr * 2u);
-  const bool vec = N % 8 == 0;                                  // rows of d 16-byte aligned: 16-byte pieces
-  const int pieces = vec ? rng / 8 : 0, xtotal = M * pieces;
-  auto load_x = [&](int r, int c, bool ok) -> u32x4 {
-    const int n = n_lo + 8 * c;
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                         dres, ok && n < N ? ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u : kOutOfRange, 0, 0));
-  };
-  auto store_x = [&](int r, int c, const u32x4& v) { *reinterpret_cast<u32x4*>(xs + r * plan.xpitch + 16 * c) = v; };
-  auto load_s = [&](int i) -> uint16_t {
-    const int n = n_lo + i / kGroups, g = c0 / G + i % kGroups;
-    const bool ok = i < rng * kGroups && n < N && g < spr;
-    return __builtin_amdgcn_raw_buffer_load_b16(sres, ok ? ((uint32_t)n * (uint32_t)spr + (uint32_t)g) * 2u : kOutOfRange, 0, 0);
-  };
-  auto store_s = [&](int i, uint16_t v) {
-    *reinterpret_cast<uint16_t*>(ss + ((i % kGroups) * plan.range + i / kGroups) * 2) = v;
-  };
-  constexpr int kX0 = MB == 1 ? 4 : 6, kS0 = kGroups == 2 ? 4 : 8;   // loads per thread ahead of the weights
-  const int xstep_r = vec ? kThreads / pieces : 0, xstep_c = vec ? kThreads - xstep_r * pieces : 0;
-  int xr = vec ? tid / pieces : 0, xc = vec ? tid - xr * pieces : 0;
-  u32x4 x0[kX0];
-  uint16_t s0[kS0];
-#pragma unroll
-  for (int j = 0; j < kX0; ++j) {
-    x0[j] = load_x(xr, xc, tid + j * kThreads < xtotal);
-    xr += xstep_r;
-    xc += xstep_c;
-    if (xc >= pieces && vec) {
-      xc -= pieces;
-      ++xr;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kS0; ++j) s0[j] = load_s(tid + j * kThreads);
-
-  // two units in flight per wave
-  uint32_t wa[8][kWords], wb[8][kWords];
-  load_unit(wave, wa);
-  load_unit(wave + kWaves, wb);
-
-  if (vec) {
-    int r = tid / pieces, c = tid - r * pieces;
-#pragma unroll
-    for (int j = 0; j < kX0; ++j) {
-      if (tid + j * kThreads < xtotal) store_x(r, c, x0[j]);
-      r += xstep_r;
-      c += xstep_c;
-      if (c >= pieces) {
-        c -= pieces;
-        ++r;
-      }
-    }
-    for (int i = tid + kX0 * kThreads; i < xtotal; i += kThreads) store_x(i / pieces, i % pieces, load_x(i / pieces, i % pieces, true));
-  } else {
-    for (int i = tid; i < M * rng; i += kThreads) {
-      const int r = i / rng, c = i - r * rng;
-      const int n = n_lo + c;
-      *reinterpret_cast<uint16_t*>(xs + r * plan.xpitch + 2 * c) = n < N ? d[(size_t)r * N + n] : (uint16_t)0;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kS0; ++j)
-    if (tid + j * kThreads < rng * kGroups) store_s(tid + j * kThreads, s0[j]);
-  for (int i = tid + kS0 * kThreads; i < rng * kGroups; i += kThreads) store_s(i, load_s(i));
-  __syncthreads();
 
   f32x4 acc[MB][kF];
 #pragma unroll
@@ -184,16 +150,19 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   asm volatile("" : "+v"(e_lo), "+v"(e_hi));
   const f16x2 b_lo = {(_Float16)-1032.f, (_Float16)-1032.f}, b_hi = {(_Float16)-72.f, (_Float16)-72.f};
 
-  // operand row li of d: row 4 (li % 4) + li / 4 of its block
-  const uint8_t* xrow = xs + ((li & 3) * 4 + (li >> 2)) * plan.xpitch + 16 * lq;
-  const uint8_t* srow = ss + ((kF * li) / G) * plan.range * 2 + 16 * lq;
+  // the wave's scales of a unit, turned to [group][32 n] (a wave's LDS accesses stay in order)
+  uint8_t* ss = scale_tile + wave * (kGroups * kUnit * 2);
+  uint8_t* s_w = ss + (s_g * kUnit + s_n) * 2;
+  const uint8_t* s_r = ss + ((kF * li) / G) * kUnit * 2 + 16 * lq;
 
-  auto use_unit = [&](int u, const uint32_t (&w)[8][kWords]) {
-    const f16x8 sc = *reinterpret_cast<const f16x8*>(srow + u * (kUnit * 2));
+  auto use_unit = [&](const Unit& t) {
+    const auto& w = t.w;
+#pragma unroll
+    for (int g = 0; g < kS; ++g) *reinterpret_cast<uint16_t*>(s_w + g * kUnit * 2) = t.s[g];
+    const f16x8 sc = *reinterpret_cast<const f16x8*>(s_r);
     f16x8 xv[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
-      xv[b] = *reinterpret_cast<const f16x8*>(xrow + b * 16 * plan.xpitch + u * (kUnit * 2));
+    for (int b = 0; b < MB; ++b) xv[b] = __builtin_bit_cast(f16x8, t.x[b]);
 #pragma unroll
     for (int wd = 0; wd < kWords; ++wd)
 #pragma unroll
@@ -210,8 +179,8 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
 #pragma unroll
           for (int jp = 0; jp < 4; ++jp) {
             const uint32_t src = c < 2 ? p[jp] : p8[jp];
-            const uint32_t t = (c & 1) ? ((src & m_hi) | e_hi) : ((src & m_lo) | e_lo);
-            const f16x2 v = (__builtin_bit_cast(f16x2, t) + ((c & 1) ? b_hi : b_lo)) * f16x2{sc[2 * jp], sc[2 * jp + 1]};
+            const uint32_t v16 = (c & 1) ? ((src & m_hi) | e_hi) : ((src & m_lo) | e_lo);
+            const f16x2 v = (__builtin_bit_cast(f16x2, v16) + ((c & 1) ? b_hi : b_lo)) * f16x2{sc[2 * jp], sc[2 * jp + 1]};
             op[2 * jp] = v[0];
             op[2 * jp + 1] = v[1];
           }
@@ -223,13 +192,15 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
       }
   };
 
-  for (int u = wave; u < units; u += 2 * kWaves) {
-    use_unit(u, wa);
-    load_unit(u + 2 * kWaves, wa);
-    if (u + kWaves < units) {
-      use_unit(u + kWaves, wb);
-      load_unit(u + 3 * kWaves, wb);
-    }
+  // One unit per wave at a time.  (Two, three or four in registers mean as many copies of the
+  // unit's 2 KB of code, which every launch fetches anew: 1 row 1024 -> 1024 6.2 / 7.3 / 8.6 us
+  // against 5.4 us, 17408 -> 5120 16.1 / 16.9 / 19.0 against 15.8.)
+  Unit t;
+  load_unit(wave, t);
+#pragma unroll 1
+  for (int u = wave; u < units; u += kWaves) {
+    use_unit(t);
+    load_unit(u + kWaves, t);
   }
 
   // ---- sums over the waves, 4 kR rows of d at a time: buffer [wave][4 kR rows][256 columns]
@@ -344,27 +315,21 @@ SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
   SkinnyPlan p;
   p.strips = (k + CW - 1) / CW;
   p.units = (n + kUnit - 1) / kUnit;
-  // workgroups: one or two per CU
-  const int slots = dev.num_cu * (mb == 1 ? 2 : 1);
+  const int slots = dev.num_cu;
   int splits = slots / p.strips;
-  constexpr int kMaxRange = 1024;             // what fits in LDS
-  const int lo = (n + kMaxRange - 1) / kMaxRange;
   if (splits > (p.units + kWaves - 1) / kWaves) splits = (p.units + kWaves - 1) / kWaves;
-  if (splits < lo) splits = lo;
   if (splits < 1) splits = 1;
   p.range = ((p.units + splits - 1) / splits) * kUnit;
   p.splits = (n + p.range - 1) / p.range;
   p.fused = p.splits > 1 && p.splits * m <= kJoinRows && p.strips <= kCounters;
-  p.xpitch = p.range * 2 + 16;
-  const uint32_t stage = (uint32_t)(mb * 16 * p.xpitch + (CW / group) * p.range * 2);
-  const uint32_t red = (uint32_t)(kWaves * red_stride(m, mb) * 4);
-  p.lds = stage > red ? stage : red;
+  p.lds = (uint32_t)(kWaves * red_stride(m, mb) * 4);
   return p;
 }
 
 template <int G>
-auto kernel_of(int m) {
-  return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1> : gemm_t_skinny_kernel<G, 2>;
+auto kernel_of(int m, int n) {
+  if (n % 8 == 0) return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1, true> : gemm_t_skinny_kernel<G, 2, true>;
+  return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1, false> : gemm_t_skinny_kernel<G, 2, false>;
 }
 
 }  // namespace
@@ -377,8 +342,7 @@ size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const Devic
 bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
   if (m > kSkinnyTRows) return false;
   const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  // (a range is limited by LDS: a very large product would need many ranges, and their sums room)
-  return p.lds <= dev.max_lds && (p.splits == 1 || (size_t)p.splits * m * k * 4 <= kMaxSums);
+  return p.lds + 8192 <= dev.max_lds && (p.splits == 1 || (size_t)p.splits * m * k * 4 <= kMaxSums);
 }
 
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
@@ -386,7 +350,7 @@ hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const
   const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
   float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
   uint32_t* counters = static_cast<uint32_t*>(workspace);
-  auto kern = group == 128 ? kernel_of<128>(m) : kernel_of<32>(m);
+  auto kern = group == 128 ? kernel_of<128>(m, n) : kernel_of<32>(m, n);
   const hipError_t e = launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d,
                                      packed, scales, y, m, n, k, p, partials, counters);
   if (e != hipSuccess || p.splits == 1 || p.fused) return e;
