@@ -171,13 +171,15 @@ enum Epilogue { kEpiProduct, kEpiSwiglu, kEpiSwigluKeep };
 // Two rows of a (gate, up) column pair.  a0, a1: this lane's column in two
 // accumulator rows.  Lanes 2i and 2i + 1 hold a pair's gate and up columns; after
 // the swap the even lane has both for row 0 and returns its SiLU(g) u, the odd
-// lane those of row 1.
+// lane those of row 1.  The reciprocal instruction (within one fp32 unit in the
+// last place, far below the fp16 rounding that follows) stands for a division of
+// ten instructions: 1282 against 1295 us at 4096 rows of 5120 -> 17408.
 __device__ inline float swiglu_pair(float a0, float a1, bool odd) {
   const float send = odd ? a0 : a1;
   const float got = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
                                                   0, __builtin_bit_cast(int, send), 0xB1, 0xf, 0xf, false));
   const float g = odd ? got : a0, u = odd ? a1 : got;
-  return g / (1.0f + __expf(-g)) * u;
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 // SALIGN: every row's scales start on a 16-byte boundary (K / G a multiple
