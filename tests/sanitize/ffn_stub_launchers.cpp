@@ -18,6 +18,11 @@ bool gemm_t_skinny_fits(int, int, int, int, const DeviceInfo&) { return false; }
 size_t gemm_t_skinny_workspace_bytes(int, int, int, int, const DeviceInfo&) { return 0; }
 hipError_t launch_gemm_t_skinny(const uint16_t*, const uint32_t*, const uint16_t*, uint16_t*, int, int, int, int, void*,
                                 const DeviceInfo&, hipStream_t) { return hipErrorNoDevice; }
+bool swiglu_backward_skinny_fits(int, int, int, int, const DeviceInfo&) { return false; }
+hipError_t launch_swiglu_backward_skinny(const uint16_t*, const uint16_t*, uint16_t*, const uint32_t*, const uint16_t*,
+                                         uint16_t*, int, int, int, int, void*, const DeviceInfo&, hipStream_t) {
+  return hipErrorNoDevice;
+}
 hipError_t launch_swiglu_grad(const uint16_t*, const uint16_t*, uint16_t*, uint16_t*, int, int, hipStream_t) {
   return hipErrorNoDevice;
 }

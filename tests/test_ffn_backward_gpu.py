@@ -59,6 +59,17 @@ def test_block_backward(w4, m, n, k, group):
     assert_close(dx, dz.astype(np.float64) @ oracle.dequantize(q, s, group), f"m={m} n={n} k={k} dx")
 
 
+# up to 32 rows: pairs' gradient within the product (n a multiple of 4, short ranges per wave: one to
+# four units of 32 rows of W) and in front of it (the last: ranges of more units)
+FEW_ROWS = [(1, 4, 32, 32), (16, 36, 544, 32), (32, 1028, 1056, 32), (17, 4100, 256, 128), (5, 16300, 512, 128),
+            (2, 2100, 16384, 128)]
+
+
+@pytest.mark.parametrize("m,n,k,group", FEW_ROWS)
+def test_block_backward_few_rows(w4, m, n, k, group):
+    test_block_backward(w4, m, n, k, group)
+
+
 def test_block_gradient_against_differences(w4):
     """Central differences of sum(h * dy) in x, in fp64 by the definition, against the library's whole chain."""
     torch = torch_mod()

@@ -158,8 +158,13 @@ w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate
   const bool product = n > 0 && k > 0;
   const size_t need = product ? t_workspace_bytes(m, 2 * n, k, group, dev) : 0;
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  const bool few_rows = product && t_skinny(m, 2 * n, k, group, dev);
+  if (few_rows && w4a16::swiglu_backward_skinny_fits((int)m, (int)(2 * n), (int)k, group, dev))
+    return status_of(w4a16::launch_swiglu_backward_skinny(dy, gate_up, dgate_up, packed, scales, dx, (int)m,
+                                                          (int)(2 * n), (int)k, group, need ? workspace : nullptr, dev,
+                                                          st));
   // (the tiled product's padded copy of its left side, where it needs one, is filled on the way)
-  uint16_t* padded = product && !t_skinny(m, 2 * n, k, group, dev) ? w4a16::gemm_t_padded((int)(2 * n), workspace) : nullptr;
+  uint16_t* padded = product && !few_rows ? w4a16::gemm_t_padded((int)(2 * n), workspace) : nullptr;
   if (n > 0) {
     const hipError_t e = w4a16::launch_swiglu_grad(dy, gate_up, dgate_up, padded, (int)m, (int)n, st);
     if (e != hipSuccess) return W4A16_ERR_HIP;

@@ -28,6 +28,7 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "swiglu_grad.hpp"
 
 namespace w4a16 {
 namespace {
@@ -51,6 +52,14 @@ struct SkinnyPlan {
 // through the pair (76) 14.3 / 12.3, 16 rows 17408 -> 5120 (400) 27.3 / 21.3; the second launch
 // also takes 2.3 us of the host's time per call, which is what bounds the small ones.
 constexpr int kJoinRows = 16;
+
+// Units per wave up to which every strip makes the pairs' gradient for itself (GRAD); past that
+// the elementwise kernel runs first, as its one pass costs less than the strips' repeated work.
+// Device time, within the product against in front of it: 19 rows, 1024 x 2048 pair (1 unit per
+// wave) 10.4 / 11.4 us, 1 row, 16384 x 2048 (2 x 8192; 2 units) 11.4 / 12.5, 1 row 32768 x 2048
+// (4) 15.3 / 15.7, 32 rows 24576 x 2048 (3) 20.6 / 21.5, 1 row 34816 x 5120 (12) 30.3 / 27.5, 32
+// rows 47.1 / 39.4; it also saves 2.7 us of the host's time per call.
+constexpr int kGradUnits = 4;
 
 // Rows of d summed over the waves at a time: 128 KB of LDS.
 __host__ __device__ constexpr int red_rows(int) { return 16; }
@@ -84,11 +93,17 @@ __device__ inline bool arrive_last(uint32_t* counter, uint32_t parts, uint32_t* 
 }
 
 // VEC: rows of d are 16-byte aligned (N a multiple of 8); otherwise d comes in 2-byte loads.
-template <int G, int MB, bool VEC>
+// GRAD (with VEC): d is the gradient of SiLU(g) u at the pairs gate_up [M, N]: `d` holds that of
+// the products h [M, N / 2], every wave makes its operands of d from the two, and the first
+// strip's workgroups write them to dgate_up.  One launch less than with the elementwise
+// kernel in front; see kGradUnits.
+template <int G, int MB, bool VEC, bool GRAD>
 __global__ void __launch_bounds__(kThreads, 2)   // (two waves per SIMD: one workgroup per CU)
 gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
                      const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
-                     SkinnyPlan plan, float* __restrict__ partials, uint32_t* __restrict__ counters) {
+                     SkinnyPlan plan, float* __restrict__ partials, uint32_t* __restrict__ counters,
+                     const uint16_t* __restrict__ gate_up, uint16_t* __restrict__ dgate_up) {
+  static_assert(VEC || !GRAD, "pairs are read eight elements at a time");
   constexpr int kGroups = CW / G;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ __attribute__((aligned(16))) uint8_t scale_tile[kWaves * kGroups * kUnit * 2];
@@ -113,7 +128,8 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   // N; rows past M feed nothing) and the unit's scales, kS per lane.  Past the wave's last unit
   // every offset lies outside the buffers (no memory access).
   constexpr int kS = kGroups / 2;               // lane: row lane / 2, groups kS (lane % 2) ..
-  const __amdgpu_buffer_rsrc_t dres = make_rsrc(d, (uint32_t)M * (uint32_t)N * 2u);
+  const __amdgpu_buffer_rsrc_t dres = make_rsrc(GRAD ? gate_up : d, (uint32_t)M * (uint32_t)N * 2u);
+  const __amdgpu_buffer_rsrc_t hres = make_rsrc(d, GRAD ? (uint32_t)M * (uint32_t)N : 0u);
   const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * (uint32_t)spr * 2u);
   const uint32_t w_v = (uint32_t)(8 * lq) * wrow + (uint32_t)(4 * kWords * li);
   const int x_row = (li & 3) * 4 + (li >> 2);
@@ -121,6 +137,7 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   struct Unit {
     uint32_t w[8][kWords];
     u32x4 x[MB];
+    u32x2 dh[GRAD ? MB : 1];
     uint16_t s[kS];
   };
   auto load_unit = [&](int u, Unit& t) {
@@ -137,6 +154,8 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
       const int r = x_row + 16 * b, n = n0 + 8 * lq;
       const bool ok = live && r < M;
       const uint32_t at = ((uint32_t)r * (uint32_t)N + (uint32_t)n) * 2u;
+      if constexpr (GRAD)
+        t.dh[b] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(hres, ok && n < N ? at >> 1 : kOutOfRange, 0, 0));
       if constexpr (VEC) {
         t.x[b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(dres, ok && n < N ? at : kOutOfRange, 0, 0));
       } else {
@@ -174,14 +193,29 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   uint8_t* s_w = ss + (s_g * kUnit + s_n) * 2;
   const uint8_t* s_r = ss + ((kF * li) / G) * kUnit * 2 + 16 * lq;
 
-  auto use_unit = [&](const Unit& t) {
+  auto use_unit = [&](const Unit& t, int u) {
     const auto& w = t.w;
 #pragma unroll
     for (int g = 0; g < kS; ++g) *reinterpret_cast<uint16_t*>(s_w + g * kUnit * 2) = t.s[g];
     const f16x8 sc = *reinterpret_cast<const f16x8*>(s_r);
     f16x8 xv[MB];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) xv[b] = __builtin_bit_cast(f16x8, t.x[b]);
+    for (int b = 0; b < MB; ++b) {
+      xv[b] = __builtin_bit_cast(f16x8, t.x[b]);
+      if constexpr (GRAD) {
+        const f16x8 z = xv[b];
+        using f16x4 = _Float16 __attribute__((ext_vector_type(4)));
+        const f16x4 dh = __builtin_bit_cast(f16x4, t.dh[b]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x2 r = grad_pair(z[2 * e], z[2 * e + 1], dh[e]);
+          xv[b][2 * e] = r[0];
+          xv[b][2 * e + 1] = r[1];
+        }
+        const int r = x_row + 16 * b, n = n_lo + kUnit * u + 8 * lq;
+        if (strip == 0 && r < M && n < N) *reinterpret_cast<f16x8*>(dgate_up + (size_t)r * N + n) = xv[b];
+      }
+    }
 #pragma unroll
     for (int wd = 0; wd < kWords; ++wd)
 #pragma unroll
@@ -218,7 +252,7 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   load_unit(wave, t);
 #pragma unroll 1
   for (int u = wave; u < units; u += kWaves) {
-    use_unit(t);
+    use_unit(t, u);
     load_unit(u + kWaves, t);
   }
 
@@ -346,9 +380,27 @@ SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
 }
 
 template <int G>
-auto kernel_of(int m, int n) {
-  if (n % 8 == 0) return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1, true> : gemm_t_skinny_kernel<G, 2, true>;
-  return blocks_of(m) == 1 ? gemm_t_skinny_kernel<G, 1, false> : gemm_t_skinny_kernel<G, 2, false>;
+auto kernel_of(int m, int n, bool grad) {
+  const bool one = blocks_of(m) == 1;
+  if (grad) return one ? gemm_t_skinny_kernel<G, 1, true, true> : gemm_t_skinny_kernel<G, 2, true, true>;
+  if (n % 8 == 0) return one ? gemm_t_skinny_kernel<G, 1, true, false> : gemm_t_skinny_kernel<G, 2, true, false>;
+  return one ? gemm_t_skinny_kernel<G, 1, false, false> : gemm_t_skinny_kernel<G, 2, false, false>;
+}
+
+// With gate_up: d is the gradient of h, and the pairs' gradient is written to dgate_up.
+hipError_t launch_any(const uint16_t* d, const uint16_t* gate_up, uint16_t* dgate_up, const uint32_t* packed,
+                      const uint16_t* scales, uint16_t* y, int m, int n, int k, int group, void* workspace,
+                      const DeviceInfo& dev, hipStream_t stream) {
+  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
+  float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
+  uint32_t* counters = static_cast<uint32_t*>(workspace);
+  auto kern = group == 128 ? kernel_of<128>(m, n, gate_up) : kernel_of<32>(m, n, gate_up);
+  const hipError_t e = launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d,
+                                     packed, scales, y, m, n, k, p, partials, counters, gate_up, dgate_up);
+  if (e != hipSuccess || p.splits == 1 || p.fused) return e;
+  const int count = m * k;
+  return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 2 + 63) / 64)), dim3(64), 0, stream,
+                       partials, y, count, p.splits);
 }
 
 }  // namespace
@@ -366,16 +418,18 @@ bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
 
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                                 int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
-  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
-  uint32_t* counters = static_cast<uint32_t*>(workspace);
-  auto kern = group == 128 ? kernel_of<128>(m, n) : kernel_of<32>(m, n);
-  const hipError_t e = launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d,
-                                     packed, scales, y, m, n, k, p, partials, counters);
-  if (e != hipSuccess || p.splits == 1 || p.fused) return e;
-  const int count = m * k;
-  return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 2 + 63) / 64)), dim3(64), 0, stream,
-                       partials, y, count, p.splits);
+  return launch_any(d, nullptr, nullptr, packed, scales, y, m, n, k, group, workspace, dev, stream);
+}
+
+bool swiglu_backward_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
+  return n % 8 == 0 && gemm_t_skinny_fits(m, n, k, group, dev) &&
+         skinny_plan(m, n, k, group, dev).range <= kGradUnits * kWaves * kUnit;
+}
+
+hipError_t launch_swiglu_backward_skinny(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up,
+                                         const uint32_t* packed, const uint16_t* scales, uint16_t* dx, int m, int n,
+                                         int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
+  return launch_any(dh, gate_up, dgate_up, packed, scales, dx, m, n, k, group, workspace, dev, stream);
 }
 
 }  // namespace w4a16

@@ -102,6 +102,12 @@ bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev);
 size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev);
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                                 int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
+// The same behind the pairs' gradient (n: rows of W): dgate_up [m, n] from dh [m, n / 2] and
+// gate_up [m, n], and dx = dgate_up . deq(W), in one pass.
+bool swiglu_backward_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev);
+hipError_t launch_swiglu_backward_skinny(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up,
+                                         const uint32_t* packed, const uint16_t* scales, uint16_t* dx, int m, int n,
+                                         int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream);
 
 // ---- gradient of SiLU(g) u (swiglu_grad.hip): m x n outputs, interleaved pairs ----
 // padded, if not null, receives dgate_up too, rows padded with zeros to a multiple of 8 elements.

@@ -10,15 +10,10 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "swiglu_grad.hpp"
 
 namespace w4a16 {
 namespace {
-
-__device__ inline f16x2 grad_pair(_Float16 g16, _Float16 u16, _Float16 dh16) {
-  const float g = (float)g16, u = (float)u16, dh = (float)dh16;
-  const float sig = 1.0f / (1.0f + __expf(-g));
-  return f16x2{(_Float16)(dh * u * sig * (1.0f + g * (1.0f - sig))), (_Float16)(dh * g * sig)};
-}
 
 __global__ void __launch_bounds__(256)
 swiglu_grad_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gate_up,
