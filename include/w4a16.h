@@ -201,6 +201,8 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * (fp16 [m, 2n], 16-byte aligned, or NULL) receives the products themselves, each
  * rounded once, g of output i in column 2i and u in column 2i + 1: what
  * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
+ * Weights enter exactly for m > 32 at group 128 and for m <= 32 with gate_up;
+ * otherwise at worst as fp16(s q), as in w4a16_gemm.
  * m <= 16 without gate_up runs as w4a16_gemv_swiglu, m <= 32 on the
  * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
  * Workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none, the pointer may be NULL):

@@ -23,6 +23,9 @@
 //   contributor instead measured 6 us slower at 133 rows: its stores, its arrival and its
 //   loads each pay the device-scope latency in turn).  Sums are fp32 throughout, products
 //   of fp16 pairs exact; results do not depend on timing.
+// * Measured (MI355X): 2048 rows, 17408 x 5120 316 us = 1.16 PFLOP/s (8192 rows 1235 us), the
+//   rate of a large dense library product: bound by the matrix cores at the clock their power
+//   leaves; 133 rows, 1001 x 1120 13 us, one step's latency after another.
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"

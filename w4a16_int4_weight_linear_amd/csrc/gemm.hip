@@ -46,10 +46,15 @@
 //   of an accumulator block.  The epilogue swaps one value per lane pair (even
 //   lanes then hold both halves of one row, odd lanes of the next), applies
 //   SiLU(g) u to the fp32 sums and rounds once; the m x 2n intermediate reaches
-//   memory only if the caller keeps it for a backward pass.  Its split tiles are
+//   memory only if the caller keeps it for a backward pass.  At g 128 its MFMAs
+//   run on the codes (kCodes).  Its split tiles are
 //   joined by a second, small kernel instead of the in-kernel fix-up: no workgroup
 //   waits for another (calls on several streams cannot hold each other up) and the
-//   workspace holds no state.
+//   workspace holds no state.  Measured, 5120 -> 17408: 512 rows 185-189 us (0.97
+//   PFLOP/s), 4096 rows 1245-1280 us (1.14-1.17; a dense fp16 library product 1160 of
+//   its best size): bound by power.  256 x 256 tiles (eight waves of 128 x 64, or four of
+//   256 x 64 with half the VALU work per MFMA) took 1315-1324 us against 1340 before
+//   the codes, and 118 against 104 us at 256 rows.
 //
 // For integer activations, codes and power-of-two scales every product and
 // partial sum is exact, so such inputs give bit-exact results.
@@ -208,7 +213,9 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   // A SwiGLU product with one scale group per step runs its MFMAs on the codes, and adds each
   // step's results, times the column's scale, to a second set of sums: two more VALU per MFMA
   // against 1.5 fewer for the operands, exact weights, and a higher clock (mfma_operands.hpp).
-  // 183.7 against 194.4 us at 512 rows of 5120 -> 17408, 1278 against 1340 at 4096.
+  // 183.7 against 194.4 us at 512 rows of 5120 -> 17408, 1278 against 1340 at 4096.  (At g 32, four
+  // groups per step and eight more VALU per MFMA, the same costs time: 37.8 against 32.9 us at 4096
+  // rows of 2048 -> 512, 339 against 277 at 4096 -> 4096; weights there stay fp16(q s).)
   constexpr bool kCodes = EPI != kEpiProduct && G == BK;
   constexpr int kSBytes = SALIGN ? 0 : BN * kGroups * 4;       // per-stage scales (unaligned case)
   constexpr int kStage = kStageBytes + kSBytes;
@@ -491,7 +498,8 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
         }
         if (kCodes && s == 0) {
 #pragma unroll
-          for (int nb = 0; nb < kNB; ++nb) gscale[nb] = kCodeUnit * (float)__builtin_bit_cast(_Float16, (uint16_t)sc[0][nb]);
+          for (int nb = 0; nb < kNB; ++nb)
+            gscale[nb] = kCodeUnit * (float)__builtin_bit_cast(_Float16, (uint16_t)sc[0][nb]);
           schedule_group_substep();
         } else {
           schedule_substep();

@@ -27,6 +27,13 @@
 //   n (stream-K).  Partial tiles go to the workspace and a second, small kernel adds
 //   them in contributor order: no workgroup waits for another, so calls on several
 //   streams cannot hold each other up, and the workspace holds no state.
+// * Measured (MI355X): 4096 rows 17408 -> 5120 583-615 us (1.19-1.25 PFLOP/s; the best
+//   dense fp16 library product measured beside it reached 1.16); 512 rows 112 us; 300 rows 2003 -> 2080 16 us and 6
+//   for the join. Bound at many rows by power: MFMAs busy 60% of the time at 1.9 GHz (with
+//   scales of one bit, i.e. operands of few, the same code takes 6% less time); at few
+//   hundred rows by the steps' latency and the partial tiles' way through memory.
+// * Measured slower: loads three steps ahead with a barrier inside the step (3%), no
+//   scheduling groups (1-2%), segments of fewer than four steps (kMinSKSteps).
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -451,7 +458,8 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
   hipError_t e = launch_kernel(group == 128 ? gemm_t_kernel<128> : gemm_t_kernel<32>, dim3(p.wgs), dim3(kThreads), 0,
                                stream, d, packed, scales, y, m, n, k, pitch, p, partials);
   if (e != hipSuccess || p.sk_tiles == 0) return e;
-  return launch_kernel(gemm_t_join_kernel, dim3((unsigned)p.sk_tiles * (kQuads / 256)), dim3(256), 0, stream, partials, y, m, k, p);
+  return launch_kernel(gemm_t_join_kernel, dim3((unsigned)p.sk_tiles * (kQuads / 256)), dim3(256), 0, stream,
+                       partials, y, m, k, p);
 }
 
 }  // namespace w4a16
