@@ -207,7 +207,8 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
  * Workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none, the pointer may be NULL):
  * a fresh one must be zero-filled once before its first use, and every call leaves
- * it ready for the next.  Calls one after another on one stream may share one,
+ * it ready for the next.  Calls one after another on one stream may share one
+ * (a call is up to three kernels: not two host threads' calls on one stream),
  * also with the three operators below (not with w4a16_gemm, whose workspace is
  * laid out differently).  No call waits for another: calls on several streams
  * may run at once, each with a workspace of its own.  Errors as w4a16_gemm;

@@ -274,3 +274,34 @@ def test_large_offsets(w4):
     rows = torch.unique(at)
     assert torch.equal(ds[rows, 0].double(), codes(rows).sum(dim=1) * d[:, rows].double().sum(dim=0))
     assert int((ds != 0).sum()) <= len(rows)
+
+
+def test_threads_on_one_stream(w4):
+    """Two host threads call at once on the same stream: their calls' kernels interleave there."""
+    import threading
+    torch = torch_mod()
+    blocks = [Block(w4, 70, 512, 640, 128, 57000), Block(w4, 300, 512, 640, 128, 57001)]
+    wants = [{a: t.clone() for a, t in b.step().items()} for b in blocks]
+    torch.cuda.synchronize()
+    start, results = threading.Barrier(2), [None, None]
+
+    def work(i):
+        start.wait()
+        results[i] = [blocks[i].step() for _ in range(20)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for r, want in zip(results, wants):
+        assert r is not None and all(same(o, want) for o in r)
+
+
+def test_pairs_gradient_is_not_written_over_the_pairs(w4):
+    b = Block(w4, 3, 64, 128, 32, 57100)
+    z = torch_mod().zeros((3, 128), dtype=torch_mod().float16, device="cuda")
+    dh = torch_mod().zeros((3, 64), dtype=torch_mod().float16, device="cuda")
+    with pytest.raises(ValueError, match="must not be gate_up"):
+        w4.gemm_swiglu_backward(dh, z, *b.gu_d, 32, dgate_up=z)

@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 
 import numpy as np
 
@@ -317,11 +318,12 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # The feed-forward block for any number of rows, with its backward pass.
 #
 # These calls run on the tensors' own device whichever is current, allocate on
-# the stream they launch on, and keep one workspace per (device, stream), grown to
-# the largest size asked for.  A workspace begins with counters that are 0 between
-# calls.  Under graph capture each call takes one from the graph's own pool and
-# clears its counters in the graph, so captured graphs share none.  A smallest call is bound by what the host does before it launches,
-# so the checks here walk the arguments once.
+# the stream they launch on, and keep one workspace per host thread, device and stream,
+# grown to the largest size asked for (a call is up to three kernels, so the calls of two
+# threads on one stream must not share one).  A workspace begins with counters that are 0
+# between calls.  Under graph capture each call takes one from the graph's own pool and
+# clears its counters in the graph, so captured graphs share none.  A smallest call is bound
+# by what the host does before it launches, so the checks here walk the arguments once.
 # ---------------------------------------------------------------------------
 def _check_ffn(what, specs):
     """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""
@@ -388,7 +390,12 @@ def _current_handle(index):
     return raw(index) if raw is not None else _torch_preload.cuda.current_stream(index).cuda_stream
 
 
-_FFN_WORKSPACES = {}
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.of = {}
+
+
+_FFN_WORKSPACES = _Workspaces()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -398,20 +405,21 @@ def _ffn_workspace_bytes(entry, m, n, k, group, device_index):
 
 
 def _ffn_workspace(entry, m, n, k, group, device, handle, given):
-    """(pointer, bytes) of the given workspace, or of one for a call on stream `handle` of the current device."""
+    """The given workspace, or one for a call on stream `handle` of the current device: pointer, bytes, and the
+    tensor, which the caller holds until it has launched."""
     if given is not None:
-        return given.data_ptr(), given.numel() * 4
+        return given.data_ptr(), given.numel() * 4, given
     nbytes = _ffn_workspace_bytes(entry, m, n, k, group, device.index)
     if nbytes == 0:
-        return 0, 0
+        return 0, 0, None
     if _torch_preload.cuda.is_current_stream_capturing():
         ws = _new_workspace(nbytes, device)
-        return ws.data_ptr(), nbytes     # freed to the graph's pool, whose later work is ordered behind this call
+        return ws.data_ptr(), nbytes, ws     # freed to the graph's pool, whose later work is ordered behind this call
     key = (device.index, handle)
-    ws = _FFN_WORKSPACES.get(key)
+    ws = _FFN_WORKSPACES.of.get(key)
     if ws is None or ws.numel() * 4 < nbytes:
-        ws = _FFN_WORKSPACES[key] = _new_workspace(nbytes, device)
-    return ws.data_ptr(), ws.numel() * 4
+        ws = _FFN_WORKSPACES.of[key] = _new_workspace(nbytes, device)
+    return ws.data_ptr(), ws.numel() * 4, ws
 
 
 _COUNTER_WORDS = 4096        # the counters a workspace begins with
@@ -458,7 +466,7 @@ def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace
         nonlocal out
         if out is None:
             out = _torch_preload.empty((m, n), dtype=x.dtype, device=device)
-        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu", m, n, k, group, device, handle, workspace)
+        ws, nbytes, held = _ffn_workspace("w4a16_gemm_swiglu", m, n, k, group, device, handle, workspace)
         _check(lib.w4a16_gemm_swiglu(x.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(),
                                      0 if gate_up is None else gate_up.data_ptr(), m, n, k, group, ws, nbytes, handle),
                "w4a16_gemm_swiglu")
@@ -484,7 +492,7 @@ def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None)
         nonlocal out
         if out is None:
             out = _torch_preload.empty((m, k), dtype=d.dtype, device=device)
-        ws, nbytes = _ffn_workspace("w4a16_gemm_t", m, n, k, group, device, handle, workspace)
+        ws, nbytes, held = _ffn_workspace("w4a16_gemm_t", m, n, k, group, device, handle, workspace)
         _check(lib.w4a16_gemm_t(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(), m, n, k, group,
                                 ws, nbytes, handle), "w4a16_gemm_t")
 
@@ -511,6 +519,8 @@ def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgat
     if workspace is not None:
         specs.append(("workspace", workspace, _I32, None))
     device = _check_ffn(what, specs)
+    if dgate_up is not None and dgate_up.data_ptr() == gate_up.data_ptr() != 0:
+        raise ValueError(f"{what}: dgate_up must not be gate_up (its pairs are read by several workgroups)")
 
     def call(handle):
         nonlocal out, dgate_up
@@ -518,8 +528,8 @@ def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgat
             out = _torch_preload.empty((m, k), dtype=dy.dtype, device=device)
         if dgate_up is None:
             dgate_up = _torch_preload.empty((m, n2), dtype=dy.dtype, device=device)
-        ws, nbytes = _ffn_workspace("w4a16_gemm_swiglu_backward", m, n, k, group, device,
-                                    handle, workspace)
+        ws, nbytes, held = _ffn_workspace("w4a16_gemm_swiglu_backward", m, n, k, group, device, handle,
+                                          workspace)
         _check(lib.w4a16_gemm_swiglu_backward(dy.data_ptr(), gate_up.data_ptr(), packed.data_ptr(), scales.data_ptr(),
                                               dgate_up.data_ptr(), out.data_ptr(), m, n, k, group, ws, nbytes,
                                               handle), "w4a16_gemm_swiglu_backward")
@@ -545,8 +555,7 @@ def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None
         nonlocal out
         if out is None:
             out = _torch_preload.empty((n, k // group), dtype=_torch_preload.float32, device=device)
-        ws, nbytes = _ffn_workspace("w4a16_gemm_dscales", m, n, k, group, device, handle,
-                                    workspace)
+        ws, nbytes, held = _ffn_workspace("w4a16_gemm_dscales", m, n, k, group, device, handle, workspace)
         _check(lib.w4a16_gemm_dscales(d.data_ptr(), x.data_ptr(), packed.data_ptr(), out.data_ptr(), m, n, k, group,
                                       ws, nbytes, handle), "w4a16_gemm_dscales")
 
