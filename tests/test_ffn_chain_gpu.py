@@ -174,8 +174,11 @@ def test_one_workspace_for_every_call(w4):
         got = dict(z=z2, h=h, dx=dx, dz=dz2, ds_gu=ds)
         assert same(got, {a: want[a] for a in got}) and torch.equal(y1, y2)
         assert int(ws[:4096].abs().sum()) == 0
+    # 1024 rows need one (the work is split along them): too small a one is refused
+    rows = torch.zeros((1024, 2 * n), dtype=torch.float16, device="cuda"), torch.zeros((1024, k), dtype=torch.float16, device="cuda")
+    assert w4.ffn_workspace("gemm_dscales", 1024, 2 * n, k, g) is not None
     with pytest.raises(w4.W4A16Error, match="WORKSPACE"):
-        w4.gemm_dscales(dz, b.x_d, b.gu_d[0], g, workspace=ws[:4096].contiguous())
+        w4.gemm_dscales(*rows, b.gu_d[0], g, workspace=ws[:4096].contiguous())
 
 
 @pytest.mark.parametrize("m", [1, 17, 50, 300])

@@ -40,7 +40,7 @@ constexpr int kSub = BR / 16;
 constexpr int kMB = 4, kNB = 2;                  // 32 x 32 blocks per wave
 constexpr int kTileBytes = BR * 512;             // one operand's tile of a step
 constexpr int kStage = 2 * kTileBytes;
-constexpr int kMinSKSteps = 4;                   // steps per split segment, at least
+constexpr SplitCost kCost = {4, 7, 1 << 20};
 constexpr int kStepLoads = 4;                    // vector loads of a wave per step
 
 __device__ inline void schedule_substep() {
@@ -120,7 +120,7 @@ dscales_kernel(const uint16_t* __restrict__ d, const uint16_t* __restrict__ x, c
   const int c_n = 128 * wm + 8 * (p16 >> 2) + 4 * h + (p16 & 3);        // + 32 i
 
   const WorkRange wr(plan, blockIdx.x);
-  const int n_items = wr.n_seg + plan.rounds;
+  const int n_items = wr.count(plan);
 
   // Part p of step r of an item into stage st: d (p = 0, 1), x (p = 2, 3).  Rows past M, and
   // steps past the item's last, go outside the buffers (no memory access, zeros); chunks past
@@ -315,7 +315,7 @@ dscales_join_kernel(const float* __restrict__ partials, float* __restrict__ ds, 
 }
 
 SplitPlan plan_of(int m, int n, int k, const DeviceInfo& dev) {
-  return split_plan((n + BN - 1) / BN, (k + BC - 1) / BC, (m + BR - 1) / BR, kMinSKSteps, dev);
+  return split_plan((n + BN - 1) / BN, (k + BC - 1) / BC, (m + BR - 1) / BR, kCost, dev);
 }
 
 size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) * 2 + 255) & ~(size_t)255) : 0; }

@@ -135,6 +135,14 @@ GemmPlan gemm_plan(int m, int n, int k, const DeviceInfo& dev) {
   return p;
 }
 
+// The SwiGLU product's split: whole tiles where a join would cost more than it saves.
+GemmPlan swiglu_plan(int m, int n, int k, const DeviceInfo& dev) {
+  const int iters = (k + BK - 1) / BK;
+  const SplitCost cost = {iters / 8 > 3 ? iters / 8 : 3, 3, 28};
+  const SplitPlan p = split_plan((m + BM - 1) / BM, (n + BN - 1) / BN, iters, cost, dev);
+  return {p.tiles_m, p.tiles_n, p.tiles_m * p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
+}
+
 // Order of one MFMA sub-step's instructions: each of its 4 MFMAs is
 // followed by up to five VALU instructions (the dequantisation of the next
 // sub-step) and by one LDS read (operands two sub-steps ahead) and one global
@@ -413,7 +421,9 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   // fix-up), then the data-parallel tiles.  The next item's first loads are
   // issued before this item's results are written, so their latency
   // overlaps the output work.
-  const int n_items = n_seg + rounds;
+  // (a SwiGLU product's last round may be a partial one)
+  const bool no_last = EPI != kEpiProduct && (rounds - 1) * wgs + xcd * per_xcd + lwg >= tiles_m * tiles_n;
+  const int n_items = n_seg + rounds - (no_last && rounds > 0 ? 1 : 0);
   Item cur = setup(0);
   if (n_items > 0) prologue_loads(cur);
   for (int item = 0; item < n_items; ++item) {
@@ -836,7 +846,7 @@ namespace {
 template <int EPI>
 hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
                       int m, int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
-  const GemmPlan p = gemm_plan(m, n, k, dev);
+  const GemmPlan p = EPI == kEpiProduct ? gemm_plan(m, n, k, dev) : swiglu_plan(m, n, k, dev);
   float* partials = nullptr;
   uint32_t* flags = nullptr;
   uint32_t* counters = nullptr;
@@ -872,7 +882,7 @@ hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t
 }
 
 size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev) {
-  const GemmPlan p = gemm_plan(m, 2 * n_out, k, dev);
+  const GemmPlan p = swiglu_plan(m, 2 * n_out, k, dev);
   return p.sk_tiles ? kCounterBytes + 2 * (size_t)p.wgs * kPartialBytes : 0;
 }
 

@@ -33,7 +33,7 @@
 //   scales of one bit, i.e. operands of few, the same code takes 6% less time); at few
 //   hundred rows by the steps' latency and the partial tiles' way through memory.
 // * Measured slower: loads three steps ahead with a barrier inside the step (3%), no
-//   scheduling groups (1-2%), segments of fewer than four steps (kMinSKSteps).
+//   scheduling groups (1-2%), segments of fewer than four steps (kCost).
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -51,7 +51,7 @@ constexpr int kBBytes = BR * BC / 2;            // packed weight tile: 64 rows o
 constexpr size_t kPartialBytes = (size_t)BM * BC * 4;
 // Steps per stream-K segment, at least.  8 / 5 / 4 / 3 steps: 128 x 1024 x 1024 13.2 / 12.0 /
 // 10.9 / 11.4 us, 300 x 2000 x 2080 22.6 / 23.1 / 22.5 / 26 us; larger products unchanged.
-constexpr int kMinSKSteps = 4;
+constexpr SplitCost kCost = {4, 4, 14};
 
 // The operand values q s of eight n of one column: word w holds the codes of n0 n2
 // n4 n6 n1 n3 n5 n7, sc their scales in the order n0 .. n7.
@@ -167,7 +167,7 @@ gemm_t_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packe
   asm volatile("" : "+v"(e_lo), "+v"(e_hi));
 
   const WorkRange wr(plan, blockIdx.x);
-  const int n_items = wr.n_seg + plan.rounds;
+  const int n_items = wr.count(plan);
 
   // Part p of step kt of the tile at (m0, c0) into stage st: gradients (p < 4), weights (p = 4).
   // Chunks past N are sent outside the buffer (zeros), rows of weights past N lie outside it.
@@ -411,7 +411,7 @@ pad_rows_kernel(const uint16_t* __restrict__ d, uint16_t* __restrict__ out, int 
 }
 
 SplitPlan plan_of(int m, int n, int k, const DeviceInfo& dev) {
-  return split_plan((m + BM - 1) / BM, (k + BC - 1) / BC, (n + BR - 1) / BR, kMinSKSteps, dev);
+  return split_plan((m + BM - 1) / BM, (k + BC - 1) / BC, (n + BR - 1) / BR, kCost, dev);
 }
 
 size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) * 2 + 255) & ~(size_t)255) : 0; }

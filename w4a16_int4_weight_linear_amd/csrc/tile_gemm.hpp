@@ -9,7 +9,10 @@
 // * the leftover tiles are dealt to the XCDs in contiguous ranges, and an XCD's
 //   (tile, step) iterations are split evenly over nsk of its workgroups, which compute
 //   them first and store fp32 partial tiles.  A workgroup's range is no longer than
-//   one tile, so it touches at most two tiles (slots 2 g and 2 g + 1).
+//   one tile, so it touches at most two tiles (slots 2 g and 2 g + 1);
+// * where splitting the leftover tiles would save fewer steps than joining them costs, nothing
+//   is split: they are a last round that not every workgroup has a tile in, and no second
+//   kernel runs.
 #pragma once
 
 #include <type_traits>
@@ -37,7 +40,13 @@ struct SplitPlan {
   int wgs, rounds, sk_tiles, nsk;           // nsk: stream-K workgroups per XCD
 };
 
-inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, const DeviceInfo& dev) {
+// What splitting costs a kernel: steps per segment, at least; and a join, in the time of steps:
+// join_steps for the second kernel, and one more for every parts_per_step partial tiles.
+struct SplitCost {
+  int min_steps, join_steps, parts_per_step;
+};
+
+inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, const SplitCost& cost, const DeviceInfo& dev) {
   SplitPlan p;
   p.tiles_m = tiles_m;
   p.tiles_n = tiles_n;
@@ -52,7 +61,7 @@ inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, 
   // stream-K workgroups per XCD, from the busiest XCD's ceil(R / 8) tiles;
   // at least one per tile, so no range is longer than a tile
   const int cnt_max = (p.sk_tiles + kXCD - 1) / kXCD;
-  long long nsk = (long long)cnt_max * iters / min_steps;
+  long long nsk = (long long)cnt_max * iters / cost.min_steps;
   if (nsk < cnt_max) nsk = cnt_max;
   if (nsk > per_xcd) nsk = per_xcd;
   // no empty ranges on an XCD with fewer leftover tiles (a join takes every workgroup between
@@ -60,6 +69,14 @@ inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, int min_steps, 
   const long long least = (long long)(p.sk_tiles >= kXCD ? p.sk_tiles / kXCD : 1) * iters;
   if (nsk > least) nsk = least;
   p.nsk = p.sk_tiles ? (int)nsk : 0;
+  if (p.sk_tiles == 0) return p;
+  const long long saved = iters - ((long long)cnt_max * iters + nsk - 1) / nsk;
+  const long long parts = nsk * (p.sk_tiles < kXCD ? p.sk_tiles : kXCD);
+  if (saved <= cost.join_steps + parts / cost.parts_per_step) {
+    if (tiles < p.wgs) p.wgs = (int)(tiles + kXCD - 1) / kXCD * kXCD;
+    p.rounds = (int)((tiles + p.wgs - 1) / p.wgs);
+    p.sk_tiles = p.nsk = 0;
+  }
   return p;
 }
 
@@ -105,6 +122,11 @@ struct WorkRange {
     e = in ? (int)sk_begin(p, cnt, lwg + 1) : 0;
     j_first = s / p.iters;
     n_seg = e > s ? (e > (j_first + 1) * p.iters ? 2 : 1) : 0;
+  }
+  // items of this workgroup (the last round may be a partial one)
+  __device__ inline int count(const SplitPlan& p) const {
+    const int last = (p.rounds - 1) * p.wgs + xcd * (p.wgs / kXCD) + lwg;
+    return n_seg + p.rounds - (p.rounds > 0 && last >= p.tiles_m * p.tiles_n ? 1 : 0);
   }
   __device__ inline TileItem item(const SplitPlan& p, int i, int tile_rows, int tile_cols) const {
     TileItem it;
