@@ -328,6 +328,7 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 def _check_ffn(what, specs):
     """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""
     tensor = _torch_preload.Tensor
+    device, other = specs[0][1].device, None
     for name, t, dtypes, shape in specs:
         if not isinstance(t, tensor):
             raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
@@ -337,12 +338,14 @@ def _check_ffn(what, specs):
             raise ValueError(f"{what}: {name} must be contiguous")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    device = specs[0][1].device
-    for name, t, _, _ in specs:
-        if not t.is_cuda:
-            raise ValueError(f"{what}: {name} is on {t.device}; every tensor must be on the HIP device")
         if t.device != device:
-            raise ValueError(f"{what}: tensors are on different devices {device}, {t.device}")
+            other = name, t.device
+    if device.type != "cuda":
+        other = specs[0][0], device
+    if other is not None:
+        if other[1].type != "cuda":
+            raise ValueError(f"{what}: {other[0]} is on {other[1]}; every tensor must be on the HIP device")
+        raise ValueError(f"{what}: tensors are on different devices {device}, {other[1]}")
     return device
 
 
@@ -416,10 +419,11 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
         ws = _new_workspace(nbytes, device)
         return ws.data_ptr(), nbytes, ws     # freed to the graph's pool, whose later work is ordered behind this call
     key = (device.index, handle)
-    ws = _FFN_WORKSPACES.of.get(key)
-    if ws is None or ws.numel() * 4 < nbytes:
-        ws = _FFN_WORKSPACES.of[key] = _new_workspace(nbytes, device)
-    return ws.data_ptr(), ws.numel() * 4, ws
+    kept = _FFN_WORKSPACES.of.get(key)
+    if kept is None or kept[1] < nbytes:
+        ws = _new_workspace(nbytes, device)
+        kept = _FFN_WORKSPACES.of[key] = ws.data_ptr(), ws.numel() * 4, ws
+    return kept
 
 
 _COUNTER_WORDS = 4096        # the counters a workspace begins with
