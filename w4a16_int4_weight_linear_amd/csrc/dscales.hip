@@ -25,7 +25,8 @@
 //   of fp16 pairs exact; results do not depend on timing.
 // * Measured (MI355X): 2048 rows, 17408 x 5120 316 us = 1.16 PFLOP/s (8192 rows 1235 us), the
 //   rate of a large dense library product: bound by the matrix cores at the clock their power
-//   leaves; 133 rows, 1001 x 1120 13 us, one step's latency after another.
+//   leaves; 133 rows, 1001 x 1120 11.4 us with the padding, one step's latency
+//   after another.
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
@@ -40,6 +41,9 @@ constexpr int kSub = BR / 16;
 constexpr int kMB = 4, kNB = 2;                  // 32 x 32 blocks per wave
 constexpr int kTileBytes = BR * 512;             // one operand's tile of a step
 constexpr int kStage = 2 * kTileBytes;
+// A join takes the time of seven steps, whatever the parts (2 or 8 KB each).  Whole against split
+// tiles, device time, 1024 x 1024: 64 rows (2 steps) 7.3 / 9.4 us, 160 (5) 8.7 / 10.9, 256 (8)
+// 10.1 / 10.8, 384 (12) 12.0 / 11.4, 512 (16) 13.7 / 11.8; 133 rows 1001 x 1120 11.4 / 16.3.
 constexpr SplitCost kCost = {4, 7, 1 << 20};
 constexpr int kStepLoads = 4;                    // vector loads of a wave per step
 

@@ -135,7 +135,12 @@ GemmPlan gemm_plan(int m, int n, int k, const DeviceInfo& dev) {
   return p;
 }
 
-// The SwiGLU product's split: whole tiles where a join would cost more than it saves.
+// The SwiGLU product's split: segments of at least three steps or an eighth of a tile's; a join
+// takes the time of three steps, and of one more per 28 partial tiles (128 KB each, written and
+// read).  Segments of three against five steps: 64 x 1536 -> 512 12.9 / 15.5 us, 33 x 2048 -> 512 14.2 /
+// 15.7, 256 x 2048 -> 512 15.7 / 16.8, but 256 x 5120 -> 17408 99.6 / 97.0.  Whole against split tiles:
+// 64 x 512 -> 512 (4 steps) 10.1 / 11.9, 64 x 768 -> 512 (6) 12.5 / 11.1 (but 2.4 us more of the host's
+// time), 64 x 1024 -> 512 (8) 15.3 / 12.5, 4096 x 2048 -> 512 (128 tiles of 16) 27.0 / 31.5.
 GemmPlan swiglu_plan(int m, int n, int k, const DeviceInfo& dev) {
   const int iters = (k + BK - 1) / BK;
   const SplitCost cost = {iters / 8 > 3 ? iters / 8 : 3, 3, 28};

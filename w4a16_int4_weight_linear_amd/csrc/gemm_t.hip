@@ -51,6 +51,10 @@ constexpr int kBBytes = BR * BC / 2;            // packed weight tile: 64 rows o
 constexpr size_t kPartialBytes = (size_t)BM * BC * 4;
 // Steps per stream-K segment, at least.  8 / 5 / 4 / 3 steps: 128 x 1024 x 1024 13.2 / 12.0 /
 // 10.9 / 11.4 us, 300 x 2000 x 2080 22.6 / 23.1 / 22.5 / 26 us; larger products unchanged.
+// A join: four steps, and one per 14 partial tiles (256 KB each, written and read).  Whole against
+// split tiles, device time: 64 x 320 -> 1024 (5 steps) 8.3 / 9.9 us, 64 x 512 -> 1024 (8) 10.4 / 9.3 (but
+// 2.4 us more of the host's time), 64 x 768 -> 1024 (12) 13.2 / 9.4, 300 x 1024 -> 2080 (16) 24.2 / 18.2;
+// 2048 rows, 160 tiles: 512 -> 5120 (8) 18.1 / 43.8, 1024 -> 5120 (16) 30.7 / 51.4.
 constexpr SplitCost kCost = {4, 4, 14};
 
 // The operand values q s of eight n of one column: word w holds the codes of n0 n2
