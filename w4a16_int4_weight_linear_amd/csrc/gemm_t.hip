@@ -405,13 +405,23 @@ gemm_t_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y,
     if (m0 + r < M) y[(size_t)(m0 + r) * K + k] = float_to_half_bits(v[r]);
 }
 
-// d [m, n] copied with the row pitch padded to 8 elements (zeros), for an n that is no multiple of 8.
+// d [m, n] copied with the row pitch padded to 8 elements (zeros), for an n that is no multiple of
+// 8: a thread makes one 16-byte chunk.  Against one element per thread and a grid row per row of d,
+// whole calls: 4096 x 17407 -> 5120 666 / 731 us, 300 x 2003 -> 2080 25.1 / 25.8, 64 x 401 -> 416 11.8 / 11.6.
 __global__ void __launch_bounds__(256)
-pad_rows_kernel(const uint16_t* __restrict__ d, uint16_t* __restrict__ out, int n, int n8) {
-  const uint16_t* src = d + (size_t)blockIdx.y * n;
-  uint16_t* dst = out + (size_t)blockIdx.y * n8;
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n8) dst[i] = i < n ? src[i] : (uint16_t)0;
+pad_rows_kernel(const uint16_t* __restrict__ d, uint16_t* __restrict__ out, uint32_t n, uint32_t per, uint32_t chunks) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const uint32_t row = i / per, c = (i - row * per) * 8;       // per: chunks of a padded row
+  const uint16_t* src = d + (size_t)row * n;
+  uint16_t t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = src[c + e < n ? c + e : n - 1];
+  u32x4 v;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2)
+    v[e >> 1] = (c + e < n ? t[e] : 0u) | (c + e + 1 < n ? (uint32_t)t[e + 1] << 16 : 0u);
+  *reinterpret_cast<u32x4*>(out + (size_t)i * 8) = v;
 }
 
 SplitPlan plan_of(int m, int n, int k, const DeviceInfo& dev) {
@@ -429,15 +439,9 @@ size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev) {
 }
 
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream) {
-  const int n8 = (n + 7) / 8 * 8;
-  // grid y is limited to 65535 rows
-  for (int r = 0; r < m; r += 65535) {
-    const int rows = m - r < 65535 ? m - r : 65535;
-    const hipError_t e = launch_kernel(pad_rows_kernel, dim3((n8 + 255) / 256, rows), dim3(256), 0, stream,
-                                       d + (size_t)r * n, out + (size_t)r * n8, n, n8);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  const uint32_t per = (uint32_t)(n + 7) / 8, chunks = (uint32_t)m * per;      // (fewer than 2^27)
+  return launch_kernel(pad_rows_kernel, dim3((chunks + 255) / 256), dim3(256), 0, stream, d, out, (uint32_t)n, per,
+                       chunks);
 }
 
 uint16_t* gemm_t_padded(int n, void* workspace) {
