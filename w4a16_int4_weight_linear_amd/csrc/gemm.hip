@@ -586,6 +586,18 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
               *reinterpret_cast<uint16_t*>(ew + (ii * 32 + 8 * (r >> 2) + (r & 3)) * kPitch + nb * 64) =
                   float_to_half_bits(acc[2 * pass + ii][nb][r]);
         // a wave's LDS accesses complete in order: its own writes are visible
+        if (EPI != kEpiProduct && (N & 7) != 0) {
+          // rows of z (an even number of columns) start on 4 bytes only: four rows of sixteen dwords
+          // per store.  With those of h below, against 16-byte chunks as eight 2-byte stores: 2048 rows
+          // 5120 -> 17407, kept, 672 / 837 us, 300 rows 1024 -> 513 19.6 / 31.4.
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int row = 4 * j + (lane >> 4), m = m0 + 64 * pass + row, n = nw + 2 * (lane & 15);
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(ep + row * kPitch + 4 * (lane & 15));
+            if (m < M && n < N) *reinterpret_cast<uint32_t*>(prod + (size_t)m * N + n) = v;
+          }
+          continue;
+        }
 #pragma unroll
         for (int j = 0; j < kRowLanes; ++j) {
           const int row = (64 / kRowLanes) * j + lane / kRowLanes, c = lane % kRowLanes;
@@ -619,20 +631,20 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
           for (int r = 0; r < 16; r += 2)
             *reinterpret_cast<uint16_t*>(hw + (i * 32 + 8 * (r >> 2) + (r & 3)) * kHPitch) =
                 float_to_half_bits(swiglu_pair(acc[i][0][r], acc[i][0][r + 1], odd));
+        if ((No & 7) != 0) {      // unaligned rows: four rows of sixteen elements per store
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = 32 * j + (lane >> 1), c = lane & 1;
-          const u32x4 v = *reinterpret_cast<const u32x4*>(hp + row * kHPitch + c * 16);
-          const int m = m0 + row, n = (nw >> 1) + 8 * c;
-          if (m < M) {
-            uint16_t* dst = y + (size_t)m * No + n;
-            if (n + 8 <= No && (No & 7) == 0) {
-              *reinterpret_cast<u32x4*>(dst) = v;
-            } else {
+          for (int j = 0; j < 32; ++j) {
+            const int row = 4 * j + (lane >> 4), m = m0 + row, n = (nw >> 1) + (lane & 15);
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(hp + row * kHPitch + 2 * (lane & 15));
+            if (m < M && n < No) y[(size_t)m * No + n] = v;
+          }
+        } else {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n + e < No) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-            }
+          for (int j = 0; j < 4; ++j) {
+            const int row = 32 * j + (lane >> 1), c = lane & 1;
+            const u32x4 v = *reinterpret_cast<const u32x4*>(hp + row * kHPitch + c * 16);
+            const int m = m0 + row, n = (nw >> 1) + 8 * c;
+            if (m < M && n < No) *reinterpret_cast<u32x4*>(y + (size_t)m * No + n) = v;
           }
         }
       }
