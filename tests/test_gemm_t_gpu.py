@@ -54,3 +54,22 @@ def test_gaussian(w4, m, n, k, group):
     y = w4.gemm_t(dev(d), dev(w4.pack(q)), dev(s), group)
     torch_mod().cuda.synchronize()
     assert_close(host(y), reference(d, q, s, group), f"m={m} n={n} k={k} g={group}")
+
+
+@pytest.mark.parametrize("m,n", [(5, 63), (17, 37), (3, 257), (40, 63), (9, 62)])
+def test_rows_do_not_see_their_neighbours(w4, m, n):
+    """Rows that start inside a dword or a chunk: infinities and NaN of one row stay in it."""
+    rng = np.random.default_rng(34000 + m + n)
+    k, group = 96, 32
+    q, s = synth.code_bank(rng, 1, n, k)[0], synth.scale_bank(rng, 1, n, k // group)[0]
+    d = synth.activations(rng, m, n)
+    p, s_d = dev(w4.pack(q)), dev(s)
+    want = host(w4.gemm_t(dev(d), p, s_d, group))
+    for row in (1, m // 2, m - 1):
+        bad = d.copy()
+        bad[row, :] = np.inf
+        bad[row, -1] = np.nan
+        got = host(w4.gemm_t(dev(bad), p, s_d, group))
+        others = np.arange(m) != row
+        assert np.array_equal(got[others].view(np.uint16), want[others].view(np.uint16))
+        assert np.isnan(got[row]).all()

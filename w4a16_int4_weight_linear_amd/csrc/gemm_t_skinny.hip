@@ -99,7 +99,9 @@ __device__ inline bool arrive_last(uint32_t* counter, uint32_t parts, uint32_t* 
   return last;
 }
 
-// VEC: rows of d are 16-byte aligned (N a multiple of 8); otherwise d comes in 2-byte loads.
+// VEC: rows of d are 16-byte aligned (N a multiple of 8); otherwise eight elements come as the five
+// dwords that hold them (as eight 2-byte loads: 1 row 17407 -> 5120 17.4 against 16.5 us, 32 rows
+// 5119 -> 17408 40.6 against 34.0; the last element's dword is read and checked by itself).
 // GRAD (with VEC): d is the gradient of SiLU(g) u at the pairs gate_up [M, N]: `d` holds that of
 // the products h [M, N / 2], every wave makes its operands of d from the two, and the first
 // strip's workgroups write them to dgate_up.  One launch less than with the elementwise
@@ -135,7 +137,8 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
   // N; rows past M feed nothing) and the unit's scales, kS per lane.  Past the wave's last unit
   // every offset lies outside the buffers (no memory access).
   constexpr int kS = kGroups / 2;               // lane: row lane / 2, groups kS (lane % 2) ..
-  const __amdgpu_buffer_rsrc_t dres = make_rsrc(GRAD ? gate_up : d, (uint32_t)M * (uint32_t)N * 2u);
+  // (to a whole dword: the last element may share one with what follows, which is cleared)
+  const __amdgpu_buffer_rsrc_t dres = make_rsrc(GRAD ? gate_up : d, ((uint32_t)M * (uint32_t)N * 2u + 3u) & ~3u);
   const __amdgpu_buffer_rsrc_t hres = make_rsrc(d, GRAD ? (uint32_t)M * (uint32_t)N : 0u);
   const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales, (uint32_t)N * (uint32_t)spr * 2u);
   const uint32_t w_v = (uint32_t)(8 * lq) * wrow + (uint32_t)(4 * kWords * li);
@@ -145,6 +148,7 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     uint32_t w[8][kWords];
     u32x4 x[MB];
     u32x2 dh[GRAD ? MB : 1];
+    uint32_t x4[VEC ? 1 : MB];
     uint16_t s[kS];
   };
   auto load_unit = [&](int u, Unit& t) {
@@ -168,12 +172,14 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
         t.x[b] = __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(dres, ok && n < N ? at : kOutOfRange, 0, 0));
       } else {
-        uint16_t e[8];
+        // the dwords that hold the eight elements, from one down to a multiple of four bytes, turned in
+        // use_unit; elements past N (the next row's) are cleared there
+        const uint32_t from = ok && n < N ? at & ~3u : kOutOfRange;
+        uint32_t e[5];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          e[j] = __builtin_amdgcn_raw_buffer_load_b16(dres, ok && n + j < N ? at + 2u * j : kOutOfRange, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t.x[b][j] = (uint32_t)e[2 * j] | ((uint32_t)e[2 * j + 1] << 16);
+        for (int j = 0; j < 5; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b32(dres, from, 4 * j, 0);
+        t.x[b] = u32x4{e[0], e[1], e[2], e[3]};
+        t.x4[b] = e[4];
       }
     }
     const uint32_t off = live ? w_v : kOutOfRange;
@@ -211,6 +217,18 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       xv[b] = __builtin_bit_cast(f16x8, t.x[b]);
+      if constexpr (!VEC) {
+        const int n = n_lo + kUnit * u + 8 * lq, left = N - n;
+        const uint32_t turn = ((uint32_t)(x_row + 16 * b) * (uint32_t)N & 1u) * 16u;      // n is even
+        const uint32_t from[5] = {t.x[b].x, t.x[b].y, t.x[b].z, t.x[b].w, t.x4[b]};
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t e = __builtin_amdgcn_alignbit(from[j + 1], from[j], turn);
+          v[j] = left >= 2 * j + 2 ? e : (left == 2 * j + 1 ? e & 0xFFFFu : 0u);
+        }
+        xv[b] = __builtin_bit_cast(f16x8, v);
+      }
       if constexpr (GRAD) {
         const f16x8 z = xv[b];
         using f16x4 = _Float16 __attribute__((ext_vector_type(4)));
