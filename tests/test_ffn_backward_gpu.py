@@ -128,3 +128,9 @@ def test_scale_gradient_is_exact_on_integers(w4, m, n, k, group):
     ds = host(w4.gemm_dscales(dev(d), dev(x), dev(w4.pack(q)), group))
     want = (q.astype(np.int64) * (d.astype(np.int64).T @ x.astype(np.int64))).reshape(n, k // group, group).sum(axis=2)
     assert np.array_equal(ds.astype(np.int64), want) and np.array_equal(ds, ds.astype(np.int64))
+
+
+# tiles of one or two steps (not split), more of them than workgroups, a partial last round
+@pytest.mark.parametrize("m,n,k,group", [(33, 1, 32, 32), (40, 4500, 4992, 32), (17, 4501, 4992, 128)])
+def test_scale_gradient_few_steps(w4, m, n, k, group):
+    test_scale_gradient(w4, m, n, k, group)

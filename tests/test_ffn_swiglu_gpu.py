@@ -86,3 +86,33 @@ def test_large_negative_and_infinite_gates(w4):
     neg = x[:, 0] < -200
     assert np.all(y[neg] == 0) and np.array_equal(np.isinf(y), np.isinf(want)) and not np.isnan(y).any()
     torch.cuda.synchronize()
+
+
+# tiles of one to three steps (not split), the last with more tiles than workgroups and a partial last round
+FEW_STEPS = [(40, 5, 32, 32), (33, 1, 128, 128), (70, 300, 96, 32), (200, 9, 384, 128), (2000, 2500, 256, 128)]
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("m,n,k,group", FEW_STEPS)
+def test_swiglu_few_steps(w4, m, n, k, group, keep):
+    """Sums so short that roundings do not average out and rows so short that one cancelled product is a
+    row: the bar is the arithmetic itself.  Weights enter as fp16(q s), each off by at most 2^-11 of
+    itself, so a product z = sum x w is off by dz <= 2^-11 sum |x w| (and fp32 sums of up to 384 terms by
+    2^-15 of that, within the factor 1 + 2^-4).  |SiLU'| <= 1.1, so h = SiLU(g) u is off by at most
+    1.1 dg (|u| + du) + |SiLU(g)| du, and its rounding adds 2^-11 |h| (fp32 SiLU: within 2^-4 of that);
+    results below 2^-14 round by 2^-25."""
+    torch = torch_mod()
+    rng = np.random.default_rng(21000 + m + n + k)
+    q, s = codes_and_scales(rng, 2 * n, k, group)
+    x = synth.activations(rng, m, k)
+    z = torch.full((m, 2 * n), float("nan"), dtype=torch.float16, device="cuda") if keep else None
+    h = host(w4.gemm_swiglu(dev(x), dev(w4.pack(q)), dev(s), group, gate_up=z)).astype(np.float64)
+    w, x64 = oracle.dequantize(q, s, group).astype(np.float64), x.astype(np.float64)
+    z64, half = x64 @ w.T, 2.0 ** -11 * (1 + 2.0 ** -4)
+    dz = half * (np.abs(x64) @ np.abs(w).T)
+    g, u, dg, du = z64[:, 0::2], z64[:, 1::2], dz[:, 0::2], dz[:, 1::2]
+    silu = g / (1 + np.exp(-g))
+    want = silu * u
+    assert np.all(np.abs(h - want) <= 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du + half * np.abs(want) + 2.0 ** -24)
+    if keep:
+        assert np.all(np.abs(host(z).astype(np.float64) - z64) <= dz + half * np.abs(z64) + 2.0 ** -24)

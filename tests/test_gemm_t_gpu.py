@@ -73,3 +73,9 @@ def test_rows_do_not_see_their_neighbours(w4, m, n):
         others = np.arange(m) != row
         assert np.array_equal(got[others].view(np.uint16), want[others].view(np.uint16))
         assert np.isnan(got[row]).all()
+
+
+# tiles of one or two steps (not split), more of them than workgroups, a partial last round
+@pytest.mark.parametrize("m,n,k,group", [(33, 1, 32, 32), (4100, 72, 4992, 32), (4100, 33, 4992, 128)])
+def test_exact_on_integers_few_steps(w4, m, n, k, group):
+    test_exact_on_integers(w4, m, n, k, group)
