@@ -201,10 +201,11 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * (fp16 [m, 2n], 16-byte aligned, or NULL) receives the products themselves, each
  * rounded once, g of output i in column 2i and u in column 2i + 1: what
  * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
- * Weights enter exactly for m > 32 at group 128 and for m <= 32 with gate_up;
- * otherwise at worst as fp16(s q), as in w4a16_gemm.
- * m <= 16 without gate_up runs as w4a16_gemv_swiglu, m <= 32 on the
- * weight-streaming kernel; beyond, the tiled GEMM with a SwiGLU epilogue.
+ * Weights enter exactly on the tiles at group 128 and, with gate_up, on the
+ * weight-streaming kernel; otherwise at worst as fp16(s q), as in w4a16_gemm.
+ * m <= 16 without gate_up runs as w4a16_gemv_swiglu, other few rows on the
+ * weight-streaming kernel (m <= 16, or m <= 32 and up to 32 MB of weights);
+ * beyond, the tiled GEMM with a SwiGLU epilogue.
  * Workspace (w4a16_gemm_swiglu_workspace_bytes; 0: none, the pointer may be NULL):
  * a fresh one must be zero-filled once before its first use, and every call leaves
  * it ready for the next.  Calls one after another on one stream may share one

@@ -88,6 +88,16 @@ def test_large_negative_and_infinite_gates(w4):
     torch.cuda.synchronize()
 
 
+# tiles of 64 rows: full and ragged, split and whole, and few rows of weights too large for two passes
+TILES_64 = [(33, 600, 2080, 32), (63, 2176, 1024, 128), (64, 1003, 1280, 128), (64, 8192, 1056, 32), (20, 8200, 4096, 128)]
+
+
+@pytest.mark.parametrize("keep", [False, True])
+@pytest.mark.parametrize("m,n,k,group", TILES_64)
+def test_swiglu_tiles_of_64_rows(w4, m, n, k, group, keep):
+    test_swiglu_any_rows(w4, m, n, k, group, keep)
+
+
 # tiles of one to three steps (not split), the last with more tiles than workgroups and a partial last round
 FEW_STEPS = [(40, 5, 32, 32), (33, 1, 128, 128), (70, 300, 96, 32), (200, 9, 384, 128), (2000, 2500, 256, 128)]
 

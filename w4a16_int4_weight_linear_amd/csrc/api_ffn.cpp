@@ -19,12 +19,16 @@ using w4a16::kMaxDim;
 using w4a16::status_of;
 using w4a16::valid_group;
 
-// Up to 32 rows the gate/up product is a weight stream: the weight-streaming kernel, its
-// blocks of 16 rows side by side in one launch; beyond, the tiled GEMM.
+// Up to 16 rows the gate/up product is a weight stream: the weight-streaming kernel.  17 to 32
+// rows are two passes of it, side by side in one launch, or the tiles, whose fixed costs are
+// larger: weight-streaming against tiles, device time, 24 rows 2048 -> 2048 (4 MB of weights) 9.4 /
+// 14.1 us, 32 rows 4096 -> 4096 (17 MB) 17.5 / 20.8, 32 rows 5120 -> 17408 (89 MB) 59.9 / 44.0.
 constexpr int64_t kSkinnyRows = 32;
+constexpr int64_t kSkinnyTwicePassBytes = (int64_t)32 << 20;
 
 bool swiglu_skinny(int64_t m, int64_t n2, int64_t k, const DeviceInfo& dev) {
-  return m <= kSkinnyRows && w4a16::gemm_skinny_fits((int)(m < 16 ? m : 16), (int)n2, (int)k, dev);
+  return m <= kSkinnyRows && (m <= 16 || n2 * (k / 2) < kSkinnyTwicePassBytes) &&
+         w4a16::gemm_skinny_fits((int)(m < 16 ? m : 16), (int)n2, (int)k, dev);
 }
 
 // The product over n of checked arguments (m, n, k > 0): up to kSkinnyTRows rows on the

@@ -51,8 +51,8 @@
 //   joined by a second, small kernel instead of the in-kernel fix-up: no workgroup
 //   waits for another (calls on several streams cannot hold each other up) and the
 //   workspace holds no state.  Measured, 5120 -> 17408: 512 rows 185-189 us (0.97
-//   PFLOP/s), 4096 rows 1245-1280 us (1.14-1.17; a dense fp16 library product 1160 of
-//   its best size): bound by power.  256 x 256 tiles (eight waves of 128 x 64, or four of
+//   PFLOP/s), 4096 rows 1245-1280 us (1.14-1.17; the best dense fp16
+//   library product measured beside it 1.16): bound by power.  256 x 256 tiles (eight waves of 128 x 64, or four of
 //   256 x 64 with half the VALU work per MFMA) took 1315-1324 us against 1340 before
 //   the codes, and 118 against 104 us at 256 rows.
 //
@@ -80,7 +80,8 @@ constexpr int kABytes = BM * BK * 2;        // activation tile: 128 rows of 256 
 constexpr int kBBytes = BN * BK / 2;        // packed weight tile: 256 rows of 64 bytes
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kWinBytes = BN * 16;            // one scale window: 256 rows x 8 groups x 2 bytes
-constexpr size_t kPartialBytes = (size_t)BM * BN * 4;
+constexpr size_t partial_bytes(int mb) { return (size_t)32 * mb * BN * 4; }     // fp32 tile of mb blocks
+constexpr size_t kPartialBytes = partial_bytes(kMB);
 constexpr uint32_t kSpinLimit = 1u << 24;   // flag polls before the fix-up gives up
 static_assert(3 * kStageBytes + 2 * kWinBytes + 1024 <= 160 * 1024, "LDS use exceeds 160 KB");
 static_assert(3 * (kStageBytes + BN * 4 * 4) <= 160 * 1024, "LDS use exceeds 160 KB");
@@ -141,10 +142,14 @@ GemmPlan gemm_plan(int m, int n, int k, const DeviceInfo& dev) {
 // 15.7, 256 x 2048 -> 512 15.7 / 16.8, but 256 x 5120 -> 17408 99.6 / 97.0.  Whole against split tiles:
 // 64 x 512 -> 512 (4 steps) 10.1 / 11.9, 64 x 768 -> 512 (6) 12.5 / 11.1 (but 2.4 us more of the host's
 // time), 64 x 1024 -> 512 (8) 15.3 / 12.5, 4096 x 2048 -> 512 (128 tiles of 16) 27.0 / 31.5.
+// Tiles of 64 rows where those hold all: half the MFMAs of a step and half the partial tiles (64
+// rows 5120 -> 17408 43.3 against 61.7 us on tiles of 128, 400 -> 416 at g 32 7.8 against 10.1).
+int swiglu_blocks(int m) { return m <= 64 ? 2 : kMB; }
 GemmPlan swiglu_plan(int m, int n, int k, const DeviceInfo& dev) {
+  const int rows = 32 * swiglu_blocks(m);
   const int iters = (k + BK - 1) / BK;
   const SplitCost cost = {iters / 8 > 3 ? iters / 8 : 3, 3, 28};
-  const SplitPlan p = split_plan((m + BM - 1) / BM, (n + BN - 1) / BN, iters, cost, dev);
+  const SplitPlan p = split_plan((m + rows - 1) / rows, (n + BN - 1) / BN, iters, cost, dev);
   return {p.tiles_m, p.tiles_n, p.tiles_m * p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
 }
 
@@ -153,9 +158,10 @@ GemmPlan swiglu_plan(int m, int n, int k, const DeviceInfo& dev) {
 // sub-step) and by one LDS read (operands two sub-steps ahead) and one global
 // load.  A scheduling fence after every sub-step keeps
 // the reads two sub-steps ahead of their use.
+template <int MB>
 __device__ inline void schedule_substep() {
 #pragma unroll
-  for (int mi = 0; mi < kMB * kNB; ++mi) {
+  for (int mi = 0; mi < MB * kNB; ++mi) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // MFMA
     if (mi < 4) {
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);           // LDS read
@@ -167,9 +173,10 @@ __device__ inline void schedule_substep() {
 }
 // ... and of the sub-step that opens a scale group of a product on codes: 16 more
 // VALU instructions before each MFMA (the results it replaces, scaled and summed).
+template <int MB>
 __device__ inline void schedule_group_substep() {
 #pragma unroll
-  for (int mi = 0; mi < kMB * kNB; ++mi) {
+  for (int mi = 0; mi < MB * kNB; ++mi) {
     __builtin_amdgcn_sched_group_barrier(0x002, 20, 0);            // VALU
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);             // MFMA
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);             // LDS read
@@ -215,13 +222,16 @@ __device__ inline float swiglu_pair(float a0, float a1, bool odd) {
 // SALIGN: every row's scales start on a 16-byte boundary (K / G a multiple
 // of 8 and a 16-byte aligned scale array), so they come in LDS windows;
 // otherwise with the stages.
-template <int G, bool KTAIL, bool SALIGN, int EPI>
+// MB: 32-row blocks per tile (4; a SwiGLU product of up to 64 rows: 2).
+template <int G, bool KTAIL, bool SALIGN, int EPI, int MB>
 __global__ void __launch_bounds__(kThreads)
 gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
             int M, int N, int K, int tiles_m, int tiles_n, int iters, int rounds, int sk_tiles, int nsk,
             float* __restrict__ partials, uint32_t* __restrict__ flags, uint32_t* __restrict__ counters,
             uint32_t* __restrict__ status, uint16_t* __restrict__ z) {
+  constexpr int kMB = MB, BM = 32 * MB, kABytes = BM * BK * 2, kStageBytes = kABytes + kBBytes;
+  constexpr size_t kPartialBytes = partial_bytes(MB);
   constexpr int kGroups = BK / G;            // scale groups per K step (1 or 4)
   // A SwiGLU product with one scale group per step runs its MFMAs on the codes, and adds each
   // step's results, times the column's scale, to a second set of sums: two more VALU per MFMA
@@ -231,7 +241,8 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   // rows of 2048 -> 512, 339 against 277 at 4096 -> 4096; weights there stay fp16(q s).)
   constexpr bool kCodes = EPI != kEpiProduct && G == BK;
   constexpr int kSBytes = SALIGN ? 0 : BN * kGroups * 4;       // per-stage scales (unaligned case)
-  constexpr int kStage = kStageBytes + kSBytes;
+  constexpr int kEpilogueBytes = kWaves * 64 * (kWaveN * 2 + 16);         // z slabs, in stage 2
+  constexpr int kStage = kStageBytes + kSBytes > kEpilogueBytes ? kStageBytes + kSBytes : kEpilogueBytes;
   // one array per stage, so the compiler tracks loads into one stage apart
   // from reads of another
   __shared__ __attribute__((aligned(16))) uint8_t stage0[kStage];
@@ -342,6 +353,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
     uint8_t* base = stage(st);
     if (p < 4) {
       const int j = p;
+      if (j >= MB) return;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xres, W4A16_LDS(base + (32 * j + 4 * wave) * 256), 16,
                                                (tail && !a_tail_ok) ? kOutOfRange : a_v,
                                                (uint32_t)(it.m0 + 32 * j) * kbytes + (uint32_t)kt * (BK * 2), 0, 0);
@@ -515,9 +527,9 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
 #pragma unroll
           for (int nb = 0; nb < kNB; ++nb)
             gscale[nb] = kCodeUnit * (float)__builtin_bit_cast(_Float16, (uint16_t)sc[0][nb]);
-          schedule_group_substep();
+          schedule_group_substep<MB>();
         } else {
-          schedule_substep();
+          schedule_substep<MB>();
         }
       }
       // operands of the next step's first two sub-steps
@@ -570,13 +582,13 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
       // column li of each block, rows 8 * (r / 4) + 4 * h + r % 4.
       constexpr int kPitch = kWaveN * 2 + 16;
       constexpr int kRowLanes = kWaveN / 8;      // lanes per output row, 16 bytes each
-      static_assert(kWaves * 64 * kPitch <= kStageBytes, "epilogue slabs exceed stage 2");
+      static_assert(kWaves * 64 * kPitch <= kStage, "epilogue slabs exceed stage 2");
       uint8_t* ep = stage2 + wave * 64 * kPitch;
       uint8_t* ew = ep + 4 * h * kPitch + li * 2;
       // the product itself: y, or the kept intermediate z
       uint16_t* const prod = EPI == kEpiProduct ? y : z;
 #pragma unroll
-      for (int pass = 0; pass < (EPI == kEpiSwiglu ? 0 : 2); ++pass) {
+      for (int pass = 0; pass < (EPI == kEpiSwiglu ? 0 : MB / 2); ++pass) {
 #pragma unroll
         for (int ii = 0; ii < 2; ++ii)
 #pragma unroll
@@ -617,11 +629,11 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
       }
       if constexpr (EPI != kEpiProduct) {
         // SiLU(gate) up: 16 outputs per row and wave, [row][16 columns] with a
-        // 48-byte row pitch, the wave's 128 rows in one pass
+        // 48-byte row pitch, the wave's rows in one pass
         constexpr int kHPitch = kWaveN + 16;
-        static_assert(kWaves * 128 * kHPitch <= kStageBytes, "SwiGLU slabs exceed stage 2");
+        static_assert(kWaves * BM * kHPitch <= kStage, "SwiGLU slabs exceed stage 2");
         const bool odd = li & 1;
-        uint8_t* hp = stage2 + wave * 128 * kHPitch;
+        uint8_t* hp = stage2 + wave * BM * kHPitch;
         uint8_t* hw = hp + (4 * h + (odd ? 1 : 0)) * kHPitch + (li >> 1) * 2;
         const int No = N >> 1;
         if constexpr (EPI == kEpiSwigluKeep) lds_barrier();   // another wave's z slab overlaps this wave's h slab
@@ -633,14 +645,14 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
                 float_to_half_bits(swiglu_pair(acc[i][0][r], acc[i][0][r + 1], odd));
         if ((No & 7) != 0) {      // unaligned rows: four rows of sixteen elements per store
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < 8 * MB; ++j) {
             const int row = 4 * j + (lane >> 4), m = m0 + row, n = (nw >> 1) + (lane & 15);
             const uint16_t v = *reinterpret_cast<const uint16_t*>(hp + row * kHPitch + 2 * (lane & 15));
             if (m < M && n < No) y[(size_t)m * No + n] = v;
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < MB; ++j) {
             const int row = 32 * j + (lane >> 1), c = lane & 1;
             const u32x4 v = *reinterpret_cast<const u32x4*>(hp + row * kHPitch + c * 16);
             const int m = m0 + row, n = (nw >> 1) + 8 * c;
@@ -780,12 +792,16 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   }
 }
 
+constexpr int swiglu_quads(int mb) { return mb * kNB * 4 * kThreads; }
+
 // Joins the split tiles of the SwiGLU product: one thread per 16-byte quad (four rows of
 // a column), the parts added in contributor order, gate and up in neighbouring lanes.
-constexpr int kQuads = kMB * kNB * 4 * kThreads;
+template <int MB>
 __global__ void __launch_bounds__(256)
 swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, uint16_t* __restrict__ z, int M, int N,
                    SplitPlan plan) {
+  constexpr int BM = 32 * MB, kQuads = swiglu_quads(MB);
+  constexpr size_t kPartialBytes = partial_bytes(MB);
   const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
   const Contributors cs(plan, tile);
   const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
@@ -860,7 +876,7 @@ size_t gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int, const DeviceIn
 }
 
 namespace {
-template <int EPI>
+template <int EPI, int MB>
 hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
                       int m, int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const GemmPlan p = EPI == kEpiProduct ? gemm_plan(m, n, k, dev) : swiglu_plan(m, n, k, dev);
@@ -879,35 +895,37 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
   }
   const bool tail = k % BK != 0;
   const bool salign = (k / group) % 8 == 0 && (reinterpret_cast<uintptr_t>(scales) & 15) == 0;
-  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true, EPI> : gemm_kernel<128, false, false, EPI>)
-              : tail       ? gemm_kernel<32, true, false, EPI>
-              : salign     ? gemm_kernel<32, false, true, EPI>
-                           : gemm_kernel<32, false, false, EPI>;
+  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true, EPI, MB> : gemm_kernel<128, false, false, EPI, MB>)
+              : tail       ? gemm_kernel<32, true, false, EPI, MB>
+              : salign     ? gemm_kernel<32, false, true, EPI, MB>
+                           : gemm_kernel<32, false, false, EPI, MB>;
   const hipError_t e =
       launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m, p.tiles_n,
                     p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
   if (EPI == kEpiProduct || e != hipSuccess || p.sk_tiles == 0) return e;
   const SplitPlan sp = {p.tiles_m, p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
-  return launch_kernel(swiglu_join_kernel, dim3((unsigned)p.sk_tiles * (kQuads / 256)), dim3(256), 0, stream, partials,
-                       y, z, m, n, sp);
+  return launch_kernel(swiglu_join_kernel<MB>, dim3((unsigned)p.sk_tiles * (swiglu_quads(MB) / 256)), dim3(256), 0,
+                       stream, partials, y, z, m, n, sp);
 }
 }  // namespace
 
 hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                        int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
-  return launch_epi<kEpiProduct>(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream);
+  return launch_epi<kEpiProduct, kMB>(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream);
 }
 
 size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev) {
   const GemmPlan p = swiglu_plan(m, 2 * n_out, k, dev);
-  return p.sk_tiles ? kCounterBytes + 2 * (size_t)p.wgs * kPartialBytes : 0;
+  return p.sk_tiles ? kCounterBytes + 2 * (size_t)p.wgs * partial_bytes(swiglu_blocks(m)) : 0;
 }
 
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                               uint16_t* z, int m, int n_out, int k, int group, void* workspace,
                               const DeviceInfo& dev, hipStream_t stream) {
-  return z ? launch_epi<kEpiSwigluKeep>(x, packed, scales, y, z, m, 2 * n_out, k, group, workspace, dev, stream)
-           : launch_epi<kEpiSwiglu>(x, packed, scales, y, nullptr, m, 2 * n_out, k, group, workspace, dev, stream);
+  const bool two = swiglu_blocks(m) == 2;
+  auto launch = z ? (two ? launch_epi<kEpiSwigluKeep, 2> : launch_epi<kEpiSwigluKeep, kMB>)
+                  : (two ? launch_epi<kEpiSwiglu, 2> : launch_epi<kEpiSwiglu, kMB>);
+  return launch(x, packed, scales, y, z, m, 2 * n_out, k, group, workspace, dev, stream);
 }
 
 }  // namespace w4a16
