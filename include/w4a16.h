@@ -64,8 +64,10 @@ typedef enum {
   W4A16_ERR_HIP = 6,       /* the HIP runtime reported an error (launch or device query) */
   W4A16_ERR_RANGE = 7,     /* a value is out of range: a code outside [-8,7], a non-finite
                               weight, or a group scale that overflows fp16 */
-  W4A16_ERR_TIMEOUT = 8    /* reported by w4a16_gemm_workspace_status only: a split-K fix-up of
+  W4A16_ERR_TIMEOUT = 8,   /* reported by w4a16_gemm_workspace_status only: a split-K fix-up of
                               an earlier w4a16_gemm gave up waiting for a partial tile */
+  W4A16_ERR_OVERLAP = 9    /* an output (or the workspace) shares memory with an input or another
+                              output; checked by the feed-forward block's calls */
 } w4a16_status;
 
 /* Version of this ABI (W4A16_ABI_VERSION). */
@@ -212,8 +214,9 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * (a call is up to three kernels: not two host threads' calls on one stream),
  * also with the three operators below (not with w4a16_gemm, whose workspace is
  * laid out differently).  No call waits for another: calls on several streams
- * may run at once, each with a workspace of its own.  Errors as w4a16_gemm;
- * k == 0 writes zeros.
+ * may run at once, each with a workspace of its own.  Errors as w4a16_gemm, and
+ * W4A16_ERR_OVERLAP where y, gate_up or the workspace shares memory with another
+ * operand (as in the three operators below); k == 0 writes zeros.
  */
 w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                                uint16_t* gate_up, int64_t m, int64_t n, int64_t k, int32_t group, void* workspace,
@@ -233,8 +236,8 @@ size_t w4a16_gemm_swiglu_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_
  * product (there is no second layout).  Weights enter as fp16(s q), sums are fp32,
  * y is rounded once.  n is any size; n == 0 writes zeros, k == 0 is a no-op.  A
  * column k whose weights are all zero still carries an infinity or NaN of d, as
- * the formula does.  Workspace (w4a16_gemm_t_workspace_bytes) as for
- * w4a16_gemm_swiglu, errors as w4a16_gemm.
+ * the formula does.  Workspace (w4a16_gemm_t_workspace_bytes) and errors as for
+ * w4a16_gemm_swiglu.
  */
 w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int64_t m,
                           int64_t n, int64_t k, int32_t group, void* workspace, size_t workspace_bytes,
@@ -252,8 +255,9 @@ size_t w4a16_gemm_t_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t gro
  *
  * in fp32 with one rounding to fp16, and dx [m, k] = dgate_up . deq(W) (the product
  * of that fp16 output, as w4a16_gemm_t).  All fp16, 16-byte aligned; gradients that
- * need more range are scaled by the caller.  n == 0 writes zeros to dx, k == 0 only
- * dgate_up.  Workspace (w4a16_gemm_swiglu_backward_workspace_bytes) and errors as
+ * need more range are scaled by the caller.  dgate_up may not be gate_up, whole or
+ * in part: its pairs are read by several workgroups (W4A16_ERR_OVERLAP, as for dx over
+ * an input).  n == 0 writes zeros to dx, k == 0 only dgate_up.  Workspace (w4a16_gemm_swiglu_backward_workspace_bytes) and errors as
  * w4a16_gemm_t.
  */
 w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate_up, const uint32_t* packed,

@@ -79,7 +79,7 @@ for _name, (_res, _args) in SIGNATURES.items():
     _fn.argtypes = _args
     globals()[_name] = _fn
 
-OK, ERR_NULL, ERR_SHAPE, ERR_GROUP, ERR_ALIGN, ERR_WORKSPACE, ERR_HIP, ERR_RANGE, ERR_TIMEOUT = range(9)
+OK, ERR_NULL, ERR_SHAPE, ERR_GROUP, ERR_ALIGN, ERR_WORKSPACE, ERR_HIP, ERR_RANGE, ERR_TIMEOUT, ERR_OVERLAP = range(10)
 
 
 class W4A16Error(RuntimeError):
@@ -323,7 +323,8 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # threads on one stream must not share one).  A workspace begins with counters that are 0
 # between calls.  Under graph capture each call takes one from the graph's own pool and
 # clears its counters in the graph, so captured graphs share none.  A smallest call is bound
-# by what the host does before it launches, so the checks here walk the arguments once.
+# by what the host does before it launches, so the checks here walk the arguments once; memory
+# shared between an output and another operand is refused by the library (ERR_OVERLAP).
 # ---------------------------------------------------------------------------
 def _check_ffn(what, specs):
     """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""

@@ -137,6 +137,7 @@ const char* w4a16_status_str(int status) {
     case W4A16_ERR_HIP: return "W4A16_ERR_HIP: HIP runtime error";
     case W4A16_ERR_RANGE: return "W4A16_ERR_RANGE: value out of range";
     case W4A16_ERR_TIMEOUT: return "W4A16_ERR_TIMEOUT: a split-K fix-up gave up waiting; outputs were written as NaN";
+    case W4A16_ERR_OVERLAP: return "W4A16_ERR_OVERLAP: an output shares memory with an input or another output";
     default: return "W4A16: unknown status";
   }
 }

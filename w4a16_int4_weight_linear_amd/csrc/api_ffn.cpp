@@ -16,6 +16,7 @@ using w4a16::common_dense_checks;
 using w4a16::DeviceInfo;
 using w4a16::kMaxBufferBytes;
 using w4a16::kMaxDim;
+using w4a16::outputs_overlap;
 using w4a16::status_of;
 using w4a16::valid_group;
 
@@ -92,6 +93,9 @@ w4a16_status w4a16_gemm_t(const uint16_t* d, const uint32_t* packed, const uint1
   if (n == 0) return status_of(w4a16::launch_zero_fill(y, (size_t)(m * k), st));
   const size_t need = t_workspace_bytes(m, n, k, group, dev);
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (outputs_overlap({{y, 2 * m * k}, {workspace, (int64_t)need}},
+                      {{d, 2 * m * n}, {packed, n * (k / 2)}, {scales, 2 * n * (k / group)}}))
+    return W4A16_ERR_OVERLAP;
   return status_of(launch_t(d, packed, scales, y, m, n, k, group, need ? workspace : nullptr, dev, st));
 }
 
@@ -121,15 +125,19 @@ w4a16_status w4a16_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const 
     const hipError_t e = gate_up ? w4a16::launch_zero_fill(gate_up, (size_t)(2 * m * n), st) : hipSuccess;
     return status_of(e != hipSuccess ? e : w4a16::launch_zero_fill(y, (size_t)(m * n), st));
   }
+  const bool streams = (!gate_up && m <= 16) || swiglu_skinny(m, 2 * n, k, dev);
+  const size_t need = streams ? 0 : w4a16::gemm_swiglu_workspace_bytes((int)m, (int)n, (int)k, dev);
+  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (outputs_overlap({{y, 2 * m * n}, {gate_up, gate_up ? 4 * m * n : 0}, {workspace, (int64_t)need}},
+                      {{x, 2 * m * k}, {packed, n * k}, {scales, 4 * n * (k / group)}}))
+    return W4A16_ERR_OVERLAP;
   // up to 16 rows with nothing kept: the decode product (its kernels for 1-4 rows are faster)
   if (!gate_up && m <= 16) return w4a16_gemv_swiglu(x, packed, scales, y, m, n, k, group, stream);
-  if (swiglu_skinny(m, 2 * n, k, dev)) {
+  if (streams) {
     return status_of(gate_up ? w4a16::launch_swiglu_skinny_keep(x, packed, scales, y, gate_up, (int)m, (int)n, (int)k,
                                                                 group, dev, st)
                              : w4a16::launch_swiglu_skinny(x, packed, scales, y, (int)m, (int)n, (int)k, group, dev, st));
   }
-  const size_t need = w4a16::gemm_swiglu_workspace_bytes((int)m, (int)n, (int)k, dev);
-  if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
   return status_of(w4a16::launch_gemm_swiglu(x, packed, scales, y, gate_up, (int)m, (int)n, (int)k, group,
                                              need ? workspace : nullptr, dev, st));
 }
@@ -162,6 +170,9 @@ w4a16_status w4a16_gemm_swiglu_backward(const uint16_t* dy, const uint16_t* gate
   const bool product = n > 0 && k > 0;
   const size_t need = product ? t_workspace_bytes(m, 2 * n, k, group, dev) : 0;
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (outputs_overlap({{dgate_up, 4 * m * n}, {dx, 2 * m * k}, {workspace, (int64_t)need}},
+                      {{dy, 2 * m * n}, {gate_up, 4 * m * n}, {packed, n * k}, {scales, 4 * n * (k / group)}}))
+    return W4A16_ERR_OVERLAP;
   const bool few_rows = product && t_skinny(m, 2 * n, k, group, dev);
   if (few_rows && w4a16::swiglu_backward_skinny_fits((int)m, (int)(2 * n), (int)k, group, dev))
     return status_of(w4a16::launch_swiglu_backward_skinny(dy, gate_up, dgate_up, packed, scales, dx, (int)m,
@@ -207,6 +218,9 @@ w4a16_status w4a16_gemm_dscales(const uint16_t* d, const uint16_t* x, const uint
     return status_of(w4a16::launch_zero_fill(reinterpret_cast<uint16_t*>(dscales), (size_t)(2 * n * (k / group)), st));
   const size_t need = w4a16::dscales_workspace_bytes((int)m, (int)n, (int)k, group, dev);
   if (need && (!workspace || workspace_bytes < need)) return W4A16_ERR_WORKSPACE;
+  if (outputs_overlap({{dscales, 4 * n * (k / group)}, {workspace, (int64_t)need}},
+                      {{d, 2 * m * n}, {x, 2 * m * k}, {packed, n * (k / 2)}}))
+    return W4A16_ERR_OVERLAP;
   return status_of(w4a16::launch_dscales(d, x, packed, dscales, (int)m, (int)n, (int)k, group,
                                          need ? workspace : nullptr, dev, st));
 }

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/w4a16.h"
 
 namespace w4a16 {
@@ -29,6 +31,30 @@ inline int common_dense_checks(const uint16_t* x, const uint32_t* packed, const 
   if (n * (k / 2) >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
   if (2 * m * k >= kMaxBufferBytes || 2 * m * n >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
   return W4A16_OK;
+}
+
+// One operand's bytes (none: a pointer that is not looked at).
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.bytes > 0 && b.bytes > 0 && (x < y ? y - x < (uintptr_t)a.bytes : x - y < (uintptr_t)b.bytes);
+}
+
+// Whether what a call writes shares memory with what it reads, or two of the things it writes
+// with each other: workgroups read an input while others already store, so the results would
+// depend on timing.
+inline bool outputs_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    for (auto b = o + 1; b != outputs.end(); ++b)
+      if (overlap(*o, *b)) return true;
+    for (const Span& i : inputs)
+      if (overlap(*o, i)) return true;
+  }
+  return false;
 }
 
 inline w4a16_status status_of(hipError_t e) { return e == hipSuccess ? W4A16_OK : W4A16_ERR_HIP; }
