@@ -35,3 +35,8 @@ def test_dispatch_and_shared_memory(tmp_path):
 
 def test_overlap_is_a_status_of_its_own():
     assert w4.ERR_OVERLAP == 9 and b"OVERLAP" in w4.lib.w4a16_status_str(w4.ERR_OVERLAP)
+
+
+def test_a_workspace_is_device_memory():
+    with pytest.raises(ValueError, match="HIP device"):
+        w4.ffn_workspace("gemm_t", 1, 1024, 1024, 128, device="cpu")

@@ -55,3 +55,69 @@ def test_shared_memory_is_refused(w4, m):
     got = w4.gemm_swiglu_backward(dh, z, p, s, g, dgate_up=view(size, m, 2 * n), out=view(2 * size, m, k))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def busy(torch, work, times=12):
+    """Some milliseconds of work on the current stream."""
+    for _ in range(times):
+        work[0] = work[0] @ work[1]
+
+
+@pytest.mark.parametrize("drop", [False, True])
+def test_workspace_used_on_another_stream_at_once(w4, drop):
+    """Made behind other work on one stream, in memory that held other values, and used at once on a second
+    stream by a call whose workgroups count their arrivals in it; then dropped while that call still waits,
+    with its memory asked for again on the first stream."""
+    torch = torch_mod()
+    m, n, k, g = 1, 1024, 1024, 128
+    rng = np.random.default_rng(62000)
+    p, s = dev(w4.pack(synth.code_bank(rng, 1, n, k)[0])), dev(synth.scale_bank(rng, 1, n, k // g)[0])
+    d = dev(synth.activations(rng, m, n))
+    want = w4.gemm_t(d, p, s, g)
+    first, second = torch.cuda.Stream(), torch.cuda.Stream()
+    work = [torch.zeros((8192, 8192), dtype=torch.float16, device="cuda") for _ in range(4)]
+    words = w4.ffn_workspace("gemm_t", m, n, k, g).numel()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(first):
+            used = torch.full((words,), -1, dtype=torch.int32, device="cuda")
+            busy(torch, work[:2])
+            del used                                   # its memory goes to the next request on this stream
+        ws = w4.ffn_workspace("gemm_t", m, n, k, g, stream=first)
+        with torch.cuda.stream(second):
+            busy(torch, work[2:])
+        out = torch.full_like(want, float("nan"))
+        second.wait_stream(torch.cuda.current_stream())
+        w4.gemm_t(d, p, s, g, out=out, workspace=ws, stream=second)
+        if drop:
+            del ws
+            with torch.cuda.stream(first):
+                taken = torch.full((words,), -1, dtype=torch.int32, device="cuda")
+        else:
+            w4.gemm_t(d, p, s, g, workspace=ws, stream=second)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        if drop:
+            assert bool((taken == -1).all())
+        else:
+            assert int(ws[:4096].abs().sum()) == 0
+
+
+def test_workspace_stream_and_device_agree(w4):
+    torch = torch_mod()
+    side = torch.cuda.Stream()
+    ws = w4.ffn_workspace("gemm_t", 1, 1024, 1024, 128, device=side.device, stream=side)
+    assert ws.device == side.device and int(ws[:4096].abs().sum()) == 0
+    assert w4.ffn_workspace("gemm_t", 1, 1024, 1024, 128, device="cuda").device == side.device
+    g = torch.cuda.CUDAGraph()
+    d = torch.ones((1, 1024), dtype=torch.float16, device="cuda")
+    p, s = torch.zeros((1024, 128), dtype=torch.int32, device="cuda"), torch.ones((1024, 8), dtype=torch.float16, device="cuda")
+    want = w4.gemm_t(d, p, s, 128)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):                          # made and used within one capture
+        out = w4.gemm_t(d, p, s, 128, workspace=w4.ffn_workspace("gemm_t", 1, 1024, 1024, 128))
+    for _ in range(3):
+        out.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and float(out[0, 0]) == -8 * 1024

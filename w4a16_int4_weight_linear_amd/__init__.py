@@ -412,6 +412,8 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
     """The given workspace, or one for a call on stream `handle` of the current device: pointer, bytes, and the
     tensor, which the caller holds until it has launched."""
     if given is not None:
+        # it may be another stream's memory: not to be handed out again before this call is done
+        given.record_stream(_torch_preload.cuda.current_stream())
         return given.data_ptr(), given.numel() * 4, given
     nbytes = _ffn_workspace_bytes(entry, m, n, k, group, device.index)
     if nbytes == 0:
@@ -436,16 +438,32 @@ def _new_workspace(nbytes, device):
     return ws
 
 
-def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None):
+def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None, stream=None):
     """A workspace tensor for gemm_swiglu, gemm_swiglu_backward, gemm_t or gemm_dscales (`call` by name)
-    of these sizes (n as in the C ABI: outputs of the gated calls, else weight rows); None if none is needed."""
+    of these sizes (n as in the C ABI: outputs of the gated calls, else weight rows); None if none is needed.
+    It is allocated and cleared on `stream` (None: the device's current one), and the host waits for that, so
+    calls on any stream may use it (one after another; under graph capture, only calls of that capture that
+    are ordered behind this one)."""
     if call not in ("gemm_swiglu", "gemm_swiglu_backward", "gemm_t", "gemm_dscales"):
         raise ValueError(f"ffn_workspace: no workspace for {call!r}")
-    device = _torch_preload.device("cuda", _torch_preload.cuda.current_device()) if device is None \
-        else _torch_preload.device(device)
-    with _torch_preload.cuda.device(device):
+    cuda = _torch_preload.cuda
+    device = _torch_preload.device(device) if device is not None else stream.device if stream is not None \
+        else _torch_preload.device("cuda")
+    if device.type != "cuda":
+        raise ValueError(f"ffn_workspace: a workspace lives on a HIP device, not on {device}")
+    if device.index is None:
+        device = _torch_preload.device("cuda", cuda.current_device())
+
+    def make(handle):
         nbytes = getattr(lib, f"w4a16_{call}_workspace_bytes")(m, n, k, group)
-        return _new_workspace(nbytes, device) if nbytes else None
+        if not nbytes:
+            return None
+        ws = _new_workspace(nbytes, device)
+        if not cuda.is_current_stream_capturing():
+            cuda.current_stream().synchronize()
+        return ws
+
+    return _launch_on("ffn_workspace", device, stream, make)
 
 
 def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace=None, stream=None):
