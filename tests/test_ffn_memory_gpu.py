@@ -121,3 +121,38 @@ def test_workspace_stream_and_device_agree(w4):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and float(out[0, 0]) == -8 * 1024
+
+
+@pytest.mark.parametrize("m", [2, 40])
+def test_operands_dropped_before_their_call_has_run(w4, m):
+    """Calls queued on a busy stream given by argument, every operand dropped at once and its memory filled
+    again on the stream it came from."""
+    torch = torch_mod()
+    n, k, g = 512, 1024, 128
+    rng = np.random.default_rng(63000 + m)
+    p, s = pair_weights(w4, rng, n, k, g)
+    x, dh = dev(synth.activations(rng, m, k)), dev(synth.activations(rng, m, n))
+    z = torch.empty((m, 2 * n), dtype=torch.float16, device="cuda")
+    h = w4.gemm_swiglu(x, p, s, g, gate_up=z)
+    dx, dz = w4.gemm_swiglu_backward(dh, z, p, s, g)
+    want = [h, dx, dz, w4.gemm_t(z, p, s, g), w4.gemm_dscales(z, x, p, g)]
+    side = torch.cuda.Stream()
+    work = [torch.zeros((8192, 8192), dtype=torch.float16, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            busy(torch, work)
+        got = []
+        copies = [t.clone() for t in (x, p, s, dh, z)]
+        side.wait_stream(torch.cuda.current_stream())
+        x2, p2, s2, dh2, z2 = copies
+        got.append(w4.gemm_swiglu(x2, p2, s2, g, gate_up=torch.empty_like(z), stream=side))
+        got.extend(w4.gemm_swiglu_backward(dh2, z2, p2, s2, g, stream=side))
+        got.append(w4.gemm_t(z2, p2, s2, g, stream=side))
+        got.append(w4.gemm_dscales(z2, x2, p2, g, stream=side))
+        sizes = [(t.numel(), t.dtype) for t in copies]
+        del copies, x2, p2, s2, dh2, z2
+        again = [torch.full((count,), -1, dtype=dtype, device="cuda") for count, dtype in sizes]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(bool((t == -1).all()) for t in again)

@@ -374,8 +374,9 @@ if _torch_preload is not None:
     _U32 = tuple(d for d in (_torch_preload.int32, getattr(_torch_preload, "uint32", None)) if d is not None)
 
 
-def _launch_on(what, device, stream, call):
-    """call(handle) with `device` and `stream` (None: the device's current one) current."""
+def _launch_on(what, device, stream, call, specs=()):
+    """call(handle) with `device` and `stream` (None: the device's current one) current.  The memory of the
+    operands in specs is held until the call has run on a stream given, which need not be theirs."""
     cuda = _torch_preload.cuda
     if stream is None:
         if device.index == cuda.current_device():
@@ -384,6 +385,8 @@ def _launch_on(what, device, stream, call):
             return call(_current_handle(device.index))
     if stream.device != device:
         raise ValueError(f"{what}: the stream is on {stream.device}, the tensors on {device}")
+    for _, t, _, _ in specs:
+        t.record_stream(stream)
     with cuda.stream(stream):
         return call(stream.cuda_stream)
 
@@ -494,7 +497,7 @@ def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace
                                      0 if gate_up is None else gate_up.data_ptr(), m, n, k, group, ws, nbytes, handle),
                "w4a16_gemm_swiglu")
 
-    _launch_on(what, device, stream, call)
+    _launch_on(what, device, stream, call, specs)
     return out
 
 
@@ -519,7 +522,7 @@ def gemm_t(d, packed, scales, group: int, out=None, workspace=None, stream=None)
         _check(lib.w4a16_gemm_t(d.data_ptr(), packed.data_ptr(), scales.data_ptr(), out.data_ptr(), m, n, k, group,
                                 ws, nbytes, handle), "w4a16_gemm_t")
 
-    _launch_on(what, device, stream, call)
+    _launch_on(what, device, stream, call, specs)
     return out
 
 
@@ -557,7 +560,7 @@ def gemm_swiglu_backward(dy, gate_up, packed, scales, group: int, out=None, dgat
                                               dgate_up.data_ptr(), out.data_ptr(), m, n, k, group, ws, nbytes,
                                               handle), "w4a16_gemm_swiglu_backward")
 
-    _launch_on(what, device, stream, call)
+    _launch_on(what, device, stream, call, specs)
     return out, dgate_up
 
 
@@ -582,7 +585,7 @@ def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None
         _check(lib.w4a16_gemm_dscales(d.data_ptr(), x.data_ptr(), packed.data_ptr(), out.data_ptr(), m, n, k, group,
                                       ws, nbytes, handle), "w4a16_gemm_dscales")
 
-    _launch_on(what, device, stream, call)
+    _launch_on(what, device, stream, call, specs)
     return out
 
 
