@@ -33,6 +33,7 @@
 // * Measured slower: a ring of units through LDS-direct loads (0.3-1.7 us), workgroups of 256 or
 //   1024 threads, 33-64 rows here instead of on the tiles (74 against 46 us, 17408 -> 5120).
 #include "device.hpp"
+#include "gemm_t_skinny_plan.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
 #include "swiglu_grad.hpp"
@@ -40,25 +41,10 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
-constexpr int kUnit = 32;                       // n per unit
-constexpr int CW = 256;                         // columns per strip
+using namespace skinny_t;
+
 constexpr int kWords = CW / 128;                // words per lane and row
 constexpr int kF = CW / 16;                     // operands (columns) per lane and unit
-
-struct SkinnyPlan {
-  int strips, splits, units, range;             // strips of CW columns, ranges of n, units of 32 n, n per range
-  uint32_t lds;
-  bool fused;                                   // the strips' last workgroups add the ranges' sums
-};
-
-// Rows (ranges x rows of d, 1 KB each) that a strip's last workgroup adds at most.  Measured,
-// last workgroup against second kernel, device time: 1 row 1024 -> 1024 (4 rows) 6.8 / 7.4 us,
-// 1 row through a 1024 x 2048 pair (4) 9.1 / 9.6, 1 row 17408 -> 5120 (25) 19.0 / 18.3, 19 rows
-// through the pair (76) 14.3 / 12.3, 16 rows 17408 -> 5120 (400) 27.3 / 21.3; the second launch
-// also takes 2.3 us of the host's time per call, which is what bounds the small ones.
-constexpr int kJoinRows = 16;
 
 // Units per wave up to which every strip makes the pairs' gradient for itself (GRAD); past that
 // the elementwise kernel runs first, as its one pass costs less than the strips' repeated work.
@@ -67,13 +53,6 @@ constexpr int kJoinRows = 16;
 // (4) 15.3 / 15.7, 32 rows 24576 x 2048 (3) 20.6 / 21.5, 1 row 34816 x 5120 (12) 30.3 / 27.5, 32
 // rows 47.1 / 39.4; it also saves 2.7 us of the host's time per call.
 constexpr int kGradUnits = 4;
-
-// Rows of d summed over the waves at a time: 128 KB of LDS.
-__host__ __device__ constexpr int red_rows(int) { return 16; }
-// floats of one wave's sums in that buffer (whole quads of rows)
-__host__ __device__ constexpr int red_stride(int m, int mb) {
-  return (m < red_rows(mb) ? (m + 3) / 4 * 4 : red_rows(mb)) * CW;
-}
 
 // The same four columns of two neighbouring n.
 __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
@@ -386,26 +365,6 @@ gemm_t_skinny_join_kernel(const float* __restrict__ partials, uint16_t* __restri
   *reinterpret_cast<uint32_t*>(y + i) = (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
 }
 
-constexpr size_t kMaxSums = (size_t)256 << 20;   // bytes of the ranges' sums, at most
-
-int blocks_of(int m) { return m <= 16 ? 1 : 2; }
-
-SkinnyPlan skinny_plan(int m, int n, int k, int group, const DeviceInfo& dev) {
-  const int mb = blocks_of(m);
-  SkinnyPlan p;
-  p.strips = (k + CW - 1) / CW;
-  p.units = (n + kUnit - 1) / kUnit;
-  const int slots = dev.num_cu;
-  int splits = slots / p.strips;
-  if (splits > (p.units + kWaves - 1) / kWaves) splits = (p.units + kWaves - 1) / kWaves;
-  if (splits < 1) splits = 1;
-  p.range = ((p.units + splits - 1) / splits) * kUnit;
-  p.splits = (n + p.range - 1) / p.range;
-  p.fused = p.splits > 1 && p.splits * m <= kJoinRows && p.strips <= kCounters;
-  p.lds = (uint32_t)(kWaves * red_stride(m, mb) * 4);
-  return p;
-}
-
 template <int G>
 auto kernel_of(int m, int n, bool grad) {
   const bool one = blocks_of(m) == 1;
@@ -433,14 +392,12 @@ hipError_t launch_any(const uint16_t* d, const uint16_t* gate_up, uint16_t* dgat
 }  // namespace
 
 size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
-  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  return p.splits > 1 ? kCounterBytes + (size_t)p.splits * m * k * 4 : 0;
+  const size_t sums = sums_bytes(skinny_plan(m, n, k, group, dev), m, k);
+  return sums ? kCounterBytes + sums : 0;
 }
 
 bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
-  if (m > kSkinnyTRows) return false;
-  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
-  return p.lds + 8192 <= dev.max_lds && (p.splits == 1 || (size_t)p.splits * m * k * 4 <= kMaxSums);
+  return m <= kSkinnyTRows && plan_fits(skinny_plan(m, n, k, group, dev), m, k, dev);
 }
 
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
