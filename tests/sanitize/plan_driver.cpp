@@ -39,6 +39,7 @@ static void walk(int tiles_m, int tiles_n, int iters, const SplitCost& cost, int
   ++g_plans;
   const int tiles = tiles_m * tiles_n;
   EXPECT(p.wgs >= kXCD && p.wgs % kXCD == 0 && p.nsk * kXCD <= p.wgs && (p.nsk > 0) == (p.sk_tiles > 0));
+  EXPECT(split_slots(p) == (p.sk_tiles ? (size_t)16 * p.nsk : 0));
   const int rows = 16, cols = 32;
   std::vector<int> next(tiles, 0), owner(tiles, -1);
   struct Part { int tile, a, b, slot; };
@@ -53,6 +54,7 @@ static void walk(int tiles_m, int tiles_n, int iters, const SplitCost& cost, int
       const int tile = it.r0 / rows * tiles_n + it.c0 / cols;
       if (i < wr.n_seg) {
         parts.push_back({tile, it.a, it.b, 2 * wg + i});
+        EXPECT((size_t)(2 * wg + i) < split_slots(p));
       } else {
         EXPECT(it.a == 0 && it.b == iters && owner[tile] < 0);
         owner[tile] = wg;

@@ -156,3 +156,33 @@ def test_operands_dropped_before_their_call_has_run(w4, m):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(bool((t == -1).all()) for t in again)
+
+
+# split tiles on few workgroups: (call, m, n, k, group), n as ffn_workspace takes it, and the plan's sizes: tiles of
+# the product, steps per tile, fewest steps of a part, fp32 values of a partial tile
+SPLIT = [("gemm_t", 64, 768, 1024, 128, 4, 12, 4, 256 * 256), ("gemm_t", 300, 2003, 2080, 32, 18, 32, 4, 256 * 256),
+         ("gemm_swiglu", 64, 256, 1024, 128, 2, 8, 3, 64 * 256), ("gemm_swiglu_backward", 70, 300, 544, 32, 3, 10, 4, 256 * 256),
+         ("gemm_dscales", 512, 1024, 1024, 128, 16, 16, 4, 256 * 2)]
+
+
+@pytest.mark.parametrize("call,m,n,k,g,tiles,steps,least,tile", SPLIT)
+def test_workspace_is_as_large_as_its_split(w4, call, m, n, k, g, tiles, steps, least, tile):
+    """No larger than the partial tiles of the workgroups that split tiles, and nothing behind it is written."""
+    torch = torch_mod()
+    rng = np.random.default_rng(64000 + m + n)
+    rows = 2 * n if "swiglu" in call else n
+    p, s = dev(w4.pack(synth.code_bank(rng, 1, rows, k)[0])), dev(synth.scale_bank(rng, 1, rows, k // g)[0])
+    x, d, dh = (dev(synth.activations(rng, m, c)) for c in (k, rows, n))
+    run = {"gemm_t": lambda **kw: w4.gemm_t(d, p, s, g, **kw), "gemm_swiglu": lambda **kw: w4.gemm_swiglu(x, p, s, g, **kw),
+           "gemm_swiglu_backward": lambda **kw: w4.gemm_swiglu_backward(dh, d, p, s, g, **kw)[0],
+           "gemm_dscales": lambda **kw: w4.gemm_dscales(d, x, p, g, **kw)}[call]
+    words = w4.ffn_workspace(call, m, n, k, g).numel()
+    buf = torch.full((words + 65536,), 77, dtype=torch.int32, device="cuda")
+    ws = buf[:words]
+    ws[:4096] = 0
+    want = run()
+    assert torch.equal(run(workspace=ws), want) and bool((buf[words:] == 77).all())
+    # two places for each workgroup that may split: of the 8 dies, each with its share of the tiles, one per `least` steps;
+    # behind them a left side with padded rows
+    per_die = min(32, -(-tiles // 8) * steps // least)
+    assert words <= 4096 + 16 * per_die * tile + m * (rows + 8) // 2 + 64

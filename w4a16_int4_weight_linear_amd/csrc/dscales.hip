@@ -328,7 +328,7 @@ size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) 
 
 size_t dscales_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  const size_t bytes = pad_bytes(m, n) + (p.sk_tiles ? 2 * (size_t)p.wgs * BN * (BC / group) * 4 : 0);
+  const size_t bytes = pad_bytes(m, n) + split_slots(p) * BN * (BC / group) * 4;
   return bytes ? kCounterBytes + bytes : 0;
 }
 

@@ -153,6 +153,8 @@ GemmPlan swiglu_plan(int m, int n, int k, const DeviceInfo& dev) {
   return {p.tiles_m, p.tiles_n, p.tiles_m * p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
 }
 
+SplitPlan split_of(const GemmPlan& p) { return {p.tiles_m, p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk}; }
+
 // Order of one MFMA sub-step's instructions: each of its 4 MFMAs is
 // followed by up to five VALU instructions (the dequantisation of the next
 // sub-step) and by one LDS read (operands two sub-steps ahead) and one global
@@ -903,9 +905,8 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
       launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m, p.tiles_n,
                     p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
   if (EPI == kEpiProduct || e != hipSuccess || p.sk_tiles == 0) return e;
-  const SplitPlan sp = {p.tiles_m, p.tiles_n, p.iters, p.wgs, p.rounds, p.sk_tiles, p.nsk};
   return launch_kernel(swiglu_join_kernel<MB>, dim3((unsigned)p.sk_tiles * (swiglu_quads(MB) / 256)), dim3(256), 0,
-                       stream, partials, y, z, m, n, sp);
+                       stream, partials, y, z, m, n, split_of(p));
 }
 }  // namespace
 
@@ -916,7 +917,7 @@ hipError_t launch_gemm(const uint16_t* x, const uint32_t* packed, const uint16_t
 
 size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& dev) {
   const GemmPlan p = swiglu_plan(m, 2 * n_out, k, dev);
-  return p.sk_tiles ? kCounterBytes + 2 * (size_t)p.wgs * partial_bytes(swiglu_blocks(m)) : 0;
+  return p.sk_tiles ? kCounterBytes + split_slots(split_of(p)) * partial_bytes(swiglu_blocks(m)) : 0;
 }
 
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,

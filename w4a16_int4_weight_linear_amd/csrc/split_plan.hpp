@@ -76,6 +76,9 @@ inline SplitPlan split_plan(int tiles_m, int tiles_n, int iters, const SplitCost
   return p;
 }
 
+// Places for partial tiles: two for each workgroup that may have split tiles (l < nsk of every XCD).
+inline size_t split_slots(const SplitPlan& p) { return 2 * (size_t)p.nsk * kXCD; }
+
 W4A16_HD inline int xcd_begin(int xcd, int count) {
   const int q = count / kXCD, r = count % kXCD;
   return xcd * q + (xcd < r ? xcd : r);
