@@ -186,3 +186,22 @@ def test_workspace_is_as_large_as_its_split(w4, call, m, n, k, g, tiles, steps, 
     # behind them a left side with padded rows
     per_die = min(32, -(-tiles // 8) * steps // least)
     assert words <= 4096 + 16 * per_die * tile + m * (rows + 8) // 2 + 64
+
+
+def test_kept_workspaces_are_bounded_and_released(w4):
+    torch = torch_mod()
+    d = torch.ones((1, 1024), dtype=torch.float16, device="cuda")
+    p, s = torch.zeros((1024, 128), dtype=torch.int32, device="cuda"), torch.ones((1024, 8), dtype=torch.float16, device="cuda")
+    want = w4.gemm_t(d, p, s, 128)
+    torch.cuda.synchronize()
+    # more handles than torch's pool of streams has, as a program with streams of its own may use
+    kept = w4._FFN_WORKSPACES.of
+    for i in range(100):
+        kept[(0, -1 - i)] = kept[(0, torch.cuda.current_stream().cuda_stream)]
+    side = torch.cuda.Stream()
+    assert torch.equal(w4.gemm_t(d, p, s, 128, stream=side), want)
+    assert len(kept) <= 32 and (0, side.cuda_stream) in kept
+    side.synchronize()
+    w4.ffn_release_workspaces()
+    assert not kept
+    assert torch.equal(w4.gemm_t(d, p, s, 128), want)

@@ -17,6 +17,7 @@ import ctypes
 import functools
 import os
 import threading
+import weakref
 
 import numpy as np
 
@@ -318,7 +319,8 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # The feed-forward block for any number of rows, with its backward pass.
 #
 # These calls run on the tensors' own device whichever is current, allocate on
-# the stream they launch on, and keep one workspace per host thread, device and stream,
+# the stream they launch on, and keep one workspace per host thread, device and stream (of the
+# last 32 streams, until ffn_release_workspaces),
 # grown to the largest size asked for (a call is up to three kernels, so the calls of two
 # threads on one stream must not share one).  A workspace begins with counters that are 0
 # between calls.  Under graph capture each call takes one from the graph's own pool and
@@ -397,12 +399,28 @@ def _current_handle(index):
     return raw(index) if raw is not None else _torch_preload.cuda.current_stream(index).cuda_stream
 
 
+class _Kept(dict):
+    """One host thread's workspaces: (device index, stream handle) -> (pointer, bytes, tensor)."""
+    __hash__ = object.__hash__
+
+
 class _Workspaces(threading.local):
     def __init__(self):
-        self.of = {}
+        self.of = _Kept()
+        with _KEPT_LOCK:
+            _ALL_KEPT.add(self.of)
 
 
+_MOST_KEPT = 32              # per host thread: as many streams as torch's pool of them has on a device
+_ALL_KEPT, _KEPT_LOCK = weakref.WeakSet(), threading.Lock()
 _FFN_WORKSPACES = _Workspaces()
+
+
+def ffn_release_workspaces():
+    """Give back the workspaces that the feed-forward block's calls keep, every host thread's."""
+    with _KEPT_LOCK:
+        for kept in _ALL_KEPT:
+            kept.clear()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -427,8 +445,12 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
     key = (device.index, handle)
     kept = _FFN_WORKSPACES.of.get(key)
     if kept is None or kept[1] < nbytes:
+        of = _FFN_WORKSPACES.of
+        of.pop(key, None)
+        while len(of) >= _MOST_KEPT:          # the oldest (its memory is its stream's, whose later work is ordered)
+            of.pop(next(iter(of), None), None)
         ws = _new_workspace(nbytes, device)
-        kept = _FFN_WORKSPACES.of[key] = ws.data_ptr(), ws.numel() * 4, ws
+        kept = of[key] = ws.data_ptr(), ws.numel() * 4, ws
     return kept
 
 
@@ -691,4 +713,4 @@ __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "u
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
            "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t",
-           "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace"] + list(SIGNATURES)
+           "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace", "ffn_release_workspaces"] + list(SIGNATURES)
