@@ -116,7 +116,7 @@ static void skinny(int m, int64_t n64, int64_t k64, int cus) {
   const int n = (int)n64, k = (int)k64;
   std::snprintf(g_what, sizeof g_what, "skinny m %d n %d k %d, %d CUs", m, n, k, cus);
   const DeviceInfo dev = device(cus);
-  const SkinnyPlan p = skinny_plan(m, n, k, 32, dev);
+  const SkinnyPlan p = skinny_plan(m, n, k, dev);
   ++g_plans;
   EXPECT(p.strips >= 1 && (int64_t)p.strips * CW >= k && (int64_t)(p.strips - 1) * CW < k);
   EXPECT(p.splits >= 1 && p.range % kUnit == 0 && p.range >= kUnit);

@@ -322,13 +322,11 @@ SplitPlan plan_of(int m, int n, int k, const DeviceInfo& dev) {
   return split_plan((n + BN - 1) / BN, (k + BC - 1) / BC, (m + BR - 1) / BR, kCost, dev);
 }
 
-size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) * 2 + 255) & ~(size_t)255) : 0; }
-
 }  // namespace
 
 size_t dscales_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  const size_t bytes = pad_bytes(m, n) + split_slots(p) * BN * (BC / group) * 4;
+  const size_t bytes = padded_bytes(m, n) + split_slots(p) * BN * (BC / group) * 4;
   return bytes ? kCounterBytes + bytes : 0;
 }
 
@@ -342,7 +340,7 @@ hipError_t launch_dscales(const uint16_t* d, const uint16_t* x, const uint32_t* 
     if (e != hipSuccess) return e;
     d = reinterpret_cast<uint16_t*>(ws);
     pitch = (uint32_t)((n + 7) / 8 * 8) * 2u;
-    ws += pad_bytes(m, n);
+    ws += padded_bytes(m, n);
   }
   float* partials = p.sk_tiles ? reinterpret_cast<float*>(ws) : nullptr;
   const hipError_t e = launch_kernel(group == 128 ? dscales_kernel<128> : dscales_kernel<32>, dim3(p.wgs),

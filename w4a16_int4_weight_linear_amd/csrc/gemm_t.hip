@@ -428,13 +428,11 @@ SplitPlan plan_of(int m, int n, int k, const DeviceInfo& dev) {
   return split_plan((m + BM - 1) / BM, (k + BC - 1) / BC, (n + BR - 1) / BR, kCost, dev);
 }
 
-size_t pad_bytes(int m, int n) { return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) * 2 + 255) & ~(size_t)255) : 0; }
-
 }  // namespace
 
 size_t gemm_t_workspace_bytes(int m, int n, int k, const DeviceInfo& dev) {
   const SplitPlan p = plan_of(m, n, k, dev);
-  const size_t bytes = pad_bytes(m, n) + split_slots(p) * kPartialBytes;
+  const size_t bytes = padded_bytes(m, n) + split_slots(p) * kPartialBytes;
   return bytes ? kCounterBytes + bytes : 0;
 }
 
@@ -460,7 +458,7 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
     }
     d = reinterpret_cast<uint16_t*>(ws);
     pitch = (uint32_t)((n + 7) / 8 * 8) * 2u;
-    ws += pad_bytes(m, n);
+    ws += padded_bytes(m, n);
   }
   float* partials = p.sk_tiles ? reinterpret_cast<float*>(ws) : nullptr;
   hipError_t e = launch_kernel(group == 128 ? gemm_t_kernel<128> : gemm_t_kernel<32>, dim3(p.wgs), dim3(kThreads), 0,

@@ -262,57 +262,54 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     load_unit(u + kWaves, t);
   }
 
-  // ---- sums over the waves, 4 kR rows of d at a time: buffer [wave][4 kR rows][256 columns]
+  // ---- sums over the waves, 16 rows of d at a time: buffer [wave][16 rows][256 columns]
   // fp32, columns 16 li + f; 16-byte chunk j of a lane's columns at j ^ (li / 2 % 4) (bank
   // spread).  Accumulator r of lane (lq, li) is row 4 r + lq of its block.
   const __amdgpu_buffer_rsrc_t pres =
       make_rsrc(partials, plan.splits > 1 ? (uint32_t)plan.splits * (uint32_t)(M * K) * 4u : 0u);
   float* red = reinterpret_cast<float*>(smem);
-  constexpr int kR = red_rows(MB) / 4;
-  const int wstride = red_stride(M, MB);
+  const int wstride = red_stride(M);
 #pragma unroll
-  for (int b = 0; b < MB; ++b)
+  for (int b = 0; b < MB; ++b) {
+    const int row0 = 16 * b;
+    if (row0 >= M) break;
+    __syncthreads();
 #pragma unroll
-    for (int r0 = 0; r0 < 4; r0 += kR) {
-      const int row0 = 16 * b + 4 * r0;
-      if (row0 >= M) break;
-      __syncthreads();
+    for (int r = 0; r < 4; ++r) {
+      if (row0 + 4 * r >= M) break;
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        if (row0 + 4 * r >= M) break;
-#pragma unroll
-        for (int j = 0; j < kF / 4; ++j) {
-          const f32x4 v = {acc[b][4 * j][r0 + r], acc[b][4 * j + 1][r0 + r], acc[b][4 * j + 2][r0 + r],
-                           acc[b][4 * j + 3][r0 + r]};
-          *reinterpret_cast<f32x4*>(red + wave * wstride + (4 * r + lq) * CW + kF * li + 4 * (j ^ ((li >> 1) & 3))) = v;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int o = tid; o < 4 * kR * CW / 2; o += kThreads) {
-        const int q = o / (CW / 2), c = (o % (CW / 2)) * 2;
-        if (row0 + q >= M) break;
-        const int l = c / kF, f = c % kF;
-        const float* src = red + q * CW + kF * l + 4 * ((f >> 2) ^ ((l >> 1) & 3)) + (f & 3);
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float2 v = *reinterpret_cast<const float2*>(src + w * wstride);
-          s0 += v.x;
-          s1 += v.y;
-        }
-        const int m = row0 + q, k = c0 + c;
-        if (m < M && k < K) {
-          if (plan.splits == 1)
-            *reinterpret_cast<uint32_t*>(y + (size_t)m * K + k) =
-                (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
-          else
-            __builtin_amdgcn_raw_buffer_store_b64(
-                u32x2{__builtin_bit_cast(uint32_t, s0), __builtin_bit_cast(uint32_t, s1)}, pres,
-                (uint32_t)(m * K + k) * 4u, (uint32_t)split * (uint32_t)(M * K) * 4u, kDeviceScope);
-        }
+      for (int j = 0; j < kF / 4; ++j) {
+        const f32x4 v = {acc[b][4 * j][r], acc[b][4 * j + 1][r], acc[b][4 * j + 2][r],
+                         acc[b][4 * j + 3][r]};
+        *reinterpret_cast<f32x4*>(red + wave * wstride + (4 * r + lq) * CW + kF * li + 4 * (j ^ ((li >> 1) & 3))) = v;
       }
     }
+    __syncthreads();
+#pragma unroll
+    for (int o = tid; o < 16 * CW / 2; o += kThreads) {
+      const int q = o / (CW / 2), c = (o % (CW / 2)) * 2;
+      if (row0 + q >= M) break;
+      const int l = c / kF, f = c % kF;
+      const float* src = red + q * CW + kF * l + 4 * ((f >> 2) ^ ((l >> 1) & 3)) + (f & 3);
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(src + w * wstride);
+        s0 += v.x;
+        s1 += v.y;
+      }
+      const int m = row0 + q, k = c0 + c;
+      if (m < M && k < K) {
+        if (plan.splits == 1)
+          *reinterpret_cast<uint32_t*>(y + (size_t)m * K + k) =
+              (uint32_t)float_to_half_bits(s0) | ((uint32_t)float_to_half_bits(s1) << 16);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64(
+              u32x2{__builtin_bit_cast(uint32_t, s0), __builtin_bit_cast(uint32_t, s1)}, pres,
+              (uint32_t)(m * K + k) * 4u, (uint32_t)split * (uint32_t)(M * K) * 4u, kDeviceScope);
+      }
+    }
+  }
 
   // ---- ranges of n: the strip's last workgroup adds the ranges' sums in range order ----
   if (plan.splits == 1 || !plan.fused || !arrive_last(counters + strip, (uint32_t)plan.splits, &arrived)) return;
@@ -377,7 +374,7 @@ auto kernel_of(int m, int n, bool grad) {
 hipError_t launch_any(const uint16_t* d, const uint16_t* gate_up, uint16_t* dgate_up, const uint32_t* packed,
                       const uint16_t* scales, uint16_t* y, int m, int n, int k, int group, void* workspace,
                       const DeviceInfo& dev, hipStream_t stream) {
-  const SkinnyPlan p = skinny_plan(m, n, k, group, dev);
+  const SkinnyPlan p = skinny_plan(m, n, k, dev);
   float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
   uint32_t* counters = static_cast<uint32_t*>(workspace);
   auto kern = group == 128 ? kernel_of<128>(m, n, gate_up) : kernel_of<32>(m, n, gate_up);
@@ -392,12 +389,12 @@ hipError_t launch_any(const uint16_t* d, const uint16_t* gate_up, uint16_t* dgat
 }  // namespace
 
 size_t gemm_t_skinny_workspace_bytes(int m, int n, int k, int group, const DeviceInfo& dev) {
-  const size_t sums = sums_bytes(skinny_plan(m, n, k, group, dev), m, k);
+  const size_t sums = sums_bytes(skinny_plan(m, n, k, dev), m, k);
   return sums ? kCounterBytes + sums : 0;
 }
 
 bool gemm_t_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
-  return m <= kSkinnyTRows && plan_fits(skinny_plan(m, n, k, group, dev), m, k, dev);
+  return m <= kSkinnyTRows && plan_fits(skinny_plan(m, n, k, dev), m, k, dev);
 }
 
 hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
@@ -407,7 +404,7 @@ hipError_t launch_gemm_t_skinny(const uint16_t* d, const uint32_t* packed, const
 
 bool swiglu_backward_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
   return n % 8 == 0 && gemm_t_skinny_fits(m, n, k, group, dev) &&
-         skinny_plan(m, n, k, group, dev).range <= kGradUnits * kWaves * kUnit;
+         skinny_plan(m, n, k, dev).range <= kGradUnits * kWaves * kUnit;
 }
 
 hipError_t launch_swiglu_backward_skinny(const uint16_t* dh, const uint16_t* gate_up, uint16_t* dgate_up,

@@ -34,19 +34,14 @@ struct SkinnyPlan {
 // also takes 2.3 us of the host's time per call, which is what bounds the small ones.
 constexpr int kJoinRows = 16;
 
-// Rows of d summed over the waves at a time: 128 KB of LDS.
-W4A16_HD constexpr int red_rows(int) { return 16; }
-// floats of one wave's sums in that buffer (whole quads of rows)
-W4A16_HD constexpr int red_stride(int m, int mb) {
-  return (m < red_rows(mb) ? (m + 3) / 4 * 4 : red_rows(mb)) * CW;
-}
+// Floats of one wave's sums (whole quads of rows of d, a block of 16 rows at a time: 128 KB of LDS).
+W4A16_HD constexpr int red_stride(int m) { return (m < 16 ? (m + 3) / 4 * 4 : 16) * CW; }
 
 constexpr size_t kMaxSums = (size_t)256 << 20;   // bytes of the ranges' sums, at most
 
 inline int blocks_of(int m) { return m <= 16 ? 1 : 2; }
 
-inline SkinnyPlan skinny_plan(int m, int n, int k, int, const DeviceInfo& dev) {
-  const int mb = blocks_of(m);
+inline SkinnyPlan skinny_plan(int m, int n, int k, const DeviceInfo& dev) {
   SkinnyPlan p;
   p.strips = (k + CW - 1) / CW;
   p.units = (n + kUnit - 1) / kUnit;
@@ -57,7 +52,7 @@ inline SkinnyPlan skinny_plan(int m, int n, int k, int, const DeviceInfo& dev) {
   p.range = ((p.units + splits - 1) / splits) * kUnit;
   p.splits = (n + p.range - 1) / p.range;
   p.fused = p.splits > 1 && p.splits * m <= kJoinRows && p.strips <= kCounters;
-  p.lds = (uint32_t)(kWaves * red_stride(m, mb) * 4);
+  p.lds = (uint32_t)(kWaves * red_stride(m) * 4);
   return p;
 }
 

@@ -93,7 +93,11 @@ hipError_t launch_gemm_t(const uint16_t* d, const uint32_t* packed, const uint16
 // Where launch_gemm_t keeps d with rows padded to 8 elements (null: n is a multiple of 8 and d
 // is read in place).  A caller that has filled it passes d = null.
 uint16_t* gemm_t_padded(int n, void* workspace);
-// d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row.
+// d [m, n] copied to out [m, ceil(n / 8) * 8] with zeros behind each row; the copy's bytes in a
+// workspace (0: n is a multiple of 8 and d is read in place).
+inline size_t padded_bytes(int m, int n) {
+  return n % 8 ? (((size_t)m * ((n + 7) / 8 * 8) * 2 + 255) & ~(size_t)255) : 0;
+}
 hipError_t launch_pad_rows(const uint16_t* d, uint16_t* out, int m, int n, hipStream_t stream);
 
 // ---- the same product for few rows, weight-streaming (gemm_t_skinny.hip) ----
