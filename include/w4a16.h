@@ -203,8 +203,12 @@ w4a16_status w4a16_gemv_swiglu(const uint16_t* x, const uint32_t* packed, const 
  * (fp16 [m, 2n], 16-byte aligned, or NULL) receives the products themselves, each
  * rounded once, g of output i in column 2i and u in column 2i + 1: what
  * w4a16_gemm_swiglu_backward reads.  y is computed from the unrounded products.
- * Weights enter exactly on the tiles at group 128 and, with gate_up, on the
- * weight-streaming kernel; otherwise at worst as fp16(s q), as in w4a16_gemm.
+ * Weights enter exactly (while 8 s is below fp16's largest value) on the tiles at
+ * group 128 and, with gate_up, on the weight-streaming kernel; otherwise at worst as
+ * fp16(s q), as in w4a16_gemm.  So up to 32 rows y itself can differ in its last bits
+ * between a call with gate_up and one without (up to 16 rows another kernel runs).
+ * An infinite or NaN x leaves the outputs of its own row alone not finite; up to 32
+ * rows they may be NaN where the formula has an infinity.
  * m <= 16 without gate_up runs as w4a16_gemv_swiglu, other few rows on the
  * weight-streaming kernel (m <= 16, or m <= 32 and up to 32 MB of weights);
  * beyond, the tiled GEMM with a SwiGLU epilogue.

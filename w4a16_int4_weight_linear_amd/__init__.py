@@ -327,6 +327,9 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # clears its counters in the graph, so captured graphs share none.  A smallest call is bound
 # by what the host does before it launches, so the checks here walk the arguments once; memory
 # shared between an output and another operand is refused by the library (ERR_OVERLAP).
+# As everywhere in this module, autograd does not see the calls: results carry no history, whatever
+# requires_grad says of an operand.  A training program makes them inside the forward and backward
+# of a torch.autograd.Function of its own.
 # ---------------------------------------------------------------------------
 def _check_ffn(what, specs):
     """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""

@@ -22,8 +22,11 @@ using w4a16::valid_group;
 
 // Up to 16 rows the gate/up product is a weight stream: the weight-streaming kernel.  17 to 32
 // rows are two passes of it, side by side in one launch, or the tiles, whose fixed costs are
-// larger: weight-streaming against tiles, device time, 24 rows 2048 -> 2048 (4 MB of weights) 9.4 /
-// 14.1 us, 32 rows 4096 -> 4096 (17 MB) 17.5 / 20.8, 32 rows 5120 -> 17408 (89 MB) 59.9 / 44.0.
+// larger.  Weight-streaming against tiles, products kept, device time in us at group 128 (at group 32,
+// where only the first keeps products of exact weights): 16 rows 2048 -> 512 (5.3 / 13.1), 16 rows 5120 -> 17408
+// (89 MB of weights) 37.8 / 43.8 (48.6 / 55.1), 1 row 36.2 / 42.7 (44.9 / 51.5); 24 rows 2048 -> 1024
+// (2 MB) 5.6 / 12.9 (5.7 / 14.2), 32 rows 4096 -> 2048 (8 MB) 13.5 / 16.8 (13.9 / 18.0), 32 rows 5120 ->
+// 17408 61.1 / 45.6 (70.6 / 55.1).
 constexpr int64_t kSkinnyRows = 32;
 constexpr int64_t kSkinnyTwicePassBytes = (int64_t)32 << 20;
 

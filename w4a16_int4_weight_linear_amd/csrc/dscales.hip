@@ -18,15 +18,15 @@
 //   acc * code is summed over the 32 lanes of a block by halving (each exchange sums
 //   two rows and keeps one per lane: 2.4 operations per accumulator instead of 10),
 //   which leaves lane l rows 2 l and 2 l + 1 of the wave's 64 per half.
-// * Leftover tiles are split along m as in tile_gemm.hpp; a part is 256 x groups fp32
+// * Leftover tiles are split along m as in split_plan.hpp; a part is 256 x groups fp32
 //   (2 or 8 KB), and a second kernel adds the parts in order (adding them in the last
 //   contributor instead measured 6 us slower at 133 rows: its stores, its arrival and its
 //   loads each pay the device-scope latency in turn).  Sums are fp32 throughout, products
 //   of fp16 pairs exact; results do not depend on timing.
-// * Measured (MI355X): 2048 rows, 17408 x 5120 316 us = 1.16 PFLOP/s (8192 rows 1235 us), the
-//   rate of a large dense library product: bound by the matrix cores at the clock their power
-//   leaves; 133 rows, 1001 x 1120 11.4 us with the padding, one step's latency
-//   after another.
+// * Measured (MI355X; boxes differ): 2048 rows, 17408 x 5120 314-325 us = 1.12-1.16 PFLOP/s (8192 rows 1235
+//   us), the rate of a large dense library product: bound by the matrix cores at the clock their
+//   power leaves (MFMAs busy 60% of the time at 1.77 GHz); 133 rows, 1001 x 1120 11.4 us with the
+//   padding, one step's latency after another.
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"

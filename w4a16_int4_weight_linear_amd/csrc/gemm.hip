@@ -50,9 +50,10 @@
 //   run on the codes (kCodes).  Its split tiles are
 //   joined by a second, small kernel instead of the in-kernel fix-up: no workgroup
 //   waits for another (calls on several streams cannot hold each other up) and the
-//   workspace holds no state.  Measured, 5120 -> 17408: 512 rows 185-189 us (0.97
-//   PFLOP/s), 4096 rows 1245-1280 us (1.14-1.17; the best dense fp16
-//   library product measured beside it 1.16): bound by power.  256 x 256 tiles (eight waves of 128 x 64, or four of
+//   workspace holds no state.  Measured, 5120 -> 17408: 512 rows 185-190 us (0.97
+//   PFLOP/s), 4096 rows 1238-1280 us (1.14-1.18; the best dense fp16
+//   library product measured beside it 1.16): bound by power (MFMAs busy 44% and 60% of
+//   the time at 2.04 and 1.72 GHz).  256 x 256 tiles (eight waves of 128 x 64, or four of
 //   256 x 64 with half the VALU work per MFMA) took 1315-1324 us against 1340 before
 //   the codes, and 118 against 104 us at 256 rows.
 //

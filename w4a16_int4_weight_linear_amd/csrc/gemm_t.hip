@@ -27,11 +27,13 @@
 //   n (stream-K).  Partial tiles go to the workspace and a second, small kernel adds
 //   them in contributor order: no workgroup waits for another, so calls on several
 //   streams cannot hold each other up, and the workspace holds no state.
-// * Measured (MI355X): 4096 rows 17408 -> 5120 583-615 us (1.19-1.25 PFLOP/s; the best
-//   dense fp16 library product measured beside it reached 1.16); 512 rows 112 us; 300 rows 2003 -> 2080 16 us and 6
-//   for the join. Bound at many rows by power: MFMAs busy 60% of the time at 1.9 GHz (with
-//   scales of one bit, i.e. operands of few, the same code takes 6% less time); at few
-//   hundred rows by the steps' latency and the partial tiles' way through memory.
+// * Measured (MI355X; boxes differ): 4096 rows 17408 -> 5120 599-636 us with its join (1.15-1.22 PFLOP/s;
+//   the best dense fp16 library product measured beside it reached 1.16); 512 rows 109-120 us; 300
+//   rows 2003 -> 2080 25 us: padded rows 5, tiles 15, join 6.  Bound at many rows by power: MFMAs busy 69%
+//   of the time at 1.6 GHz (with scales of one bit, i.e. operands of few, the same code takes 6% less
+//   time); at few hundred rows by the steps' latency and the partial tiles' way through memory.
+//   A product whose tiles are all split (160 tiles: the backward pass at 2048 rows) reads 3.7 GB instead of
+//   0.84, as the workgroups of an XCD are at different places of the sum and share nothing in its L2.
 // * Measured slower: loads three steps ahead with a barrier inside the step (3%), no
 //   scheduling groups (1-2%), segments of fewer than four steps (kCost).
 #include "device.hpp"

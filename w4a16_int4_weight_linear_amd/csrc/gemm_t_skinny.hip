@@ -12,7 +12,9 @@
 // * Two words of neighbouring n give their nibble pairs by one byte permute per four
 //   columns; an AND-OR makes fp16 1024 + u or 64 + u of a pair, a packed subtraction the
 //   code and a packed multiplication by the two rows' scales the operand q s (rounded
-//   once, as in the GEMM).  Eight n of a column are exactly a lane's slice of
+//   once, as in the GEMM; exact weights, by a second MFMA on what the rounding leaves of a scale in two
+//   parts, would take 17.4 against 15.8 us at 1 row 17408 -> 5120, 22.4 / 20.9 at 16 rows 5120 -> 17408
+//   and 5.8 / 5.4 at 1 row 1024 -> 1024, for an error of 2.1e-4 instead of 2.7e-4).  Eight n of a column are exactly a lane's slice of
 //   v_mfma_f32_16x16x32_f16, so a unit is 16 such operands, each used by the one or two
 //   blocks of sixteen rows of d.
 // * A wave loads what a unit needs, weights, operands of d (already in MFMA layout) and
@@ -26,10 +28,11 @@
 //   its last workgroup, in range order (one launch; no workgroup waits for another), or,
 //   where that workgroup would have more than kJoinRows rows to add, by a second kernel on
 //   the whole device.  Results do not depend on timing.
-// * Measured (MI355X, weights from HBM): 1 row 17408 -> 5120 (46 MB) 15.5 us = 2.97 TB/s, 16
-//   rows 5120 -> 17408 19.8 us, 1 row 1024 -> 1024 5.4 us.  Bound by latency: with no loads
-//   at all the first takes 8.7 us (launch, start, joins), without the offset and scale
-//   arithmetic 13.9, without the sums over the waves 14.9.
+// * Measured (MI355X, device time in graph replays over 1 GB of weights in turn, i.e. from HBM): 1
+//   row 17408 -> 5120 (46 MB) 15.6-16.0 us = 2.9 TB/s, 16 rows 5120 -> 17408 20.9-21.2 us with its
+//   join, 1 row 1024 -> 1024 5.4 us.  Bound by latency: with no loads at all the first takes 8.7 us
+//   (launch, start, six units of arithmetic, joins), without the offset and scale arithmetic 13.9,
+//   without the sums over the waves 14.9; a wave loads its next unit only when it has used the last.
 // * Measured slower: a ring of units through LDS-direct loads (0.3-1.7 us), workgroups of 256 or
 //   1024 threads, 33-64 rows here instead of on the tiles (74 against 46 us, 17408 -> 5120).
 #include "device.hpp"

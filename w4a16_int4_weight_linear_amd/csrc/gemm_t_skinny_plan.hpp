@@ -27,11 +27,16 @@ struct SkinnyPlan {
   bool fused;                                   // the strips' last workgroups add the ranges' sums
 };
 
-// Rows (ranges x rows of d, 1 KB each) that a strip's last workgroup adds at most.  Measured,
-// last workgroup against second kernel, device time: 1 row 1024 -> 1024 (4 rows) 6.8 / 7.4 us,
-// 1 row through a 1024 x 2048 pair (4) 9.1 / 9.6, 1 row 17408 -> 5120 (25) 19.0 / 18.3, 19 rows
-// through the pair (76) 14.3 / 12.3, 16 rows 17408 -> 5120 (400) 27.3 / 21.3; the second launch
-// also takes 2.3 us of the host's time per call, which is what bounds the small ones.
+// Rows (ranges x rows of d, 1 KB each) that a strip's last workgroup adds at most.  Measured, last
+// workgroup against second kernel, device time in us (graph replays over 1 GB of weights in turn):
+// 1 row 5120 -> 17408 (3 rows) 16.7 / 17.5, 1 row 1024 -> 1024 (4) 5.4 / 6.0, 1 row through a 1024 x
+// 2048 pair (4) 6.8 / 7.6, 1 row 2048 -> 2048 (8) 6.3 / 6.7, 4 rows 5120 -> 17408 (12) 17.5 / 17.9, 1 row
+// 17408 -> 5120 (12) 15.7 / 15.6, 4 rows 1024 -> 1024 (16) 6.0 / 6.4, 1 row 4096 -> 4096 (16) 9.4 / 7.2,
+// 1 row 16384 -> 4096 (16) 13.9 / 12.8, 8 rows 1024 -> 1024 (32) 7.2 / 6.9, 4 rows 17408 -> 5120 (48)
+// 17.0 / 16.9, 19 rows through the pair (76) 12.1 / 10.5, 16 rows 17408 -> 5120 (192) 21.5 / 18.7.  The
+// second launch also takes 2.3 us of the host's time per call, which bounds small calls made one after
+// another (through the binding 7.8 us with one launch, 10.1 with two); in a graph twelve and more
+// ranges of one row lose up to 2 us by the rule.
 constexpr int kJoinRows = 16;
 
 // Floats of one wave's sums (whole quads of rows of d, a block of 16 rows at a time: 128 KB of LDS).
