@@ -205,3 +205,66 @@ def test_kept_workspaces_are_bounded_and_released(w4):
     w4.ffn_release_workspaces()
     assert not kept
     assert torch.equal(w4.gemm_t(d, p, s, 128), want)
+
+
+@pytest.mark.parametrize("m", [1, 20, 70])
+def test_no_input_features(w4, m):
+    """k == 0: empty sums, zeros; the pairs' gradient does not depend on k."""
+    torch = torch_mod()
+    n, g = 24, 32
+    f16 = dict(dtype=torch.float16, device="cuda")
+    p0, s0, x0 = torch.zeros((2 * n, 0), dtype=torch.int32, device="cuda"), torch.zeros((2 * n, 0), **f16), torch.zeros((m, 0), **f16)
+    z = torch.full((m, 2 * n), float("nan"), **f16)
+    h = w4.gemm_swiglu(x0, p0, s0, g, gate_up=z)
+    assert torch.equal(h, torch.zeros((m, n), **f16)) and torch.equal(z, torch.zeros((m, 2 * n), **f16))
+    rng = np.random.default_rng(65000 + m)
+    p, s = pair_weights(w4, rng, n, 32, g)
+    z, dh = dev(synth.activations(rng, m, 2 * n)), dev(synth.activations(rng, m, n))
+    want = w4.gemm_swiglu_backward(dh, z, p, s, g)[1]
+    dx, dz = w4.gemm_swiglu_backward(dh, z, p0, s0, g)
+    assert dx.shape == (m, 0) and torch.equal(dz, want)
+    assert w4.gemm_t(z, p0, s0, g).shape == (m, 0) and w4.gemm_dscales(z, x0, p0, g).shape == (2 * n, 0)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("m", [2, 150])
+def test_captured_on_a_forked_stream(w4, m):
+    """A capture that forks: one branch's calls on a stream given by argument, their inputs made (and dropped)
+    on the capturing stream, one of them with a workspace of its own."""
+    torch = torch_mod()
+    n, k, g = 512, 1024, 128
+    rng = np.random.default_rng(66000 + m)
+    p, s = pair_weights(w4, rng, n, k, g)
+    x, dh = dev(synth.activations(rng, m, k)), dev(synth.activations(rng, m, n))
+    side = torch.cuda.Stream()
+
+    def step(fork):
+        z = torch.empty((m, 2 * n), dtype=torch.float16, device="cuda")
+        h = w4.gemm_swiglu(x, p, s, g, gate_up=z)
+        twice = dh * 2
+        if fork:
+            side.wait_stream(torch.cuda.current_stream())
+            dx, dz = w4.gemm_swiglu_backward(twice, z, p, s, g, stream=side)
+            del twice
+            ws = w4.ffn_workspace("gemm_t", m, 2 * n, k, g)
+            t = w4.gemm_t(z, p, s, g, workspace=ws)
+            torch.cuda.current_stream().wait_stream(side)
+        else:
+            dx, dz = w4.gemm_swiglu_backward(twice, z, p, s, g)
+            t = w4.gemm_t(z, p, s, g)
+        return h, dx, dz, t
+
+    want = [t.clone() for t in step(False)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(True)
+    for rep in range(4):
+        x.copy_(torch.randn_like(x))
+        want = step(False)
+        for t in got:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), f"replay {rep}"
