@@ -70,6 +70,18 @@ typedef enum {
                               output; checked by the feed-forward block's calls */
 } w4a16_status;
 
+/* Activations of w4a16_linear (see there). */
+typedef enum {
+  W4A16_ACT_NONE = 0,
+  W4A16_ACT_RELU = 1,      /* max(z, 0); its slope at 0 is 0 */
+  W4A16_ACT_SILU = 2,      /* z / (1 + e^-z) */
+  W4A16_ACT_GELU = 3,      /* z Phi(z), Phi the normal distribution */
+  W4A16_ACT_GELU_TANH = 4  /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+} w4a16_activation;
+
+/* Types of the router's logits. */
+typedef enum { W4A16_F32 = 0, W4A16_F16 = 1 } w4a16_dtype;
+
 /* Version of this ABI (W4A16_ABI_VERSION). */
 int w4a16_abi_version(void);
 
@@ -291,6 +303,53 @@ w4a16_status w4a16_gemm_dscales(const uint16_t* d, const uint16_t* x, const uint
 size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
 
 /*
+ * The linear layer with what surrounds it folded into the product, any m >= 1:
+ *
+ *     z = x . deq(W)^T + bias,   y = act(z) + residual
+ *
+ * x [m, k], packed [n, k/8], scales [n, k/group], y [m, n] as for w4a16_gemm; bias fp16 [n] and
+ * residual fp16 [m, n] (each 16-byte aligned, or NULL: none); activation one of w4a16_activation.
+ * Bias, activation and residual are applied in fp32 to the fp32 sums, y is rounded once.  `pre` (fp16
+ * [m, n], 16-byte aligned, or NULL) receives z, rounded once: what w4a16_linear_backward reads; y
+ * is computed from the unrounded z.  residual may be y itself (y += act(z)); any other sharing of
+ * memory between an output and another operand is W4A16_ERR_OVERLAP.  Kernels as w4a16_gemm_swiglu's
+ * (m = 1 and 2-4: the decode kernels; up to 16 rows, or 32 and up to 32 MB of weights, the
+ * weight-streaming kernel; beyond, tiles), with their weights: exact on the decode kernels, and at group 128
+ * on the others where the scales' alignment allows (K / 128 even, or the tiles), else fp16(s q).
+ * Workspace (w4a16_linear_workspace_bytes) and errors as w4a16_gemm_swiglu, also W4A16_ERR_RANGE for an
+ * unknown activation; k == 0 is refused (W4A16_ERR_SHAPE): there is no product to fold into.
+ */
+w4a16_status w4a16_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, const uint16_t* bias,
+                          const uint16_t* residual, uint16_t* y, uint16_t* pre, int64_t m, int64_t n, int64_t k,
+                          int32_t group, int32_t activation, void* workspace, size_t workspace_bytes,
+                          w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_linear needs on the current device; 0: none, the pointer may be NULL. */
+size_t w4a16_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
+ * Backward pass of w4a16_linear: dy [m, n] is the gradient of y (and, unchanged, of residual), pre
+ * [m, n] the z it kept.  Writes
+ *
+ *     dpre = dy act'(pre)   fp16 [m, n], in fp32 with one rounding
+ *     dbias[n] = sum over rows of dy act'(pre)   fp32 [n], of the unrounded values, in a fixed order
+ *     dx = dpre . deq(W)   fp16 [m, k], the product of that fp16 output, as w4a16_gemm_t
+ *
+ * dbias may be NULL (not computed).  With W4A16_ACT_NONE dpre is dy: pre and dpre must be NULL, and dx is
+ * the product of dy.  All 16-byte aligned.  The gradient of the scales is w4a16_gemm_dscales of dpre
+ * (or dy).  Outputs that share memory with another operand are W4A16_ERR_OVERLAP; m, n or k of 0 is as
+ * in w4a16_gemm_t (m == 0 writes zeros to dbias).  Workspace (w4a16_linear_backward_workspace_bytes, which
+ * covers calls with and without dbias) and errors as w4a16_gemm_t.
+ */
+w4a16_status w4a16_linear_backward(const uint16_t* dy, const uint16_t* pre, const uint32_t* packed,
+                                   const uint16_t* scales, uint16_t* dpre, float* dbias, uint16_t* dx, int64_t m,
+                                   int64_t n, int64_t k, int32_t group, int32_t activation, void* workspace,
+                                   size_t workspace_bytes, w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_linear_backward needs on the current device. */
+size_t w4a16_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t group);
+
+/*
  * MoE grouped GEMM (the routed-expert layers of the 35B-A3B MoE model on the
  * LLM170 CUDA/W4A16 page, g32).  x [rows, k] holds one row per (token, expert)
  * pair, sorted by expert; rows offsets[e] .. offsets[e+1]-1 belong to expert e
@@ -362,6 +421,64 @@ w4a16_status w4a16_grouped_gemm_swiglu(const uint16_t* x, const int32_t* pair_to
 w4a16_status w4a16_moe_combine(const uint16_t* y_pairs, const int32_t* pair_row, const float* weights,
                                uint16_t* out, int64_t tokens, int32_t topk, int64_t rows, int64_t n,
                                w4a16_stream_t stream);
+
+/*
+ * The router's choice: logits [tokens, experts] (fp32 or fp16: `dtype`, a w4a16_dtype; 16-byte aligned)
+ * -> ids int32 [tokens, topk], the topk largest logits of each token in falling order (equal ones: the
+ * lowest expert first), and weights fp32 [tokens, topk], their softmax
+ *
+ *     weights[t, s] = exp(l_s - max) / sum_j exp(l_j - max)
+ *
+ * with j over all experts, or over the chosen ones if `renormalize` is not 0.  An expert whose logit is
+ * -inf is masked out: it is never chosen, and a slot that is left without an expert gets id -1 and weight
+ * 0, which w4a16_moe_route and w4a16_moe_ffn pass over (so a token may have none).  NaN counts as the
+ * largest logit; a NaN or +inf among the logits that the sum covers leaves the token's weights NaN.  1 <= topk <= experts <= 1024, topk
+ * <= 64 (else W4A16_ERR_SHAPE); an unknown dtype is W4A16_ERR_RANGE.  No workspace.
+ */
+w4a16_status w4a16_moe_topk(const void* logits, int32_t dtype, int32_t* ids, float* weights, int64_t tokens,
+                            int32_t experts, int32_t topk, int32_t renormalize, w4a16_stream_t stream);
+
+/*
+ * Backward pass of w4a16_moe_topk: dweights fp32 [tokens, topk] -> dlogits [tokens, experts] of the logits'
+ * dtype (rounded once), from the ids and weights that the forward pass wrote:
+ *
+ *     mean = sum_s w_s dw_s
+ *     renormalize: dlogits[id_s] = w_s (dw_s - mean), 0 elsewhere (logits are not read, and may be NULL)
+ *     else:        dlogits[e] = p_e (dw_s - mean) if e = id_s, -p_e mean elsewhere, p the softmax of the logits
+ *
+ * Slots with an id outside [0, experts) count for nothing; the ids of a token are distinct otherwise.
+ * dlogits may not share memory with an input (W4A16_ERR_OVERLAP).  Sizes and errors as w4a16_moe_topk.
+ */
+w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, int32_t dtype, const int32_t* ids,
+                                     const float* weights, void* dlogits, int64_t tokens, int32_t experts,
+                                     int32_t topk, int32_t renormalize, w4a16_stream_t stream);
+
+/*
+ * The routed experts' whole feed-forward for a few tokens (decoding), in two kernels:
+ *
+ *     y[t] = residual[t] + sum_s weights[t, s] * W2[e] . (SiLU(g) * u),  (g, u) = W1[e] . x[t],  e = ids[t, s]
+ *
+ * x, y, residual fp16 [tokens, hidden] (residual NULL: none; it may be y itself); ids int32 and weights
+ * fp32 [tokens, topk] as w4a16_moe_topk writes them (an id outside [0, experts) contributes nothing; a token
+ * may name an expert twice); gate_up [experts, 2 inter, hidden/8] and its scales interleave gate (even) and up
+ * rows as for w4a16_grouped_gemm_swiglu, down [experts, hidden, inter/8] and its scales as for
+ * w4a16_grouped_gemm.  Each used expert's weights are read once, and exactly; sums are fp32; SiLU(g) u
+ * is kept to 22 bits between the kernels (up to 2^24 in size); slots are added in order, with the
+ * residual, and y is rounded once.  A not finite x leaves its own token's outputs alone not finite.
+ * 1 <= tokens <= 64 and tokens * topk <= 512, hidden and inter multiples of group and at least one group,
+ * one expert's weights below 2 GiB (else W4A16_ERR_SHAPE; banks may be larger than that).  For more tokens:
+ * w4a16_moe_route, w4a16_grouped_gemm_swiglu, w4a16_grouped_gemm, w4a16_moe_combine.  Workspace
+ * (w4a16_moe_ffn_workspace_bytes) as for w4a16_gemm_swiglu, which may share one with it; sharing
+ * of memory other than residual = y is W4A16_ERR_OVERLAP; tokens == 0 or hidden == 0 is a no-op.
+ */
+w4a16_status w4a16_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
+                           const uint16_t* gate_up_scales, const uint32_t* down, const uint16_t* down_scales,
+                           const uint16_t* residual, uint16_t* y, int64_t tokens, int32_t topk, int32_t experts,
+                           int64_t hidden, int64_t inter, int32_t group, void* workspace, size_t workspace_bytes,
+                           w4a16_stream_t stream);
+
+/* Bytes of device workspace w4a16_moe_ffn needs (0 for sizes it refuses). */
+size_t w4a16_moe_ffn_workspace_bytes(int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32_t group);
 
 /* --------------------------------------------------------- measurement ---- */
 

@@ -72,6 +72,14 @@ SIGNATURES = {
     "w4a16_gemm_swiglu_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "w4a16_grouped_gemm_swiglu": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i64, _i32,
                                                  _vp]),
+    "w4a16_linear": (ctypes.c_int, [_vp] * 7 + [_i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp]),
+    "w4a16_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "w4a16_linear_backward": (ctypes.c_int, [_vp] * 7 + [_i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp]),
+    "w4a16_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "w4a16_moe_topk": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i64, _i32, _i32, _i32, _vp]),
+    "w4a16_moe_topk_backward": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp]),
+    "w4a16_moe_ffn": (ctypes.c_int, [_vp] * 9 + [_i64, _i32, _i32, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "w4a16_moe_ffn_workspace_bytes": (_sz, [_i64, _i32, _i64, _i64, _i32]),
 }
 
 for _name, (_res, _args) in SIGNATURES.items():
@@ -439,7 +447,11 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
         # it may be another stream's memory: not to be handed out again before this call is done
         given.record_stream(_torch_preload.cuda.current_stream())
         return given.data_ptr(), given.numel() * 4, given
-    nbytes = _ffn_workspace_bytes(entry, m, n, k, group, device.index)
+    return _kept_workspace(_ffn_workspace_bytes(entry, m, n, k, group, device.index), device, handle)
+
+
+def _kept_workspace(nbytes, device, handle):
+    """A workspace of at least nbytes for a call on stream `handle` of the current device."""
     if nbytes == 0:
         return 0, 0, None
     if _torch_preload.cuda.is_current_stream_capturing():
@@ -467,12 +479,12 @@ def _new_workspace(nbytes, device):
 
 
 def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None, stream=None):
-    """A workspace tensor for gemm_swiglu, gemm_swiglu_backward, gemm_t or gemm_dscales (`call` by name)
-    of these sizes (n as in the C ABI: outputs of the gated calls, else weight rows); None if none is needed.
+    """A workspace tensor for gemm_swiglu, gemm_swiglu_backward, gemm_t, gemm_dscales, linear or
+    linear_backward (`call` by name) of these sizes (n as in the C ABI: outputs of the gated calls, else weight rows); None if none is needed.
     It is allocated and cleared on `stream` (None: the device's current one), and the host waits for that, so
     calls on any stream may use it (one after another; under graph capture, only calls of that capture that
     are ordered behind this one)."""
-    if call not in ("gemm_swiglu", "gemm_swiglu_backward", "gemm_t", "gemm_dscales"):
+    if call not in ("gemm_swiglu", "gemm_swiglu_backward", "gemm_t", "gemm_dscales", "linear", "linear_backward"):
         raise ValueError(f"ffn_workspace: no workspace for {call!r}")
     cuda = _torch_preload.cuda
     device = _torch_preload.device(device) if device is not None else stream.device if stream is not None \
@@ -614,6 +626,225 @@ def gemm_dscales(d, x, packed, group: int, out=None, workspace=None, stream=None
     return out
 
 
+# ---------------------------------------------------------------------------
+# The linear layer with bias, activation and residual folded into its product, and its backward pass:
+# devices, streams, workspaces and autograd as for the feed-forward block's calls above.
+# ---------------------------------------------------------------------------
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _activation(what, name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"{what}: activation must be one of {', '.join(ACTIVATIONS)}, not {name!r}")
+    return ACTIVATIONS[name]
+
+
+def linear(x, packed, scales, group: int, bias=None, activation: str = "none", residual=None, pre=None, out=None,
+           workspace=None, stream=None):
+    """y [m, n] = act(x . deq(packed, scales)^T + bias) + residual for any m.  bias fp16 [n]; residual fp16 [m, n],
+    which may be `out`; pre (fp16 [m, n]), if given, receives the pre-activations for linear_backward."""
+    what = "linear"
+    act = _activation(what, activation)
+    _matrices(what, group, x=x, packed=packed, scales=scales)
+    (m, k), n = x.shape, packed.shape[0]
+    _check_k(what, k, group)
+    specs = [("x", x, _F16, None), ("packed", packed, _U32, (n, k // 8)), ("scales", scales, _F16, (n, k // group))]
+    if bias is not None:
+        specs.append(("bias", bias, _F16, (n,)))
+    if residual is not None:
+        specs.append(("residual", residual, _F16, (m, n)))
+    if pre is not None:
+        specs.append(("pre", pre, _F16, (m, n)))
+    if out is not None:
+        specs.append(("out", out, _F16, (m, n)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+
+    def call(handle):
+        nonlocal out
+        if out is None:
+            out = _torch_preload.empty((m, n), dtype=x.dtype, device=device)
+        ws, nbytes, held = _ffn_workspace("w4a16_linear", m, n, k, group, device, handle, workspace)
+        _check(lib.w4a16_linear(x.data_ptr(), packed.data_ptr(), scales.data_ptr(),
+                                0 if bias is None else bias.data_ptr(), 0 if residual is None else residual.data_ptr(),
+                                out.data_ptr(), 0 if pre is None else pre.data_ptr(), m, n, k, group, act, ws, nbytes,
+                                handle), "w4a16_linear")
+
+    _launch_on(what, device, stream, call, specs)
+    return out
+
+
+def linear_backward(dy, packed, scales, group: int, pre=None, activation: str = "none", out=None, dpre=None, dbias=None,
+                    workspace=None, stream=None):
+    """(dx [m, k], dpre [m, n], dbias fp32 [n]) from dy [m, n] and the pre-activations that linear kept.  dbias: a
+    tensor to write, True to have one made, None (and returned as None) for a layer without bias.  With
+    activation "none" there are no pre-activations: dpre is dy's, and None is returned for it."""
+    what = "linear_backward"
+    act = _activation(what, activation)
+    _matrices(what, group, dy=dy, packed=packed, scales=scales)
+    (m, n), k = dy.shape, packed.shape[1] * 8
+    _check_k(what, k, group)
+    if (pre is None) != (act == 0):
+        raise ValueError(f"{what}: pre is for a layer with an activation" if act == 0 else
+                         f"{what}: pre, the pre-activations that linear kept, is missing")
+    if dpre is not None and act == 0:
+        raise ValueError(f"{what}: dpre is dy itself in a layer without activation")
+    specs = [("dy", dy, _F16, None), ("packed", packed, _U32, (n, k // 8)), ("scales", scales, _F16, (n, k // group))]
+    if pre is not None:
+        specs.append(("pre", pre, _F16, (m, n)))
+    if out is not None:
+        specs.append(("out", out, _F16, (m, k)))
+    if dpre is not None:
+        specs.append(("dpre", dpre, _F16, (m, n)))
+    if dbias is not None and dbias is not True:
+        specs.append(("dbias", dbias, _F32, (n,)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+
+    def call(handle):
+        nonlocal out, dpre, dbias
+        if out is None:
+            out = _torch_preload.empty((m, k), dtype=dy.dtype, device=device)
+        if dpre is None and act != 0:
+            dpre = _torch_preload.empty((m, n), dtype=dy.dtype, device=device)
+        if dbias is True:
+            dbias = _torch_preload.empty(n, dtype=_torch_preload.float32, device=device)
+        ws, nbytes, held = _ffn_workspace("w4a16_linear_backward", m, n, k, group, device, handle, workspace)
+        _check(lib.w4a16_linear_backward(dy.data_ptr(), 0 if pre is None else pre.data_ptr(), packed.data_ptr(),
+                                         scales.data_ptr(), 0 if dpre is None else dpre.data_ptr(),
+                                         0 if dbias is None else dbias.data_ptr(), out.data_ptr(), m, n, k, group, act,
+                                         ws, nbytes, handle), "w4a16_linear_backward")
+
+    _launch_on(what, device, stream, call, specs)
+    return out, dpre, dbias
+
+
+# ---------------------------------------------------------------------------
+# The router's choice with its gradient, and the routed experts' feed-forward for a few tokens (the
+# same conventions).
+# ---------------------------------------------------------------------------
+def _logits_dtype(what, logits):
+    if not isinstance(logits, _torch_preload.Tensor):
+        raise TypeError(f"{what}: logits must be a torch.Tensor, not {type(logits).__name__}")
+    if logits.dim() != 2:
+        raise ValueError(f"{what}: logits must be [tokens, experts]")
+    return 1 if logits.dtype == _torch_preload.float16 else 0
+
+
+def moe_topk(logits, topk: int, renormalize: bool = True, ids=None, weights=None, stream=None):
+    """The router's choice: (ids int32 [tokens, topk], weights fp32 [tokens, topk]) from logits [tokens, experts]
+    (fp32 or fp16), the largest first, equal ones by expert; weights are the softmax over all experts, or over the
+    chosen ones (renormalize).  A logit of -inf is never chosen: id -1 and weight 0 where none is left."""
+    what = "moe_topk"
+    dtype = _logits_dtype(what, logits)
+    tokens, experts = logits.shape
+    if not 1 <= topk <= min(experts, 64) or experts > 1024:
+        raise ValueError(f"{what}: topk = {topk} of {experts} experts: 1 <= topk <= min(experts, 64), experts <= 1024")
+    specs = [("logits", logits, _F32 + _F16, None)]
+    if ids is not None:
+        specs.append(("ids", ids, _I32, (tokens, topk)))
+    if weights is not None:
+        specs.append(("weights", weights, _F32, (tokens, topk)))
+    device = _check_ffn(what, specs)
+
+    def call(handle):
+        nonlocal ids, weights
+        if ids is None:
+            ids = _torch_preload.empty((tokens, topk), dtype=_torch_preload.int32, device=device)
+        if weights is None:
+            weights = _torch_preload.empty((tokens, topk), dtype=_torch_preload.float32, device=device)
+        _check(lib.w4a16_moe_topk(logits.data_ptr(), dtype, ids.data_ptr(), weights.data_ptr(), tokens, experts, topk,
+                                  bool(renormalize), handle), "w4a16_moe_topk")
+
+    _launch_on(what, device, stream, call, specs)
+    return ids, weights
+
+
+def moe_topk_backward(dweights, logits, ids, weights, renormalize: bool = True, out=None, stream=None):
+    """dlogits [tokens, experts] (the logits' dtype) from dweights fp32 [tokens, topk] and what moe_topk took and gave."""
+    what = "moe_topk_backward"
+    dtype = _logits_dtype(what, logits)
+    tokens, experts = logits.shape
+    if not isinstance(ids, _torch_preload.Tensor) or ids.dim() != 2:
+        raise ValueError(f"{what}: ids must be a [tokens, topk] tensor")
+    topk = ids.shape[1]
+    if not 1 <= topk <= min(experts, 64) or experts > 1024:
+        raise ValueError(f"{what}: topk = {topk} of {experts} experts: 1 <= topk <= min(experts, 64), experts <= 1024")
+    specs = [("logits", logits, _F32 + _F16, None), ("dweights", dweights, _F32, (tokens, topk)),
+             ("ids", ids, _I32, (tokens, topk)), ("weights", weights, _F32, (tokens, topk))]
+    if out is not None:
+        specs.append(("out", out, (logits.dtype,), (tokens, experts)))
+    device = _check_ffn(what, specs)
+
+    def call(handle):
+        nonlocal out
+        if out is None:
+            out = _torch_preload.empty((tokens, experts), dtype=logits.dtype, device=device)
+        _check(lib.w4a16_moe_topk_backward(dweights.data_ptr(), logits.data_ptr(), dtype, ids.data_ptr(),
+                                           weights.data_ptr(), out.data_ptr(), tokens, experts, topk, bool(renormalize),
+                                           handle), "w4a16_moe_topk_backward")
+
+    _launch_on(what, device, stream, call, specs)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group):
+    return lib.w4a16_moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group)
+
+
+def moe_ffn(x, ids, weights, gate_up, gate_up_scales, down, down_scales, group: int, residual=None, out=None,
+            workspace=None, stream=None):
+    """The routed experts' feed-forward for up to 64 tokens and 512 (token, slot) pairs: out [tokens, hidden] =
+    residual + sum over a token's slots of weight * down(SiLU(g) u).  gate_up [experts, 2 inter, hidden/8] interleaves
+    gate and up rows, down [experts, hidden, inter/8]; ids and weights [tokens, topk] as moe_topk gives them;
+    residual may be `out`."""
+    what = "moe_ffn"
+    tensor = _torch_preload.Tensor
+    for name, t, dims in (("x", x, 2), ("ids", ids, 2), ("gate_up", gate_up, 3), ("down", down, 3)):
+        if not isinstance(t, tensor):
+            raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
+        if t.dim() != dims:
+            raise ValueError(f"{what}: {name} must be {dims}-D")
+    if group not in (32, 128):
+        raise ValueError(f"{what}: the group size must be 32 or 128 (got {group})")
+    (tokens, hidden), topk = x.shape, ids.shape[1]
+    experts, inter = gate_up.shape[0], down.shape[2] * 8
+    if hidden % group or inter % group:
+        raise ValueError(f"{what}: hidden = {hidden} and inter = {inter} must be multiples of the group size {group}")
+    specs = [("x", x, _F16, None), ("ids", ids, _I32, (tokens, topk)), ("weights", weights, _F32, (tokens, topk)),
+             ("gate_up", gate_up, _U32, (experts, 2 * inter, hidden // 8)),
+             ("gate_up_scales", gate_up_scales, _F16, (experts, 2 * inter, hidden // group)),
+             ("down", down, _U32, (experts, hidden, inter // 8)),
+             ("down_scales", down_scales, _F16, (experts, hidden, inter // group))]
+    if residual is not None:
+        specs.append(("residual", residual, _F16, (tokens, hidden)))
+    if out is not None:
+        specs.append(("out", out, _F16, (tokens, hidden)))
+    if workspace is not None:
+        specs.append(("workspace", workspace, _I32, None))
+    device = _check_ffn(what, specs)
+
+    def call(handle):
+        nonlocal out
+        if out is None:
+            out = _torch_preload.empty((tokens, hidden), dtype=x.dtype, device=device)
+        if workspace is not None:
+            workspace.record_stream(_torch_preload.cuda.current_stream())
+            ws, nbytes, held = workspace.data_ptr(), workspace.numel() * 4, workspace
+        else:
+            ws, nbytes, held = _kept_workspace(_moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group), device, handle)
+        _check(lib.w4a16_moe_ffn(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), gate_up.data_ptr(),
+                                 gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
+                                 0 if residual is None else residual.data_ptr(), out.data_ptr(), tokens, topk, experts,
+                                 hidden, inter, group, ws, nbytes, handle), "w4a16_moe_ffn")
+
+    _launch_on(what, device, stream, call, specs)
+    return out
+
+
 def _bank_shapes(what, packed, scales, k, group):
     _require_tensors(what, packed=packed, scales=scales)
     if packed.dim() != 3 or scales.dim() != 3:
@@ -716,4 +947,5 @@ __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "u
            "gemm_workspace", "gemm_workspace_status", "gemm_noalloc",
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
            "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t",
-           "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace", "ffn_release_workspaces"] + list(SIGNATURES)
+           "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace", "ffn_release_workspaces", "ACTIVATIONS", "linear",
+           "linear_backward", "moe_topk", "moe_topk_backward", "moe_ffn"] + list(SIGNATURES)

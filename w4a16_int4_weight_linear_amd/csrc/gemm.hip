@@ -64,6 +64,7 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 #include "mfma_operands.hpp"
 #include "tile_gemm.hpp"
 
@@ -205,8 +206,9 @@ struct Item {
 
 // What the epilogue writes: the product; or, with weight rows that interleave
 // SwiGLU gate (even) and up (odd) rows, y [M, N / 2] = SiLU(gate) * up, without
-// or with the product itself (fp16, z [M, N]).
-enum Epilogue { kEpiProduct, kEpiSwiglu, kEpiSwigluKeep };
+// or with the product itself (fp16, z [M, N]); or the linear layer's (LinearEpilogue, the
+// kernel's last argument).
+enum Epilogue { kEpiProduct, kEpiSwiglu, kEpiSwigluKeep, kEpiLinear };
 
 // Two rows of a (gate, up) column pair.  a0, a1: this lane's column in two
 // accumulator rows.  Lanes 2i and 2i + 1 hold a pair's gate and up columns; after
@@ -225,14 +227,14 @@ __device__ inline float swiglu_pair(float a0, float a1, bool odd) {
 // SALIGN: every row's scales start on a 16-byte boundary (K / G a multiple
 // of 8 and a 16-byte aligned scale array), so they come in LDS windows;
 // otherwise with the stages.
-// MB: 32-row blocks per tile (4; a SwiGLU product of up to 64 rows: 2).
-template <int G, bool KTAIL, bool SALIGN, int EPI, int MB>
+// MB: 32-row blocks per tile (4; a SwiGLU product or a linear layer of up to 64 rows: 2).
+template <int G, bool KTAIL, bool SALIGN, int EPI, int MB, typename... Epi>
 __global__ void __launch_bounds__(kThreads)
 gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
             int M, int N, int K, int tiles_m, int tiles_n, int iters, int rounds, int sk_tiles, int nsk,
             float* __restrict__ partials, uint32_t* __restrict__ flags, uint32_t* __restrict__ counters,
-            uint32_t* __restrict__ status, uint16_t* __restrict__ z) {
+            uint32_t* __restrict__ status, uint16_t* __restrict__ z, Epi... epi) {
   constexpr int kMB = MB, BM = 32 * MB, kABytes = BM * BK * 2, kStageBytes = kABytes + kBBytes;
   constexpr size_t kPartialBytes = partial_bytes(MB);
   constexpr int kGroups = BK / G;            // scale groups per K step (1 or 4)
@@ -575,7 +577,63 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
       cur = nxt;
     }
 
-    if (dp) {
+    if (dp && EPI == kEpiLinear) {
+      // The sums through LDS as fp32 (stage 2, 32 rows of the wave at a time), so that a lane has
+      // eight neighbouring columns of a row: whole 16-byte accesses to y, pre and residual, and one
+      // rounding of act(z) + residual.
+      constexpr int kPitch = kWaveN * 4 + 16;
+      static_assert(kWaves * 32 * kPitch <= kStage, "epilogue slabs exceed stage 2");
+      uint8_t* ep = stage2 + wave * 32 * kPitch;
+      auto finish = [&](const LinearEpilogue& le) {
+        const float bias = le.bias && nw + li < N ? half_bits_to_float(le.bias[nw + li]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kMB; ++i) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            *reinterpret_cast<float*>(ep + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch + li * 4) = acc[i][0][r] + bias;
+          // (a wave's LDS accesses complete in order: its own writes are visible)
+          if (N & 7) {          // rows of any alignment: two rows of 32 columns per access
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int row = 2 * j + h, m = m0 + 32 * i + row, n = nw + li;
+              const float v = *reinterpret_cast<const float*>(ep + row * kPitch + li * 4);
+              if (m < M && n < N) {
+                const size_t at = (size_t)m * N + n;
+                if (le.pre) le.pre[at] = float_to_half_bits(v);
+                const float o = activate(le.act, v);
+                y[at] = float_to_half_bits(le.residual ? o + half_bits_to_float(le.residual[at]) : o);
+              }
+            }
+            continue;
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int row = 16 * j + (lane >> 2), c = lane & 3, m = m0 + 32 * i + row, n = nw + 8 * c;
+            if (m >= M || n >= N) continue;
+            const size_t at = (size_t)m * N + n;
+            f16x8 res = f16x8{};
+            if (le.residual) res = *reinterpret_cast<const f16x8*>(le.residual + at);
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const f32x4 t = *reinterpret_cast<const f32x4*>(ep + row * kPitch + c * 32 + 16 * q);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) v[4 * q + u] = t[u];
+            }
+            f16x8 o;
+            if (le.pre) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u) o[u] = (_Float16)v[u];
+              *reinterpret_cast<f16x8*>(le.pre + at) = o;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = (_Float16)(activate(le.act, v[u]) + (float)res[u]);
+            *reinterpret_cast<f16x8*>(y + at) = o;
+          }
+        }
+      };
+      (finish(epi), ...);
+    } else if (dp) {
       // Output through LDS (stage 2, free once the last step's barrier has
       // passed; the next item's first load into it follows that item's first
       // barrier): each wave writes its 128 x 32 fp16 slab in two passes of 64
@@ -795,7 +853,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   }
 }
 
-constexpr int swiglu_quads(int mb) { return mb * kNB * 4 * kThreads; }
+constexpr int tile_quads(int mb) { return mb * kNB * 4 * kThreads; }
 
 // Joins the split tiles of the SwiGLU product: one thread per 16-byte quad (four rows of
 // a column), the parts added in contributor order, gate and up in neighbouring lanes.
@@ -803,7 +861,7 @@ template <int MB>
 __global__ void __launch_bounds__(256)
 swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y, uint16_t* __restrict__ z, int M, int N,
                    SplitPlan plan) {
-  constexpr int BM = 32 * MB, kQuads = swiglu_quads(MB);
+  constexpr int BM = 32 * MB, kQuads = tile_quads(MB);
   constexpr size_t kPartialBytes = partial_bytes(MB);
   const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
   const Contributors cs(plan, tile);
@@ -829,6 +887,29 @@ swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y,
     for (int r = 0; r < 4; ++r)
       if (m0 + r < M) z[(size_t)(m0 + r) * N + n] = float_to_half_bits(v[r]);
   }
+}
+
+// The same for the linear layer.
+template <int MB>
+__global__ void __launch_bounds__(256)
+linear_join_kernel(const float* __restrict__ partials, uint16_t* y, int M, int N, SplitPlan plan, LinearEpilogue ep) {
+  constexpr int BM = 32 * MB, kQuads = tile_quads(MB);
+  constexpr size_t kPartialBytes = partial_bytes(MB);
+  const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
+  const Contributors cs(plan, tile);
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(partials) + (size_t)c * 16;
+  int tm, tn;
+  tile_coords(plan.rounds * plan.wgs + tile, plan.tiles_m, plan.tiles_n, tm, tn);
+  const int t = c % kThreads, bq = c / kThreads, i = bq >> 2, q = bq & 3;
+  const int n = tn * BN + (t >> 6) * kWaveN + (t & 31);
+  const int m0 = tm * BM + 32 * i + 8 * q + 4 * ((t >> 5) & 1);
+  if (n >= N || m0 >= M) return;
+  f32x4 v = f32x4{};
+  for (int l = cs.first; l <= cs.last; ++l)
+    v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(l) * kPartialBytes);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (m0 + r < M) store_result(y, (size_t)(m0 + r) * N + n, n, v[r], ep);
 }
 
 // ---- scratch of the allocation-free entry point (w4a16_gemm_noalloc) ----
@@ -879,9 +960,10 @@ size_t gemm_workspace_bytes(int64_t m, int64_t n, int64_t k, int, const DeviceIn
 }
 
 namespace {
-template <int EPI, int MB>
+template <int EPI, int MB, typename... Epi>
 hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
-                      int m, int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
+                      int m, int n, int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream,
+                      const Epi&... epi) {
   const GemmPlan p = EPI == kEpiProduct ? gemm_plan(m, n, k, dev) : swiglu_plan(m, n, k, dev);
   float* partials = nullptr;
   uint32_t* flags = nullptr;
@@ -898,16 +980,20 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
   }
   const bool tail = k % BK != 0;
   const bool salign = (k / group) % 8 == 0 && (reinterpret_cast<uintptr_t>(scales) & 15) == 0;
-  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true, EPI, MB> : gemm_kernel<128, false, false, EPI, MB>)
-              : tail       ? gemm_kernel<32, true, false, EPI, MB>
-              : salign     ? gemm_kernel<32, false, true, EPI, MB>
-                           : gemm_kernel<32, false, false, EPI, MB>;
+  auto kern = group == 128 ? (salign ? gemm_kernel<128, false, true, EPI, MB, Epi...>
+                                     : gemm_kernel<128, false, false, EPI, MB, Epi...>)
+              : tail       ? gemm_kernel<32, true, false, EPI, MB, Epi...>
+              : salign     ? gemm_kernel<32, false, true, EPI, MB, Epi...>
+                           : gemm_kernel<32, false, false, EPI, MB, Epi...>;
   const hipError_t e =
       launch_kernel(kern, dim3(p.wgs), dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, p.tiles_m, p.tiles_n,
-                    p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z);
+                    p.iters, p.rounds, p.sk_tiles, p.nsk, partials, flags, counters, status, z, epi...);
   if (EPI == kEpiProduct || e != hipSuccess || p.sk_tiles == 0) return e;
-  return launch_kernel(swiglu_join_kernel<MB>, dim3((unsigned)p.sk_tiles * (swiglu_quads(MB) / 256)), dim3(256), 0,
-                       stream, partials, y, z, m, n, split_of(p));
+  const dim3 grid((unsigned)p.sk_tiles * (tile_quads(MB) / 256));
+  if constexpr (EPI == kEpiLinear)
+    return launch_kernel(linear_join_kernel<MB>, grid, dim3(256), 0, stream, partials, y, m, n, split_of(p), epi...);
+  else
+    return launch_kernel(swiglu_join_kernel<MB>, grid, dim3(256), 0, stream, partials, y, z, m, n, split_of(p));
 }
 }  // namespace
 
@@ -928,6 +1014,18 @@ hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const u
   auto launch = z ? (two ? launch_epi<kEpiSwigluKeep, 2> : launch_epi<kEpiSwigluKeep, kMB>)
                   : (two ? launch_epi<kEpiSwiglu, 2> : launch_epi<kEpiSwiglu, kMB>);
   return launch(x, packed, scales, y, z, m, 2 * n_out, k, group, workspace, dev, stream);
+}
+
+size_t gemm_linear_workspace_bytes(int m, int n, int k, const DeviceInfo& dev) {
+  const GemmPlan p = swiglu_plan(m, n, k, dev);
+  return p.sk_tiles ? kCounterBytes + split_slots(split_of(p)) * partial_bytes(swiglu_blocks(m)) : 0;
+}
+
+hipError_t launch_gemm_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                              int n, int k, int group, const LinearEpilogue& ep, void* workspace, const DeviceInfo& dev,
+                              hipStream_t stream) {
+  auto launch = swiglu_blocks(m) == 2 ? launch_epi<kEpiLinear, 2, LinearEpilogue> : launch_epi<kEpiLinear, kMB, LinearEpilogue>;
+  return launch(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream, ep);
 }
 
 }  // namespace w4a16

@@ -30,6 +30,7 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 #include "mfma_operands.hpp"
 
 namespace w4a16 {
@@ -59,16 +60,18 @@ static_assert(kWaves * kMaxBlocks * 1024 <= kLds, "the final partial tiles reuse
 // outputs; workgroup ranges are whole pairs and the epilogue writes
 // y[m, i] = SiLU(gate_i) * up_i (fp32, rounded once) instead of both rows.  KEEP:
 // both rows go to z [M, N] as well (the fp16 pre-activations a backward pass reads).
-template <int G, bool ALIGNED, bool SWIGLU, bool KEEP>
+// Epi: none, or the linear layer's epilogue (neither SWIGLU nor KEEP).
+template <int G, bool ALIGNED, bool SWIGLU, bool KEEP, typename... Epi>
 __global__ void __launch_bounds__(kThreads)
 gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
                    const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
-                   int M, int N, int K, int rows_base, int rows_extra, uint16_t* __restrict__ z) {
+                   int M, int N, int K, int rows_base, int rows_extra, uint16_t* __restrict__ z, Epi... epi) {
   __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
   // grid row p: rows 16 p .. 16 p + 15 (the SwiGLU product of up to 32 rows is one launch)
   if (const int p = blockIdx.y; p > 0) {
     x += (size_t)16 * p * K;
     y += (size_t)16 * p * (SWIGLU ? N >> 1 : N);
+    (epi.skip_rows(16 * p, N), ...);
     if constexpr (KEEP) z += (size_t)16 * p * N;
     M -= 16 * p;
   }
@@ -365,17 +368,18 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int rr = 16 * wave + 4 * lq + j;
-        if (rr < nr) y[(size_t)li * N + r0 + rr] = float_to_half_bits(t[j]);
+        if (rr < nr) store_result(y, (size_t)li * N + r0 + rr, r0 + rr, t[j], epi...);
       }
     }
   }
 }
 
-template <int G, bool ALIGNED, bool SWIGLU, bool KEEP>
+template <int G, bool ALIGNED, bool SWIGLU, bool KEEP, typename... Epi>
 hipError_t launch_ga(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
-                     int m, int n, int k, int blocks, int units, hipStream_t stream) {
-  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU, KEEP>, dim3(blocks, (m + 15) / 16), dim3(kThreads), 0,
-                       stream, x, packed, scales, y, m, n, k, units / blocks, units % blocks, z);
+                     int m, int n, int k, int blocks, int units, hipStream_t stream, const Epi&... epi) {
+  return launch_kernel(gemm_skinny_kernel<G, ALIGNED, SWIGLU, KEEP, Epi...>, dim3(blocks, (m + 15) / 16),
+                       dim3(kThreads), 0, stream, x, packed, scales, y, m, n, k, units / blocks, units % blocks, z,
+                       epi...);
 }
 
 // n weight rows in units of `unit` rows (2: gate/up pairs); returns the grid.
@@ -390,9 +394,9 @@ int skinny_grid(int n, int unit, const DeviceInfo& dev) {
   return g;
 }
 
-template <bool SWIGLU, bool KEEP>
+template <bool SWIGLU, bool KEEP, typename... Epi>
 hipError_t launch_s(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, uint16_t* z,
-                    int m, int n, int k, int group, const DeviceInfo& dev, hipStream_t stream) {
+                    int m, int n, int k, int group, const DeviceInfo& dev, hipStream_t stream, const Epi&... epi) {
   const int unit = SWIGLU ? 2 : 1;
   const int g = skinny_grid(n, unit, dev);
   const int units = n / unit;
@@ -401,9 +405,10 @@ hipError_t launch_s(const uint16_t* x, const uint32_t* packed, const uint16_t* s
   // 16-byte (g32) or 4-byte (g128) aligned in memory
   const uintptr_t sp = reinterpret_cast<uintptr_t>(scales);
   const bool al = group == 32 ? spr % 8 == 0 && (sp & 15) == 0 : spr % 2 == 0 && (sp & 3) == 0;
-  auto launch = group == 32 ? (al ? launch_ga<32, true, SWIGLU, KEEP> : launch_ga<32, false, SWIGLU, KEEP>)
-                            : (al ? launch_ga<128, true, SWIGLU, KEEP> : launch_ga<128, false, SWIGLU, KEEP>);
-  return launch(x, packed, scales, y, z, m, n, k, g, units, stream);
+  auto launch =
+      group == 32 ? (al ? launch_ga<32, true, SWIGLU, KEEP, Epi...> : launch_ga<32, false, SWIGLU, KEEP, Epi...>)
+                  : (al ? launch_ga<128, true, SWIGLU, KEEP, Epi...> : launch_ga<128, false, SWIGLU, KEEP, Epi...>);
+  return launch(x, packed, scales, y, z, m, n, k, g, units, stream, epi...);
 }
 
 }  // namespace
@@ -427,6 +432,12 @@ hipError_t launch_swiglu_skinny_keep(const uint16_t* x, const uint32_t* packed, 
                                      uint16_t* z, int m, int n_out, int k, int group, const DeviceInfo& dev,
                                      hipStream_t stream) {
   return launch_s<true, true>(x, packed, scales, y, z, m, 2 * n_out, k, group, dev, stream);
+}
+
+hipError_t launch_linear_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                                int n, int k, int group, const LinearEpilogue& ep, const DeviceInfo& dev,
+                                hipStream_t stream) {
+  return launch_s<false, false>(x, packed, scales, y, nullptr, m, n, k, group, dev, stream, ep);
 }
 
 }  // namespace w4a16

@@ -35,6 +35,7 @@
 //   without the sums over the waves 14.9; a wave loads its next unit only when it has used the last.
 // * Measured slower: a ring of units through LDS-direct loads (0.3-1.7 us), workgroups of 256 or
 //   1024 threads, 33-64 rows here instead of on the tiles (74 against 46 us, 17408 -> 5120).
+#include "arrive.hpp"
 #include "device.hpp"
 #include "gemm_t_skinny_plan.hpp"
 #include "kernels.hpp"
@@ -60,25 +61,6 @@ constexpr int kGradUnits = 4;
 // The same four columns of two neighbouring n.
 __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
   return __builtin_amdgcn_perm(w1, w0, hi ? 0x07060302u : 0x05040100u);
-}
-
-// A workgroup's part of a result is stored (device scope) and complete for this wave; counts
-// the workgroup's arrival at `counter`.  Returns true in all threads of the workgroup that
-// arrives last of `parts`, which then sees every part (through device-scope loads) and has
-// put the counter back to 0.  No workgroup waits for another.  All threads must call it;
-// `flag` is a word of LDS that nothing else uses meanwhile.
-__device__ inline bool arrive_last(uint32_t* counter, uint32_t parts, uint32_t* flag) {
-  __builtin_amdgcn_s_waitcnt(0);                 // this wave's stores have reached the device's memory
-  __syncthreads();                               // ... and every other wave's
-  if (threadIdx.x == 0) {
-    const uint32_t before = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (before == parts - 1u) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = before == parts - 1u;
-  }
-  __syncthreads();
-  const bool last = *flag != 0u;
-  __syncthreads();                               // (the word may be written again after this)
-  return last;
 }
 
 // VEC: rows of d are 16-byte aligned (N a multiple of 8); otherwise eight elements come as the five

@@ -61,6 +61,7 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 #include "wave_stamps.hpp"
 
 W4A16_STAMP_STORAGE(w4a16_wave_stamps_gemv)
@@ -113,11 +114,12 @@ __host__ __device__ inline GemvLayout gemv_layout(int m, int chunks, int spr, in
 //   sc : a 16-byte-aligned copy of the scales of the workgroup's rows (plus slack);
 //   part[wave][2][4] : partial sums of the first / last row of each wave;
 //   res[row][m] : finished fp32 sums of the workgroup's rows, written to y at the end.
-template <int M, bool GATED>
+// Epi: none, or the linear layer's epilogue (not GATED).
+template <int M, bool GATED, typename... Epi>
 __global__ void __launch_bounds__(kGemvThreads)
 gemv_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
-            int n, int k, int gshift, int rows_base, int rows_extra, uint32_t sc_shift) {
+            int n, int k, int gshift, int rows_base, int rows_extra, uint32_t sc_shift, Epi... epi) {
   // rows_base / rows_extra count row units: single rows, or gate/up row pairs.
   constexpr int kUnit = GATED ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -134,7 +136,7 @@ gemv_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   // wave index, made explicitly wave-uniform so the bookkeeping lives in SGPRs
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // timeline stamps (profiling build only; the M = 1 decode kernel)
-  constexpr bool kStamped = M == 1 && !GATED;
+  constexpr bool kStamped = M == 1 && !GATED && sizeof...(Epi) == 0;
   W4A16_STAMP_DECL;
   if (kStamped) W4A16_STAMP(0);
   const int blk = blockIdx.x;
@@ -485,7 +487,7 @@ gemv_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   if constexpr (!GATED) {
     for (int e = lane; e < (whole_hi - whole_lo) * M; e += 64) {
       const int rl = whole_lo + e / M, m = e - (e / M) * M;
-      y[(size_t)m * n + wg_r0 + rl] = float_to_half_bits(res[rl * M + m]);
+      store_result(y, (size_t)m * n + wg_r0 + rl, wg_r0 + rl, res[rl * M + m], epi...);
     }
   }
   // ---- rows cut between waves: after one workgroup barrier, the lanes chosen
@@ -510,7 +512,7 @@ gemv_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
       if constexpr (GATED) {
         res[comb_row * M + m] = sum;
       } else {
-        y[(size_t)m * n + wg_r0 + comb_row] = float_to_half_bits(sum);
+        store_result(y, (size_t)m * n + wg_r0 + comb_row, wg_r0 + comb_row, sum, epi...);
       }
     }
   }
@@ -531,14 +533,14 @@ gemv_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
   }
 }
 
-template <int M, bool GATED>
+template <int M, bool GATED, typename... Epi>
 hipError_t launch_gemv_m(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                          int n, int k, int group, const GemvPlan& plan, const DeviceInfo& dev,
-                         hipStream_t stream) {
+                         hipStream_t stream, const Epi&... epi) {
   static std::atomic<uint64_t> attr_set{0};   // one bit per device
   const uint64_t bit = 1ull << (dev.device & 63);
   if (!(attr_set.load(std::memory_order_acquire) & bit)) {
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv_kernel<M, GATED>),
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemv_kernel<M, GATED, Epi...>),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_acq_rel);
@@ -546,8 +548,8 @@ hipError_t launch_gemv_m(const uint16_t* x, const uint32_t* packed, const uint16
   const int gshift = group == 128 ? 2 : 0;   // log2(group / 32)
   const uint32_t sc_shift = (uint32_t)(reinterpret_cast<uintptr_t>(scales) & 15u);
   const uint16_t* sc_aligned = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(scales) - sc_shift);
-  return launch_kernel(gemv_kernel<M, GATED>, dim3(plan.blocks), dim3(kGemvThreads), plan.lds, stream, x, packed,
-                       sc_aligned, y, n, k, gshift, plan.rows_base, plan.rows_extra, sc_shift);
+  return launch_kernel(gemv_kernel<M, GATED, Epi...>, dim3(plan.blocks), dim3(kGemvThreads), plan.lds, stream, x, packed,
+                       sc_aligned, y, n, k, gshift, plan.rows_base, plan.rows_extra, sc_shift, epi...);
 }
 
 size_t plan_lds(int m, int units, int k, int group, int blocks, int unit) {
@@ -608,6 +610,12 @@ hipError_t launch_gemv(const uint16_t* x, const uint32_t* packed, const uint16_t
     case 4: return launch_gemv_m<4, false>(x, packed, scales, y, n, k, group, plan, dev, stream);
     default: return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_gemv_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n,
+                              int k, int group, const LinearEpilogue& ep, const GemvPlan& plan, const DeviceInfo& dev,
+                              hipStream_t stream) {
+  return launch_gemv_m<1, false>(x, packed, scales, y, n, k, group, plan, dev, stream, ep);
 }
 
 }  // namespace w4a16

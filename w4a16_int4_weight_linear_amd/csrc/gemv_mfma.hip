@@ -56,6 +56,7 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 #include "mfma_operands.hpp"
 #include "wave_stamps.hpp"
 
@@ -122,18 +123,19 @@ __device__ inline f16x4 as_h4(uint32_t a, uint32_t b) { return __builtin_bit_cas
 // rows_base / rows_extra count row units: single rows, or (gate, up) row pairs
 // (GATED).  `scales` is rounded down to 16 bytes by the launcher and sc_shift
 // bytes added back here, so the 16-byte staging loads are aligned in memory.
-template <int M, int G, bool GATED, int D>
+// Epi: none, or the linear layer's epilogue (not GATED).
+template <int M, int G, bool GATED, int D, typename... Epi>
 __global__ void __launch_bounds__(kThreads)
 gemv_mfma_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
                  const uint16_t* __restrict__ scales, uint16_t* __restrict__ y,
-                 int N, int K, int rows_base, int rows_extra, uint32_t sc_shift) {
+                 int N, int K, int rows_base, int rows_extra, uint32_t sc_shift, Epi... epi) {
   constexpr int kUnit = GATED ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // timeline stamps (profiling build only; the four-row, non-gated kernel)
-  constexpr bool kStamped = M == 4 && !GATED;
+  constexpr bool kStamped = M == 4 && !GATED && sizeof...(Epi) == 0;
   W4A16_STAMP_DECL;
   if (kStamped) W4A16_STAMP(0);
   const int lr = (lane & 3) + 4 * (lane >> 5);    // weight row of the block (B column)
@@ -368,7 +370,7 @@ gemv_mfma_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ pa
       const int row = kRows * bb + c;
       if (row < nr) {
 #pragma unroll
-        for (int m = 0; m < M; ++m) y[(size_t)m * N + r0 + row] = float_to_half_bits(v[m]);
+        for (int m = 0; m < M; ++m) store_result(y, (size_t)m * N + r0 + row, r0 + row, v[m], epi...);
       }
     }
   }
@@ -378,12 +380,12 @@ gemv_mfma_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ pa
   }
 }
 
-template <int M, int G, bool GATED, int D>
+template <int M, int G, bool GATED, int D, typename... Epi>
 hipError_t launch_d(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n, int k,
-                    int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream) {
+                    int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream, const Epi&... epi) {
   static std::atomic<uint64_t> attr_set{0};   // one bit per device
   const uint64_t bit = 1ull << (dev.device & 63);
-  auto kern = gemv_mfma_kernel<M, G, GATED, D>;
+  auto kern = gemv_mfma_kernel<M, G, GATED, D, Epi...>;
   if (!(attr_set.load(std::memory_order_acquire) & bit)) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_lds);
@@ -394,26 +396,27 @@ hipError_t launch_d(const uint16_t* x, const uint32_t* packed, const uint16_t* s
   const uint32_t sc_shift = (uint32_t)(reinterpret_cast<uintptr_t>(scales) & 15u);
   const uint16_t* sc_aligned = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(scales) - sc_shift);
   return launch_kernel(kern, dim3(blocks), dim3(kThreads), lds, stream, x, packed, sc_aligned, y, n, k,
-                       units / blocks, units % blocks, sc_shift);
+                       units / blocks, units % blocks, sc_shift, epi...);
 }
 
-template <int M, int G, bool GATED>
+template <int M, int G, bool GATED, typename... Epi>
 hipError_t launch_m(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n, int k,
-                    int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream) {
+                    int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream, const Epi&... epi) {
   // units per wave of the largest workgroup: 8-row blocks x 256-k lines over the waves
   const int unit = GATED ? 2 : 1;
   const int per = n / unit;
   const int rows = unit * (per / blocks + (per % blocks ? 1 : 0));
   const int upw = ((rows + kRows - 1) / kRows) * ((k + KL - 1) / KL) / kWaves;
-  return upw <= kShallowUnits ? launch_d<M, G, GATED, kShallowDepth>(x, packed, scales, y, n, k, blocks, lds, dev, stream)
-                              : launch_d<M, G, GATED, kDepth>(x, packed, scales, y, n, k, blocks, lds, dev, stream);
+  return upw <= kShallowUnits
+             ? launch_d<M, G, GATED, kShallowDepth>(x, packed, scales, y, n, k, blocks, lds, dev, stream, epi...)
+             : launch_d<M, G, GATED, kDepth>(x, packed, scales, y, n, k, blocks, lds, dev, stream, epi...);
 }
 
-template <int M, bool GATED>
+template <int M, bool GATED, typename... Epi>
 hipError_t launch_g(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n, int k,
-                    int group, int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream) {
-  return group == 32 ? launch_m<M, 32, GATED>(x, packed, scales, y, n, k, blocks, lds, dev, stream)
-                     : launch_m<M, 128, GATED>(x, packed, scales, y, n, k, blocks, lds, dev, stream);
+                    int group, int blocks, size_t lds, const DeviceInfo& dev, hipStream_t stream, const Epi&... epi) {
+  return group == 32 ? launch_m<M, 32, GATED>(x, packed, scales, y, n, k, blocks, lds, dev, stream, epi...)
+                     : launch_m<M, 128, GATED>(x, packed, scales, y, n, k, blocks, lds, dev, stream, epi...);
 }
 
 }  // namespace
@@ -453,6 +456,17 @@ hipError_t launch_gemv_mfma(const uint16_t* x, const uint32_t* packed, const uin
     case 2: return launch_g<2, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream);
     case 3: return launch_g<3, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream);
     case 4: return launch_g<4, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_gemv_mfma_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                                   int m, int n, int k, int group, const LinearEpilogue& ep, int blocks, size_t lds,
+                                   const DeviceInfo& dev, hipStream_t stream) {
+  switch (m) {
+    case 2: return launch_g<2, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
+    case 3: return launch_g<3, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
+    case 4: return launch_g<4, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
     default: return hipErrorInvalidValue;
   }
 }

@@ -8,6 +8,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/w4a16.h"
+
 namespace w4a16 {
 
 struct DeviceInfo {
@@ -77,6 +79,42 @@ size_t gemm_swiglu_workspace_bytes(int m, int n_out, int k, const DeviceInfo& de
 hipError_t launch_gemm_swiglu(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
                               uint16_t* z, int m, int n_out, int k, int group, void* workspace,
                               const DeviceInfo& dev, hipStream_t stream);
+
+// ---- the linear layer: the same products with z = product + bias, y = act(z) + residual ----
+// bias [n] and residual [m, n] (or y itself) may be null; pre [m, n] (or null) receives z.
+struct LinearEpilogue {
+  const uint16_t* bias;
+  const uint16_t* residual;
+  uint16_t* pre;
+  int act;                 // W4A16_ACT_*
+#ifdef __HIPCC__
+  __device__ void skip_rows(int rows, int n) {
+    if (residual) residual += (size_t)rows * n;
+    if (pre) pre += (size_t)rows * n;
+  }
+#endif
+};
+hipError_t launch_gemv_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n,
+                              int k, int group, const LinearEpilogue& ep, const GemvPlan& plan, const DeviceInfo& dev,
+                              hipStream_t stream);                                        // one row
+hipError_t launch_gemv_mfma_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y,
+                                   int m, int n, int k, int group, const LinearEpilogue& ep, int blocks, size_t lds,
+                                   const DeviceInfo& dev, hipStream_t stream);            // two to four
+hipError_t launch_linear_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                                int n, int k, int group, const LinearEpilogue& ep, const DeviceInfo& dev,
+                                hipStream_t stream);                                      // blocks of 16, one launch
+size_t gemm_linear_workspace_bytes(int m, int n, int k, const DeviceInfo& dev);
+hipError_t launch_gemm_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
+                              int n, int k, int group, const LinearEpilogue& ep, void* workspace, const DeviceInfo& dev,
+                              hipStream_t stream);
+
+// ---- gradient of its epilogue (linear_grad.hip) ----
+// dpre [m, n] = dy act'(pre) (act none: neither dpre nor pre), dbias [n] (or null) its column sums
+// before rounding.  padded, if not null, receives dpre too, rows padded with zeros to a multiple of 8.
+// The workspace, needed where linear_grad_workspace_bytes says so, begins with the counters.
+size_t linear_grad_workspace_bytes(int m, int n, bool bias);
+hipError_t launch_linear_grad(const uint16_t* dy, const uint16_t* pre, uint16_t* dpre, uint16_t* padded, float* dbias,
+                              int m, int n, int act, uint32_t* counters, float* partials, hipStream_t stream);
 
 // ---- workspaces of the feed-forward block's operators ----
 // A workspace begins with arrival counters, all 0 between calls (zero-filled once by the
@@ -148,6 +186,24 @@ hipError_t launch_moe_route(const int32_t* ids, int pairs, int topk, int experts
                             int32_t* pair_token, int32_t* pair_row, const DeviceInfo& dev, hipStream_t stream);
 hipError_t launch_moe_combine(const uint16_t* y_pairs, const int32_t* pair_row, const float* weights, uint16_t* out,
                               int tokens, int topk, int n, int rows, hipStream_t stream);
+
+// ---- router's choice and its gradient (moe_topk.hip) ----
+// logits [tokens, experts], fp16 (half) or fp32; ids and weights [tokens, topk].
+constexpr int kMoeTopkExperts = 1024, kMoeTopkSlots = 64;      // most experts, most slots
+hipError_t launch_moe_topk(const void* logits, bool half, int32_t* ids, float* weights, int tokens, int experts,
+                           int topk, bool renormalize, hipStream_t stream);
+hipError_t launch_moe_topk_backward(const float* dweights, const void* logits, bool half, const int32_t* ids,
+                                    const float* weights, void* dlogits, int tokens, int experts, int topk,
+                                    bool renormalize, hipStream_t stream);
+
+// ---- the routed experts' feed-forward for a few tokens (moe_ffn.hip) ----
+// residual may be null, or y itself.  The workspace needs no initial state behind its counters.
+constexpr int kMoeFfnTokens = 64, kMoeFfnPairs = 512;          // most tokens, most (token, slot) pairs
+size_t moe_ffn_workspace_bytes(int pairs, int inter);
+hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
+                          const uint16_t* gate_up_scales, const uint32_t* down, const uint16_t* down_scales,
+                          const uint16_t* residual, uint16_t* y, int tokens, int topk, int experts, int hidden,
+                          int inter, int group, void* workspace, hipStream_t stream);
 
 // ---- streaming-read HBM probe (probe.hip) ----
 int probe_sink_words(const DeviceInfo& dev);
