@@ -34,8 +34,8 @@ int ffn_sizes(int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32
     return W4A16_ERR_SHAPE;
   if (hidden < 0 || hidden > kMaxDim || hidden % group || inter < group || inter > kMaxDim || inter % group)
     return W4A16_ERR_SHAPE;
-  // one expert's weights, and what the kernels hand on of all pairs, in 32-bit offsets
-  if (inter * hidden >= kMaxBufferBytes || 4 * kMoeFfnPairs * inter >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
+  // one expert's weights in 32-bit offsets
+  if (inter * hidden >= kMaxBufferBytes) return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }
 
@@ -81,7 +81,7 @@ w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, 
 
 size_t w4a16_moe_ffn_workspace_bytes(int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32_t group) {
   if (ffn_sizes(tokens, topk, hidden, inter, group) != W4A16_OK || tokens == 0 || hidden == 0) return 0;
-  return w4a16::moe_ffn_workspace_bytes((int)(tokens * topk), (int)inter);
+  return w4a16::moe_ffn_workspace_bytes((int)(tokens * topk), (int)hidden, (int)inter);
 }
 
 w4a16_status w4a16_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
@@ -98,7 +98,7 @@ w4a16_status w4a16_moe_ffn(const uint16_t* x, const int32_t* ids, const float* w
       !aligned(gate_up_scales, 2) || !aligned(down_scales, 2) || !aligned(ids, 4) || !aligned(weights, 4) ||
       !aligned(workspace, 16))
     return W4A16_ERR_ALIGN;
-  const size_t need = w4a16::moe_ffn_workspace_bytes((int)(tokens * topk), (int)inter);
+  const size_t need = w4a16::moe_ffn_workspace_bytes((int)(tokens * topk), (int)hidden, (int)inter);
   if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE;
   // (the residual's elements are read by the threads that then write y's: it may be y itself; an
   // expert's weights are below 2 GiB and experts below 2^31: the banks' sizes fit 64 bits)
@@ -111,7 +111,7 @@ w4a16_status w4a16_moe_ffn(const uint16_t* x, const int32_t* ids, const float* w
   w4a16::DeviceInfo dev;
   if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
   return status_of(w4a16::launch_moe_ffn(x, ids, weights, gate_up, gate_up_scales, down, down_scales, residual, y,
-                                         (int)tokens, topk, experts, (int)hidden, (int)inter, group, workspace,
+                                         (int)tokens, topk, experts, (int)hidden, (int)inter, group, workspace, dev,
                                          reinterpret_cast<hipStream_t>(stream)));
 }
 

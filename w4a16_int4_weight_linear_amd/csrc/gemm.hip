@@ -569,6 +569,13 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
         for (int nb = 0; nb < kNB; ++nb) acc[i][nb] = sum[i][nb] + gscale[nb] * acc[i][nb];
     }
 
+    // (ahead of the next item's loads, which it would wait behind)
+    float bias = 0.0f;
+    auto load_bias = [&](const LinearEpilogue& le) {
+      if (le.bias && nw + li < N) bias = half_bits_to_float(le.bias[nw + li]);
+    };
+    (load_bias(epi), ...);
+
     // the next item's first loads (stages 0 and 1 and the windows are free
     // once the last step's barrier has passed)
     if (item + 1 < n_items) {
@@ -580,39 +587,49 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
     if (dp && EPI == kEpiLinear) {
       // The sums through LDS as fp32 (stage 2, 32 rows of the wave at a time), so that a lane has
       // eight neighbouring columns of a row: whole 16-byte accesses to y, pre and residual, and one
-      // rounding of act(z) + residual.
+      // rounding of act(z) + residual.  The loop over the 32-row blocks stays a loop (the accumulators
+      // move down a block each time): unrolled, five activations make its code too long to inline.
       constexpr int kPitch = kWaveN * 4 + 16;
       static_assert(kWaves * 32 * kPitch <= kStage, "epilogue slabs exceed stage 2");
       uint8_t* ep = stage2 + wave * 32 * kPitch;
       auto finish = [&](const LinearEpilogue& le) {
-        const float bias = le.bias && nw + li < N ? half_bits_to_float(le.bias[nw + li]) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kMB; ++i) {
+#pragma unroll 1
+        for (int mb = m0; mb < m0 + BM; mb += 32) {
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            *reinterpret_cast<float*>(ep + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch + li * 4) = acc[i][0][r] + bias;
+            *reinterpret_cast<float*>(ep + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch + li * 4) = acc[0][0][r] + bias;
+#pragma unroll
+          for (int i = 0; i + 1 < kMB; ++i) acc[i][0] = acc[i + 1][0];
           // (a wave's LDS accesses complete in order: its own writes are visible)
           if (N & 7) {          // rows of any alignment: two rows of 32 columns per access
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+              float v[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int row = 2 * j + h, m = m0 + 32 * i + row, n = nw + li;
-              const float v = *reinterpret_cast<const float*>(ep + row * kPitch + li * 4);
-              if (m < M && n < N) {
-                const size_t at = (size_t)m * N + n;
-                if (le.pre) le.pre[at] = float_to_half_bits(v);
-                const float o = activate(le.act, v);
-                y[at] = float_to_half_bits(le.residual ? o + half_bits_to_float(le.residual[at]) : o);
+              for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(ep + (j0 + 2 * j + h) * kPitch + li * 4);
+              if (le.pre) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (mb + j0 + 2 * j + h < M && nw + li < N)
+                    le.pre[(size_t)(mb + j0 + 2 * j + h) * N + nw + li] = float_to_half_bits(v[j]);
+              }
+              activate(le.act, v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const size_t at = (size_t)(mb + j0 + 2 * j + h) * N + nw + li;
+                if (mb + j0 + 2 * j + h < M && nw + li < N)
+                  y[at] = float_to_half_bits(le.residual ? v[j] + half_bits_to_float(le.residual[at]) : v[j]);
               }
             }
             continue;
           }
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 2; ++j) {
-            const int row = 16 * j + (lane >> 2), c = lane & 3, m = m0 + 32 * i + row, n = nw + 8 * c;
-            if (m >= M || n >= N) continue;
+            const int row = 16 * j + (lane >> 2), c = lane & 3, m = mb + row, n = nw + 8 * c;
+            const bool in = m < M && n < N;
             const size_t at = (size_t)m * N + n;
             f16x8 res = f16x8{};
-            if (le.residual) res = *reinterpret_cast<const f16x8*>(le.residual + at);
+            if (le.residual && in) res = *reinterpret_cast<const f16x8*>(le.residual + at);
             float v[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -621,14 +638,15 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
               for (int u = 0; u < 4; ++u) v[4 * q + u] = t[u];
             }
             f16x8 o;
-            if (le.pre) {
+            if (le.pre && in) {
 #pragma unroll
               for (int u = 0; u < 8; ++u) o[u] = (_Float16)v[u];
               *reinterpret_cast<f16x8*>(le.pre + at) = o;
             }
+            activate(le.act, v);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o[u] = (_Float16)(activate(le.act, v[u]) + (float)res[u]);
-            *reinterpret_cast<f16x8*>(y + at) = o;
+            for (int u = 0; u < 8; ++u) o[u] = (_Float16)(v[u] + (float)res[u]);
+            if (in) *reinterpret_cast<f16x8*>(y + at) = o;
           }
         }
       };

@@ -62,12 +62,13 @@ linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__
       for (int i = 0; i < 8; ++i) d[i] = (float)v[i];
       if constexpr (SLOPE) {
         const f16x8 z = __builtin_nontemporal_load(reinterpret_cast<const f16x8*>(pre + row + col(0)));
+        float zf[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) zf[i] = (float)z[i];
+        times_slope(act, zf, d);
         f16x8 o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d[i] *= activation_slope(act, (float)z[i]);
-          o[i] = (_Float16)d[i];
-        }
+        for (int i = 0; i < 8; ++i) o[i] = (_Float16)d[i];
         *reinterpret_cast<f16x8*>(dpre + row + col(0)) = o;
       }
     } else {
@@ -78,9 +79,9 @@ linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__
         z[i] = SLOPE && col(i) < N ? half_bits_to_float(pre[row + col(i)]) : 0.0f;
       }
       if constexpr (SLOPE) {
+        times_slope(act, z, d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          d[i] *= activation_slope(act, z[i]);
           if (col(i) < N) dpre[row + col(i)] = float_to_half_bits(d[i]);
           if (padded && col(i) < np) padded[(size_t)r * np + col(i)] = float_to_half_bits(col(i) < N ? d[i] : 0.0f);
         }

@@ -6,36 +6,114 @@
 // With up to 512 (token, slot) pairs nearly every expert that is used is used once or twice, so
 // the layer is a stream of the used experts' weights: 1.77 MB each at 2048 x 512, g32.
 //
-// * gate/up: one workgroup per (pair, 32 weight rows).  Every wave reads all pairs' experts itself;
-//   the first pair of an expert does the expert's work for all its pairs, the others leave at once.
-//   So no routing kernel runs first, and an expert's weights are read once.  A wave owns 8 rows.
-// * down and combine: one workgroup per 8 output columns, for all experts: a wave takes every eighth
-//   used expert, the pairs' results meet in LDS, and the router's weights add them in slot order
-//   with the residual, one rounding at the end: no partial results in memory, no atomics.
+// * Few pairs (kDirectPairs): two kernels, each pair by itself.  Gate/up: a workgroup per (pair, 32 weight
+//   rows).  Down and combine: a workgroup per 8 output columns, a wave per pair; the pairs' results meet
+//   in LDS and the router's weights add them in slot order with the residual.
+// * More pairs: three kernels.  In both products the workgroups walk over (block of up to four pairs of one
+//   expert, band of weight rows), the next one's loads in flight while this one is computed, so an expert's
+//   weights are read once for every four of its pairs; each workgroup sorts the pairs into blocks
+//   itself (group_pairs).  A third kernel adds a token's results with the router's weights.
+// No atomics on results and no order that depends on timing: a token's output has the same bits in any batch
+// of the same kind.
 //
-// Both run on v_mfma_f32_4x4x4_16b_f16: block b of 16 is four weight rows (B columns) at 32 k of their
+// All products run on v_mfma_f32_4x4x4_16b_f16: block b of 16 is four weight rows (B columns) at 32 k of their
 // own (one 16-byte load per lane: 4 rows x 256 contiguous bytes), times four activation rows (A).  A
 // lane's 32 k lie in one scale group, so the codes enter as the integers u - 8 (exact in fp16) and
-// the scale is applied to the fp32 result: weights are exact.
+// the scale is applied to the fp32 result: weights are exact.  The MFMA wants neighbouring lanes on
+// different weight rows; loaded so, every four lanes touch four cache lines.  So weights and scales are loaded
+// with sixteen lanes side by side on a row and the lanes are permuted afterwards (spread_rows).
 //
 // h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11 (22 bits, |h| up to 2^24):
-// rounded once to fp16 it would add as much error again as the rounding of y.  The parts are two
-// of the four A rows, so they cost no extra instruction while an expert has one or two pairs.
+// rounded once to fp16 it would add as much error again as the rounding of y.
+#include <type_traits>
+
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
 #include "mfma_operands.hpp"
+#include "tile_gemm.hpp"
 
 namespace w4a16 {
 namespace {
 
 constexpr int kStepK = 512;                      // k of one step: 16 chunks of 32
-constexpr int kRowsWave = 8;                     // weight rows of a wave (two groups of four)
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kBlock = 4;                        // pairs of a block: the A rows
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+static_assert(kThreads >= kMoeFfnPairs && kThreads >= 8 * kMoeFfnTokens, "one pair, and one output, per thread");
 
-// What the first kernel leaves about a pair: the next pair of the same expert, and whether it is the first.
-constexpr uint32_t kNoPair = 0xFFFFu, kFirst = 0x10000u;
 constexpr float kHScale = 0x1p-8f, kLoScale = 0x1p11f;
+
+// The pairs in blocks of up to four of one expert each.
+struct Blocks {
+  unsigned long long val[2 * kMoeFfnPairs];      // of the expert in this place: its pairs per wave (a byte
+                                                 // each), then its first block
+  int key[2 * kMoeFfnPairs];                     // an expert's place (open addressing; -1: free)
+  int expert[kMoeFfnPairs];                      // of block b
+  uint16_t size[kMoeFfnPairs];                   // its pairs: 1 .. 4,
+  uint16_t pair[kMoeFfnPairs * kBlock];          // pair[4 b + i]
+  uint32_t wave_sum[kWaves];
+};
+
+// Sum of eight bytes (up to 512).
+__device__ inline uint32_t byte_sum(unsigned long long v) {
+  v = (v & 0x00FF00FF00FF00FFull) + ((v >> 8) & 0x00FF00FF00FF00FFull);
+  return (uint32_t)((v * 0x0001000100010001ull) >> 48);
+}
+
+// Sorts the pairs; returns the number of blocks.  Blocks and their pairs are in the pairs' order, the same in
+// every workgroup (which share the blocks out).  Pairs whose id is no expert are in no block.
+__device__ inline int group_pairs(Blocks& s, const int32_t* __restrict__ ids, int pairs, int experts) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int e = tid < pairs ? ids[tid] : -1;
+  const bool known = e >= 0 && e < experts;
+#pragma unroll
+  for (int i = 0; i < 2 * kMoeFfnPairs; i += kThreads) {
+    s.key[tid + i] = -1;
+    s.val[tid + i] = 0;
+  }
+  __syncthreads();
+  uint32_t at = 0, rank = 0;
+  if (known) {
+    // (512 pairs at most in 1024 places: a free one is found)
+    at = ((uint32_t)e * 0x9E3779B1u) >> 22;
+    for (int k = atomicCAS(&s.key[at], -1, e); k != -1 && k != e; k = atomicCAS(&s.key[at], -1, e)) at = (at + 1) & 1023u;
+    atomicAdd(&s.val[at], 1ull << (8 * wave));
+  }
+  for (int l = 0; l < pairs - 64 * wave && l < 63; ++l)     // the wave's pairs of this expert before this one
+    rank += lane > l && __builtin_amdgcn_readlane(e, l) == e ? 1u : 0u;
+  __syncthreads();
+  const unsigned long long counts = known ? s.val[at] : 0ull;
+  const uint32_t count = byte_sum(counts);
+  if (known) rank += byte_sum(counts & ((1ull << (8 * wave)) - 1));    // (and those of the waves before: eight at most)
+  const uint32_t mine = known && rank == 0 ? (count + kBlock - 1) / kBlock : 0u;      // blocks of the expert
+  uint32_t upto = mine;                                     // sum over this wave's lanes so far
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t v = (uint32_t)__shfl_up((int)upto, d, 64);
+    if (lane >= d) upto += v;
+  }
+  if (lane == 63) s.wave_sum[wave] = upto;
+  __syncthreads();
+  uint32_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? s.wave_sum[w] : 0u;
+    total += s.wave_sum[w];
+  }
+  if (mine) s.val[at] = before + upto - mine;
+  __syncthreads();
+  if (known) {
+    const uint32_t b = (uint32_t)s.val[at] + rank / kBlock;
+    s.pair[kBlock * b + rank % kBlock] = (uint16_t)tid;
+    if (rank % kBlock == 0) {
+      s.expert[b] = e;
+      s.size[b] = (uint16_t)min((uint32_t)kBlock, count - rank);
+    }
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane((int)total);
+}
 
 // The eight codes of a packed word as fp16 integers u - 8, in the order of permute_a: a nibble
 // under the exponent of 1024 (mantissa bits 0-3) or of 64 (bits 4-7), less 1032 or 72.
@@ -51,331 +129,565 @@ __device__ inline void decode_codes(uint32_t q, f16x4& a, f16x4& b) {
 }
 
 // Four activation rows times a lane's four weight rows over its chunk of 32 k: a[w] is the lane's
-// activations of word w, in permute_a's order.
-__device__ inline f32x4 chunk_product(const u32x4& wv, const u32x4 (&a)[4]) {
-  f32x4 t = f32x4{};
+// activations of word w, in permute_a's order.  With two sets of rows the codes are decoded once.
+template <int SETS>
+__device__ inline void chunk_product(const u32x4& wv, const u32x4 (&a)[SETS][4], f32x4 (&t)[SETS]) {
+#pragma unroll
+  for (int q = 0; q < SETS; ++q) t[q] = f32x4{};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     f16x4 b0, b1;
     decode_codes(wv[w], b0, b1);
-    t = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[w].x, a[w].y}), b0, t, 0, 0, 0);
-    t = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[w].z, a[w].w}), b1, t, 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < SETS; ++q) {
+      t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q][w].x, a[q][w].y}), b0, t[q], 0, 0, 0);
+      t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q][w].z, a[q][w].w}), b1, t[q], 0, 0, 0);
+    }
   }
-  return t;
 }
 
-// Sum over a lane's sixteen chunks (lanes 4 c + column); every lane gets it, the same bits (8 before
-// 4: the sums then have a period of 8 lanes, so every lane adds the same two), whichever lane
-// serves a token.
-__device__ inline float chunk_sum(float v) {
-  v = dpp_add<0x128>(v);   // row_ror:8
-  v = dpp_add<0x124>(v);   // row_ror:4
-  v += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401F));   // lane ^ 16
-  v += __shfl_xor(v, 32, 64);
+// From the lane that loaded it (row l / 16, chunk l % 16) to the one that multiplies it (row l % 4, chunk l / 4).
+__device__ inline uint32_t spread_rows(uint32_t v, int lane) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(((lane & 3) << 6) + (lane & ~3), (int)v);
+}
+__device__ inline u32x4 spread_rows(const u32x4& v, int lane) {
+  return u32x4{spread_rows(v.x, lane), spread_rows(v.y, lane), spread_rows(v.z, lane), spread_rows(v.w, lane)};
+}
+
+// Four values' sums over the sixteen chunks (lanes 4 c + column): a lane gets that of value
+// sum_index(lane).  Two lane swaps halve the lanes of a value while two values share a register, then
+// two DPP steps finish (8 before 4: the sums then have a period of 8 lanes, so every lane adds the
+// same two).  All four are added in the same order, so a pair's result has the same bits whichever
+// A row serves it.  The swaps are inline assembly because both registers are outputs (the compiler's
+// builtins lose one of them); the s_nop give the wait states around them.
+__device__ inline int sum_index(int lane) { return ((lane >> 3) & 2) | (lane >> 5); }
+__device__ inline float chunk_sums(f32x4 v) {
+  float a = v[0], b = v[1], c = v[2], d = v[3];
+  asm volatile("s_nop 1\n\tv_permlane32_swap_b32 %0, %1\n\tv_permlane32_swap_b32 %2, %3\n\ts_nop 1"
+               : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+  float s = a + b, t = c + d;                    // lanes 0-31: values 0 and 2, 32-63: 1 and 3
+  asm volatile("s_nop 1\n\tv_permlane16_swap_b32 %0, %1\n\ts_nop 1" : "+v"(s), "+v"(t));
+  s += t;                                        // rows of sixteen lanes: values 0, 2, 1, 3
+  s = dpp_add<0x128>(s);                         // row_ror:8
+  return dpp_add<0x124>(s);                      // row_ror:4
+}
+
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// A load's offset, or one outside every buffer.  (The empty asm keeps the choice a value: as a branch
+// around the load, every other load would be waited for where the branch joins.)
+__device__ inline uint32_t offset_if(bool in, uint32_t off) {
+  uint32_t v = in ? off : kOutOfRange;
+  asm("" : "+v"(v));
   return v;
 }
 
-// ---- gate/up ----
-constexpr int kUpThreads = 256, kUpWaves = kUpThreads / 64;
-constexpr int kUpRows = kUpWaves * kRowsWave;    // weight rows of a workgroup
-constexpr int kUpSteps = 4;                      // steps of a staged piece of x
-constexpr int kUpK = kUpSteps * kStepK;          // 2048 k
-constexpr int kUpTokens = 4;                     // pairs per pass: the A rows
-constexpr int kXPitch = kUpK * 2 + 16;           // bytes per staged row: rows shift by 4 banks
 
-// NC: 64-pair blocks (pairs <= 64 NC).  h: [pair][2][inter] fp16.
-template <int G, int NC>
-__global__ void __launch_bounds__(kUpThreads)
-moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
-                   const uint16_t* __restrict__ scales, uint16_t* __restrict__ h, uint32_t* __restrict__ link,
-                   int pairs, int topk, int experts, int rows, int K) {
-  __shared__ __attribute__((aligned(16))) uint8_t xs[kUpTokens * kXPitch];
-  __shared__ uint16_t lists[kUpWaves][64 * NC];
+// A value as the two parts of h.
+__device__ inline void split_h(float v, uint16_t& hi, uint16_t& lo) {
+  const _Float16 h = (_Float16)v;
+  hi = __builtin_bit_cast(uint16_t, h);
+  // (past fp16's range the upper part says it alone)
+  lo = __builtin_fabsf((float)h) <= 65504.0f ? float_to_half_bits((v - (float)h) * kLoScale) : (uint16_t)0;
+}
+__device__ inline float silu_product(float gate, float up) {
+  return gate * __builtin_amdgcn_rcpf(1.0f + __expf(-gate)) * up;
+}
+// The lane's neighbour in the weight rows: the up row of an even lane's gate row.
+__device__ inline float next_row(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xf, 0xf, false));
+}
+// Place of element k of an h row in its step, in the order of the A loads: word, chunk, row of `rows`, permute_a's order.
+__device__ inline uint32_t h_place(uint32_t k, uint32_t rows, uint32_t row) {
+  const uint32_t c = k % kStepK / 32, w = k % 32 / 8, j = k % 8;
+  return ((w * 16 + c) * rows + row) * 8 + (((j & 1) << 2) | (j & 2) | (j >> 2));
+}
+__host__ __device__ inline int h_steps(int inter) { return (inter + kStepK - 1) / kStepK; }
+
+// ---- few pairs: each by itself ----
+constexpr int kDirectPairs = 64;
+constexpr int kBandRows = 4 * kWaves;            // gate/up rows of a workgroup: four per wave
+constexpr int kXSteps = 4;                       // steps of a staged piece of x
+constexpr int kXK = kXSteps * kStepK;            // 2048 k
+constexpr uint32_t kDirectStep = 2 * kStepK * 2; // bytes of a pair's h per step: upper and lower parts
+
+// h: [pair][step] blocks of kDirectStep bytes (h_place, two rows).
+template <int G>
+__global__ void __launch_bounds__(kThreads)
+moe_gate_up_direct_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids,
+                          const uint32_t* __restrict__ packed, const uint16_t* __restrict__ scales,
+                          uint16_t* __restrict__ h, int topk, int experts, int rows, int K) {
+  __shared__ __attribute__((aligned(16))) uint8_t xs[2][2 * kXK];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int li = lane & 3, c = lane >> 2;        // weight row (and A row), chunk
-  const int band = blockIdx.x, p = blockIdx.y;
-
-  // ---- this pair's expert, and the pairs that share it ----
-  int id[NC];
-#pragma unroll
-  for (int b = 0; b < NC; ++b) id[b] = 64 * b + lane < pairs ? ids[64 * b + lane] : -1;
-  int e = -1;
-#pragma unroll
-  for (int b = 0; b < NC; ++b)
-    if (b == p >> 6) e = __builtin_amdgcn_readlane(id[b], p & 63);
-  const bool known = e >= 0 && e < experts;
-  int count = 0;
-  uint32_t next = kNoPair;
-  bool first = known;
-  uint16_t* list = lists[wave];                  // (each wave's own: no barrier)
-#pragma unroll
-  for (int b = 0; b < NC; ++b) {
-    const uint64_t m = __builtin_amdgcn_ballot_w64(id[b] == e && known);
-    const uint64_t at_p = b == p >> 6 ? 1ull << (p & 63) : 0ull;
-    const uint64_t below = b < p >> 6 ? ~0ull : (b == p >> 6 ? at_p - 1 : 0ull);
-    if (m & below) first = false;
-    const uint64_t above = m & ~below & ~at_p;
-    if (above && next == kNoPair) next = 64 * b + (uint32_t)__builtin_ctzll(above);
-    if (known && id[b] == e) list[count + __builtin_popcountll(m & ((1ull << lane) - 1))] = (uint16_t)(64 * b + lane);
-    count += __builtin_popcountll(m);
-  }
-  __builtin_amdgcn_wave_barrier();
-  if (band == 0 && threadIdx.x == 0) link[p] = next | (first ? kFirst : 0u);
-  if (!first) return;
-
+  const int wave = uniform(threadIdx.x >> 6);
+  const int c = lane >> 2, p = blockIdx.y, r0 = blockIdx.x * kBandRows;
+  const int e = ids[p];
+  if (e < 0 || e >= experts) return;
   const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
-  const __amdgpu_buffer_rsrc_t wres =
-      make_rsrc(reinterpret_cast<const uint8_t*>(packed) + (size_t)e * rows * row_w, (uint32_t)rows * row_w);
-  const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + (size_t)e * rows * spr, (uint32_t)rows * spr * 2u);
-  const int r0 = band * kUpRows + wave * kRowsWave;
-  const int pieces = (K + kUpK - 1) / kUpK;
-  const int inter = rows >> 1;
-
-  u32x4 raw[kUpSteps][2];
-  uint32_t sc[kUpSteps][2];
-  // (a row past the expert's last, or a chunk past K, reads zero codes and a zero scale)
-  auto load_weights = [&](int piece) {
+  const size_t first = (size_t)e * rows + r0;
+  const uint32_t lrow = (uint32_t)(wave * 4 + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
+  const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
+  const uint16_t* xp = x + (size_t)(p / topk) * K;
+  float acc = 0.0f;
+  for (int k0 = 0, buf = 0; k0 < K; k0 += kXK, buf ^= 1) {
+    // every thread stages 8 bytes of the piece's 4 KB (and permutes them with its neighbour's)
+    const __amdgpu_buffer_rsrc_t xres = make_rsrc(xp + k0, (uint32_t)(K - k0) * 2u);
+    u32x4 xv = u32x4{};
+    if (wave < 4) xv = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xres, 16u * threadIdx.x, 0, 0));
+    const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
+                                                  (uint32_t)(rows - r0) * row_w - (uint32_t)k0 / 2);
+    const __amdgpu_buffer_rsrc_t sres =
+        make_rsrc(scales + first * spr + k0 / G, ((uint32_t)(rows - r0) * spr - (uint32_t)k0 / G) * 2u);
+    u32x4 wv[kXSteps];
+    uint32_t sc[kXSteps];
 #pragma unroll
-    for (int s = 0; s < kUpSteps; ++s)
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const uint32_t k = (uint32_t)(piece * kUpK + s * kStepK + 32 * c), r = (uint32_t)(r0 + 4 * g + li);
-        const bool in = k < (uint32_t)K;
-        raw[s][g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                  wres, in ? r * row_w + (k >> 1) : kOutOfRange, 0, kStream));
-        sc[s][g] = __builtin_amdgcn_raw_buffer_load_b16(sres, in ? (r * spr + k / G) * 2u : kOutOfRange, 0, 0);
-      }
-  };
-  for (int i0 = 0; i0 < count; i0 += kUpTokens) {
-    const int here = min(kUpTokens, count - i0);
-    f32x4 acc[2] = {f32x4{}, f32x4{}};
-    for (int piece = 0; piece < pieces; ++piece) {
-      // wave w stages row w of the pass
-      u32x4 xv[kUpSteps];
-      if (wave < here) {
-        const int token = __builtin_amdgcn_readfirstlane(list[i0 + wave]) / topk;
-        const uint16_t* src = x + (size_t)token * K;
-#pragma unroll
-        for (int s = 0; s < kUpSteps; ++s) {
-          const int k = piece * kUpK + s * kStepK + 8 * lane;
-          xv[s] = k < K ? *reinterpret_cast<const u32x4*>(src + k) : u32x4{};
-        }
-      }
-      if (pieces > 1 || i0 == 0) load_weights(piece);
-      if (piece > 0 || i0 > 0) __syncthreads();  // the rows staged before are read
-      if (wave < here) {
-#pragma unroll
-        for (int s = 0; s < kUpSteps; ++s)
-          *reinterpret_cast<u32x4*>(xs + wave * kXPitch + s * (2 * kStepK) + 16 * lane) = permute_a(xv[s]);
-      }
-      __syncthreads();
-      const uint8_t* xa = xs + min(li, here - 1) * kXPitch + 64 * c;
-#pragma unroll
-      for (int s = 0; s < kUpSteps; ++s) {
-        if (piece * kUpK + s * kStepK >= K) break;
-        u32x4 a[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) a[w] = *reinterpret_cast<const u32x4*>(xa + s * (2 * kStepK) + 16 * w);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const f32x4 t = chunk_product(raw[s][g], a);
-          const float f = half_bits_to_float(sc[s][g]);
-#pragma unroll
-          for (int i = 0; i < kUpTokens; ++i) acc[g][i] = __builtin_fmaf(f, t[i], acc[g][i]);
-        }
-      }
+    for (int s = 0; s < kXSteps; ++s) {
+      const bool in = (uint32_t)(k0 + s * kStepK) + 32u * lchunk < (uint32_t)K;     // (else: the next row's)
+      wv[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                            wres, offset_if(in, w_off) + (uint32_t)(kStepK / 2) * s, 0, kStream));
+      sc[s] = __builtin_amdgcn_raw_buffer_load_b16(sres, offset_if(in, s_off) + (uint32_t)(kStepK / G * 2) * s, 0, 0);
     }
-    // the lane of chunk 4 g + i and an even row stores output (row / 2) of pair i
-    float gate = 0.0f, up = 0.0f;
+    if (wave < 4) *reinterpret_cast<u32x4*>(xs[buf] + 16 * threadIdx.x) = permute_a(xv);
+    lds_barrier();
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+    for (int s = 0; s < kXSteps; ++s) {
+      if (k0 + s * kStepK >= K) break;
+      u32x4 a[1][4];
 #pragma unroll
-      for (int i = 0; i < kUpTokens; ++i) {
-        const float v = chunk_sum(acc[g][i]);
-        const float o = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0xB1, 0xf,
-                                                                              0xf, false));
-        if (c == 4 * g + i) {
-          gate = v;
-          up = o;
-        }
-      }
-    const int r = r0 + 4 * (c >> 2) + li, i = c & 3, o = r >> 1;
-    if (c < 8 && !(li & 1) && i < here && o < inter) {
-      const float v = gate / (1.0f + __expf(-gate)) * up * kHScale;
-      const _Float16 hi = (_Float16)v;
-      // (past fp16's range the upper part says it alone)
-      const _Float16 lo = __builtin_fabsf((float)hi) <= 65504.0f ? (_Float16)((v - (float)hi) * kLoScale) : (_Float16)0.f;
-      const int at = (o & ~7) + ((o & 1) << 2) + (o & 2) + ((o >> 2) & 1);   // permute_a's order
-      uint16_t* dst = h + (size_t)list[i0 + i] * 2 * inter + at;
-      dst[0] = __builtin_bit_cast(uint16_t, hi);
-      dst[inter] = __builtin_bit_cast(uint16_t, lo);
+      for (int w = 0; w < 4; ++w)
+        a[0][w] = *reinterpret_cast<const u32x4*>(xs[buf] + s * (2 * kStepK) + 64 * c + 16 * w);
+      f32x4 t[1];
+      chunk_product(spread_rows(wv[s], lane), a, t);
+      acc = __builtin_fmaf(half_bits_to_float(spread_rows(sc[s], lane)), t[0][0], acc);
     }
+  }
+  const float gate = chunk_sums(f32x4{acc, 0.f, 0.f, 0.f}), up = next_row(gate);
+  const uint32_t o = (uint32_t)(r0 + wave * 4 + lane) >> 1;      // (lanes 0 and 2)
+  if (lane < 4 && !(lane & 1) && o < (uint32_t)rows >> 1) {
+    uint16_t hi, lo;
+    split_h(silu_product(gate, up) * kHScale, hi, lo);
+    uint16_t* dst = h + ((size_t)p * h_steps(rows >> 1) + o / kStepK) * (kDirectStep / 2);
+    dst[h_place(o, 2, 0)] = hi;
+    dst[h_place(o, 2, 1)] = lo;
   }
 }
 
-// ---- down and combine ----
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64;
-static_assert(kDownThreads >= kMoeFfnPairs && kDownThreads >= 8 * kMoeFfnTokens, "one pair, and one output, per thread");
+constexpr int kDepth = 3;                        // steps in flight per wave
 
 template <int G>
-__global__ void __launch_bounds__(kDownThreads)
-moe_down_kernel(const uint16_t* __restrict__ h, const uint32_t* __restrict__ link, const int32_t* __restrict__ ids,
-                const float* __restrict__ weights, const uint32_t* __restrict__ packed,
-                const uint16_t* __restrict__ scales, const uint16_t* residual, uint16_t* y, int pairs, int topk,
-                int tokens, int experts, int N, int K) {
-  __shared__ float part[kMoeFfnPairs][8];        // a pair's result in the workgroup's columns
-  __shared__ int ids_l[kMoeFfnPairs];
-  __shared__ float weights_l[kMoeFfnPairs];
-  __shared__ uint32_t link_l[kMoeFfnPairs];
-  __shared__ uint16_t list[kMoeFfnPairs];        // the first pair of each used expert
-  __shared__ int counts[kDownWaves];
+__global__ void __launch_bounds__(kThreads)
+moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+                       const uint32_t* __restrict__ packed, const uint16_t* __restrict__ scales, const uint16_t* residual,
+                       uint16_t* y, int pairs, int topk, int tokens, int experts, int N, int K) {
+  __shared__ float part[kDirectPairs][8];        // a pair's result in the workgroup's columns, times its weight
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int li = lane & 3, c = lane >> 2;
-  const int n0 = blockIdx.x * 8;
-
-  const uint32_t my_link = tid < pairs ? link[tid] : 0u;
-  if (tid < pairs) {
-    link_l[tid] = my_link;
-    ids_l[tid] = ids[tid];
-    weights_l[tid] = weights[tid];
-  }
+  const int wave = uniform(tid >> 6);
+  const int li = lane & 3, c = lane >> 2, n0 = blockIdx.x * 8;
+  const int id = lane < pairs ? ids[lane] : -1;                  // every wave: all pairs
   // this thread's output, at the end: token tid / 8, column tid % 8
   const int ot = tid >> 3, on = n0 + (tid & 7);
   const bool out = ot < tokens && on < N;
   const float res = out && residual ? half_bits_to_float(residual[(size_t)ot * N + on]) : 0.0f;
-  const bool first = (my_link & kFirst) != 0;
-  const uint64_t firsts = __builtin_amdgcn_ballot_w64(first);
-  if (lane == 0) counts[wave] = __builtin_popcountll(firsts);
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kDownWaves; ++w) {
-    before += w < wave ? counts[w] : 0;
-    total += counts[w];
-  }
-  total = __builtin_amdgcn_readfirstlane(total);
-  if (first) list[before + __builtin_popcountll(firsts & ((1ull << lane) - 1))] = (uint16_t)tid;
-  __syncthreads();
+  const float weight = lane < pairs ? weights[lane] : 0.0f;
 
   const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
-  const int steps = (K + kStepK - 1) / kStepK;
-  const __amdgpu_buffer_rsrc_t hres = make_rsrc(h, (uint32_t)pairs * 2u * (uint32_t)K * 2u);
-  // one step: 512 k of the 8 columns for up to two pairs (p0; p1 or none) of one expert
+  const int steps = h_steps(K);
+  const uint32_t lrow = (uint32_t)lane >> 4, lchunk = (uint32_t)(lane & 15);
+  const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
   struct Step {
-    int it, p0, p1, e, s;
+    int pair, s;
   };
   struct Data {
-    u32x4 w[2], a[4];
+    u32x4 w[2], a[1][4];
     uint32_t sc[2];
-  };
-  auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  auto pair_of = [&](Step& st, int p0) {
-    st.p0 = p0;
-    st.p1 = uniform((int)(link_l[p0] & kNoPair));
-    st.s = 0;
-  };
-  auto item_of = [&](Step& st, int it) {
-    st.it = it;
-    if (it >= total) return;
-    pair_of(st, uniform(list[it]));
-    st.e = uniform(ids_l[st.p0]);
   };
   auto advance = [&](Step& st) {
     if (++st.s < steps) return;
-    const int p2 = st.p1 == (int)kNoPair ? (int)kNoPair : uniform((int)(link_l[st.p1] & kNoPair));
-    if (p2 != (int)kNoPair) pair_of(st, p2);
-    else item_of(st, st.it + kDownWaves);
+    st.s = 0;
+    st.pair += kWaves;
   };
-  auto load = [&](const Step& st, Data& d) {
-    const __amdgpu_buffer_rsrc_t wres =
-        make_rsrc(reinterpret_cast<const uint8_t*>(packed) + (size_t)st.e * N * row_w, (uint32_t)N * row_w);
-    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + (size_t)st.e * N * spr, (uint32_t)N * spr * 2u);
-    const uint32_t k = (uint32_t)(st.s * kStepK + 32 * c);
-    const bool in = k < (uint32_t)K;
+  auto load = [&](const Step& st, Data& d) __attribute__((always_inline)) {
+    const int p = st.pair < pairs ? st.pair : 0, k0 = st.s * kStepK;
+    const int e = __builtin_amdgcn_readlane(id, p);
+    const bool live = st.pair < pairs && e >= 0 && e < experts;
+    const size_t first = (size_t)(live ? e : 0) * N + n0;
+    const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
+                                                  live ? (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2 : 0u);
+    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
+                                                  live ? ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+    const bool in = (uint32_t)k0 + 32u * lchunk < (uint32_t)K;
+    const uint32_t wo = offset_if(in, w_off), so = offset_if(in, s_off);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const uint32_t r = (uint32_t)(n0 + 4 * g + li);
-      d.w[g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                             wres, in ? r * row_w + (k >> 1) : kOutOfRange, 0, kStream));
-      d.sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, in ? (r * spr + k / G) * 2u : kOutOfRange, 0, 0);
+      d.w[g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres, wo + 4u * g * row_w, 0, kStream));
+      d.sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, so + 8u * g * spr, 0, 0);
     }
-    // A rows: the upper parts of p0 and p1, then their lower parts (no p1: p0's again, not stored)
-    const uint32_t pair = (uint32_t)((li & 1) && st.p1 != (int)kNoPair ? st.p1 : st.p0);
-    const uint32_t at = ((pair * 2u + (uint32_t)(li >> 1)) * (uint32_t)K + k) * 2u;
+    // A rows: upper and lower parts, twice; chunks past K were never written
+    const __amdgpu_buffer_rsrc_t hres = make_rsrc(
+        reinterpret_cast<const uint8_t*>(h) + (size_t)(p * steps + st.s) * kDirectStep, live ? kDirectStep : 0u);
+    const uint32_t a_off = offset_if(k0 + 32 * c < K, 32u * c + 16u * (li & 1));
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      d.a[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, in ? at + 16u * w : kOutOfRange, 0, 0));
+      d.a[0][w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, a_off + 512u * w, 0, 0));
   };
-  f32x4 acc[2] = {f32x4{}, f32x4{}};
+  f32x4 acc = f32x4{};                           // upper and lower parts' sums, columns 0-3 and 4-7
   auto compute = [&](const Step& st, const Data& d) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const f32x4 t = chunk_product(d.w[g], d.a);
-      const float f = half_bits_to_float(d.sc[g]);
+      f32x4 t[1];
+      chunk_product(spread_rows(d.w[g], lane), d.a, t);
+      const float f = half_bits_to_float(spread_rows(d.sc[g], lane));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[g][i] = __builtin_fmaf(f, t[i], acc[g][i]);
+      for (int i = 0; i < 2; ++i) acc[2 * g + i] = __builtin_fmaf(f, t[0][i], acc[2 * g + i]);
     }
     if (st.s + 1 < steps) return;
-#pragma unroll
-    for (int g = 0; g < 2; ++g)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float v = chunk_sum(__builtin_fmaf(acc[g][2 + i], 1.0f / kLoScale, acc[g][i])) * (1.0f / kHScale);
-        if (c == 2 * g + i && (i == 0 || st.p1 != (int)kNoPair)) part[i ? st.p1 : st.p0][4 * g + li] = v;
-      }
-    acc[0] = acc[1] = f32x4{};
+    const int e = __builtin_amdgcn_readlane(id, st.pair);
+    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), st.pair));
+    const float r = chunk_sums(f32x4{__builtin_fmaf(acc[1], 1.0f / kLoScale, acc[0]),
+                                     __builtin_fmaf(acc[3], 1.0f / kLoScale, acc[2]), 0.f, 0.f}) * (1.0f / kHScale);
+    const int at = sum_index(lane);
+    if (at < 2 && (lane & 12) == 0) part[st.pair][4 * at + li] = e >= 0 && e < experts ? w * r : 0.0f;
+    acc = f32x4{};
   };
-  // the next step's loads go out before this one's arithmetic
-  Step cur;
-  item_of(cur, wave);
-  Data d;
-  if (cur.it < total) load(cur, d);
-  while (cur.it < total) {
-    Step nxt = cur;
-    advance(nxt);
-    Data dn = d;
-    if (nxt.it < total) load(nxt, dn);
-    compute(cur, d);
-    cur = nxt;
-    d = dn;
+  Step cur = {wave, 0}, ahead = cur;
+  Data d[kDepth];
+#pragma unroll
+  for (int u = 0; u < kDepth; ++u) {
+    load(ahead, d[u]);
+    advance(ahead);
+  }
+  while (cur.pair < pairs) {
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      if (cur.pair < pairs) compute(cur, d[u]);
+      advance(cur);
+      load(ahead, d[u]);
+      advance(ahead);
+    }
   }
   __syncthreads();
   if (!out) return;
   float v = 0.0f;
-  for (int s = 0; s < topk; ++s) {
-    const int p = ot * topk + s;
-    const int e = ids_l[p];
-    if (e >= 0 && e < experts) v = __builtin_fmaf(weights_l[p], part[p][tid & 7], v);
-  }
+  for (int s = 0; s < topk; ++s) v += part[ot * topk + s][tid & 7];
   y[(size_t)ot * N + on] = float_to_half_bits(v + res);
+}
+
+// ---- more pairs: an expert's blocks ----
+constexpr int kXPitch = kXK * 2 + 16;            // bytes per staged row of x: rows shift by 4 banks
+constexpr int kXBuf = kBlock * kXPitch;
+constexpr uint32_t kHStep = 2 * kBlock * kStepK * 2;   // bytes of a block's h per step: upper parts, then lower parts
+
+// h: [block][step][part] (h_place, four rows).  A workgroup's work items are blockIdx.x, + gridDim.x, ...: item = block * bands
+// + band (32 weight rows); a piece of one, 2048 k, is what is loaded and computed at a time.
+template <int G>
+__global__ void __launch_bounds__(kThreads, 4)
+moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
+                   const uint16_t* __restrict__ scales, uint16_t* __restrict__ h, int pairs, int topk, int experts,
+                   int rows, int K, int bands) {
+  __shared__ __attribute__((aligned(16))) uint8_t xs[2 * kXBuf];
+  __shared__ __attribute__((aligned(16))) Blocks bl;
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int li = lane & 3, c = lane >> 2;        // weight row (and A row), chunk
+  const int total = group_pairs(bl, ids, pairs, experts);
+
+  const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
+  const int pieces = (K + kXK - 1) / kXK;
+  const int inter = rows >> 1;
+  const float per_token = 1.0f / (float)topk;
+
+  struct Work {
+    int block, band, piece;
+  };
+  struct Data {
+    u32x4 x[2], w[kXSteps];
+    uint32_t sc[kXSteps];
+  };
+  const int dblock = (int)gridDim.x / bands, dband = (int)gridDim.x % bands;
+  auto advance = [&](Work& k) {
+    if (++k.piece < pieces) return;
+    k.piece = 0;
+    k.block += dblock;
+    k.band += dband;
+    if (k.band >= bands) {
+      k.band -= bands;
+      ++k.block;
+    }
+  };
+  // A lane's place in a work item's rows, and how far its chunks are from the row's end.
+  const uint32_t lrow = (uint32_t)(wave * 4 + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
+  const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
+  // Every load is made, in a fixed order (so each wait is for its own).  What is there is in the buffers'
+  // descriptors, in scalar registers: they begin at the piece and end with the expert's last row, or
+  // with the row of x, or are empty.
+  auto load = [&](const Work& k, Data& d) __attribute__((always_inline)) {
+    const bool live = k.block < total;
+    const int b = live ? k.block : 0;
+    const int e = uniform(bl.expert[b]), n = live ? uniform(bl.size[b]) : 0;
+    // waves 2 r and 2 r + 1 stage the halves of row r
+    const int row = wave >> 1, k0 = k.piece * kXK;
+    const int pair = row < n ? uniform(bl.pair[kBlock * b + row]) : 0;
+    const int token = uniform((int)(((float)pair + 0.5f) * per_token));
+    const __amdgpu_buffer_rsrc_t xres = make_rsrc(x + (size_t)token * K + k0, row < n ? (uint32_t)(K - k0) * 2u : 0u);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      d.x[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             xres, (uint32_t)(wave & 1) * (4u * kStepK) + 16u * (uint32_t)lane +
+                                                       2u * kStepK * s, 0, 0));
+    __builtin_amdgcn_sched_barrier(0);           // (these first: they are waited for without the weights)
+    const int r0 = k.band * kBandRows;
+    const size_t first = (size_t)e * rows + r0;
+    const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
+                                                  live ? (uint32_t)(rows - r0) * row_w - (uint32_t)k0 / 2 : 0u);
+    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
+                                                  live ? ((uint32_t)(rows - r0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+#pragma unroll
+    for (int s = 0; s < kXSteps; ++s) {
+      const bool in = (uint32_t)(k0 + s * kStepK) + 32u * lchunk < (uint32_t)K;     // (else: the next row's)
+      d.w[s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             wres, offset_if(in, w_off) + (uint32_t)(kStepK / 2) * s, 0, kStream));
+      d.sc[s] = __builtin_amdgcn_raw_buffer_load_b16(sres, offset_if(in, s_off) + (uint32_t)(kStepK / G * 2) * s, 0, 0);
+    }
+  };
+  f32x4 acc = f32x4{};
+  auto stage = [&](const Data& d, uint8_t* buf) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      *reinterpret_cast<u32x4*>(buf + (wave >> 1) * kXPitch + ((wave & 1) * 2 + s) * (2 * kStepK) + 16 * lane) =
+          permute_a(d.x[s]);
+  };
+  auto compute = [&](const Work& k, const Data& d, const uint8_t* buf) {
+    const uint8_t* xa = buf + li * kXPitch + 64 * c;
+#pragma unroll
+    for (int s = 0; s < kXSteps; ++s) {
+      if (k.piece * kXK + s * kStepK >= K) break;
+      u32x4 a[1][4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) a[0][w] = *reinterpret_cast<const u32x4*>(xa + s * (2 * kStepK) + 16 * w);
+      f32x4 t[1];
+      chunk_product(spread_rows(d.w[s], lane), a, t);
+      const float f = half_bits_to_float(spread_rows(d.sc[s], lane));
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i) acc[i] = __builtin_fmaf(f, t[0][i], acc[i]);
+    }
+    if (k.piece + 1 < pieces) return;
+    // the first four lanes of each row of sixteen have one pair's sums; the even ones (gate rows) store
+    const int n = uniform(bl.size[k.block]), i = sum_index(lane);
+    const float gate = chunk_sums(acc), up = next_row(gate);
+    acc = f32x4{};
+    const uint32_t o = (uint32_t)(k.band * kBandRows + wave * 4 + li) >> 1;
+    if (i < n && (lane & 13) == 0 && o < (uint32_t)inter) {
+      uint16_t hi, lo;
+      split_h(silu_product(gate, up) * kHScale, hi, lo);
+      uint16_t* dst = h + ((size_t)k.block * h_steps(inter) + o / kStepK) * (kHStep / 2) + h_place(o, kBlock, i);
+      dst[0] = hi;
+      dst[kHStep / 4] = lo;
+    }
+  };
+  // Two sets of registers and of staged rows in turn: the next item's loads are out while one is computed, and
+  // a buffer is written again after the barrier that follows its readers.
+  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0}, ahead = cur;
+  Data d[2];
+  load(ahead, d[0]);
+  advance(ahead);
+  auto phase = [&](auto u_tag) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_tag)::value;
+    uint8_t* buf = xs + u * kXBuf;
+    stage(d[u], buf);
+    load(ahead, d[1 - u]);
+    advance(ahead);
+    lds_barrier();
+    compute(cur, d[u], buf);
+    advance(cur);
+    return cur.block < total;
+  };
+  if (cur.block >= total) return;
+  while (phase(std::integral_constant<int, 0>{}) && phase(std::integral_constant<int, 1>{})) {
+  }
+}
+
+// Down: a work item is (block, band of 128 columns), sixteen columns per wave; a piece of one is 512 k.  part
+// [pair][N] fp32 receives the pairs' results.
+constexpr int kDownGroups = 4;                   // groups of four columns per wave
+constexpr int kDownCols = 4 * kDownGroups * kWaves;
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 4)
+moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
+                const uint16_t* __restrict__ scales, float* __restrict__ part, int pairs, int experts, int N, int K,
+                int bands) {
+  __shared__ __attribute__((aligned(16))) uint8_t hs[2 * kHStep];
+  __shared__ __attribute__((aligned(16))) Blocks bl;
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int c = lane >> 2;
+  const int total = group_pairs(bl, ids, pairs, experts);
+
+  const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
+  const int steps = h_steps(K);
+  const uint32_t lrow = (uint32_t)(16 * wave + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
+  const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
+  struct Work {
+    int block, band, s;
+  };
+  struct Data {
+    u32x4 h, w[kDownGroups];
+    uint32_t sc[kDownGroups];
+  };
+  const int dblock = (int)gridDim.x / bands, dband = (int)gridDim.x % bands;
+  auto advance = [&](Work& k) {
+    if (++k.s < steps) return;
+    k.s = 0;
+    k.block += dblock;
+    k.band += dband;
+    if (k.band >= bands) {
+      k.band -= bands;
+      ++k.block;
+    }
+  };
+  auto load = [&](const Work& k, Data& d) __attribute__((always_inline)) {
+    const bool live = k.block < total;
+    const int b = live ? k.block : 0, k0 = k.s * kStepK, n0 = k.band * kDownCols;
+    // wave w stages the w-th KB: word w % 4 of the upper (w < 4) or lower parts; chunks past K were never written
+    const __amdgpu_buffer_rsrc_t hres =
+        make_rsrc(reinterpret_cast<const uint8_t*>(h) + (size_t)(b * steps + k.s) * kHStep, live ? kHStep : 0u);
+    d.h = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                        hres, offset_if(k0 + 32 * c < K, 1024u * wave + 16u * lane), 0, 0));
+    __builtin_amdgcn_sched_barrier(0);
+    const size_t first = (size_t)uniform(bl.expert[b]) * N + n0;
+    const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
+                                                  live ? (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2 : 0u);
+    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
+                                                  live ? ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+    const bool in = (uint32_t)k0 + 32u * lchunk < (uint32_t)K;
+    const uint32_t wo = offset_if(in, w_off), so = offset_if(in, s_off);
+#pragma unroll
+    for (int g = 0; g < kDownGroups; ++g) {
+      d.w[g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres, wo + 4u * g * row_w, 0, kStream));
+      d.sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, so + 8u * g * spr, 0, 0);
+    }
+  };
+  f32x4 acc[kDownGroups];
+#pragma unroll
+  for (int g = 0; g < kDownGroups; ++g) acc[g] = f32x4{};
+  auto compute = [&](const Work& k, const Data& d, const uint8_t* buf) {
+    u32x4 a[2][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) a[q][w] = *reinterpret_cast<const u32x4*>(buf + (4 * q + w) * 1024 + 16 * lane);
+#pragma unroll
+    for (int g = 0; g < kDownGroups; ++g) {
+      f32x4 t[2];
+      chunk_product(spread_rows(d.w[g], lane), a, t);
+      const float f = half_bits_to_float(spread_rows(d.sc[g], lane));
+#pragma unroll
+      for (int i = 0; i < kBlock; ++i)
+        acc[g][i] = __builtin_fmaf(f, __builtin_fmaf(t[1][i], 1.0f / kLoScale, t[0][i]), acc[g][i]);
+    }
+    if (k.s + 1 < steps) return;
+    // a row of sixteen lanes has one pair's sums, column li of each group in all its lanes: lane 4 g + li stores group g's
+    float r = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kDownGroups; ++g) {
+      const float v = chunk_sums(acc[g]);
+      if ((c & 3) == g) r = v;
+      acc[g] = f32x4{};
+    }
+    const int i = sum_index(lane), n = k.band * kDownCols + 16 * wave + (lane & 15);
+    if (i < bl.size[k.block] && n < N) part[(size_t)bl.pair[kBlock * k.block + i] * N + n] = r * (1.0f / kHScale);
+  };
+  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0}, ahead = cur;
+  Data d[2];
+  load(ahead, d[0]);
+  advance(ahead);
+  auto phase = [&](auto u_tag) __attribute__((always_inline)) {
+    constexpr int u = decltype(u_tag)::value;
+    uint8_t* buf = hs + u * kHStep;
+    *reinterpret_cast<u32x4*>(buf + 1024 * wave + 16 * lane) = d[u].h;
+    load(ahead, d[1 - u]);
+    advance(ahead);
+    lds_barrier();
+    compute(cur, d[u], buf);
+    advance(cur);
+    return cur.block < total;
+  };
+  if (cur.block >= total) return;
+  while (phase(std::integral_constant<int, 0>{}) && phase(std::integral_constant<int, 1>{})) {
+  }
+}
+
+// y = residual + sum over a token's slots of weight * part, four columns per thread.
+__global__ void __launch_bounds__(256)
+moe_ffn_combine_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+                       const uint16_t* residual, uint16_t* y, int topk, int experts, int N) {
+  const int n = 4 * (blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
+  if (n >= N) return;
+  const size_t at = (size_t)t * N + n;
+  f16x4 res = f16x4{};
+  if (residual) res = *reinterpret_cast<const f16x4*>(residual + at);
+  f32x4 v = f32x4{};
+  for (int s0 = 0; s0 < topk; s0 += 8) {         // eight slots' loads in flight
+    f32x4 q[8];
+    float w[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int p = t * topk + s0 + s;
+      const bool in = s0 + s < topk && ids[p] >= 0 && ids[p] < experts;
+      w[s] = in ? weights[p] : 0.0f;
+      q[s] = in ? *reinterpret_cast<const f32x4*>(part + (size_t)p * N + n) : f32x4{};
+    }
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(w[s], q[s][i], v[i]);
+  }
+  f16x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (_Float16)(v[i] + (float)res[i]);
+  *reinterpret_cast<f16x4*>(y + at) = o;
 }
 
 }  // namespace
 
-size_t moe_ffn_workspace_bytes(int pairs, int inter) {
-  const size_t links = ((size_t)pairs * sizeof(uint32_t) + 255) & ~(size_t)255;
-  return kCounterBytes + links + (size_t)pairs * 2 * inter * sizeof(uint16_t);
+size_t moe_ffn_workspace_bytes(int pairs, int hidden, int inter) {
+  if (pairs <= kDirectPairs) return kCounterBytes + (size_t)pairs * h_steps(inter) * kDirectStep;
+  // (as many blocks as pairs at most)
+  return kCounterBytes + (size_t)pairs * h_steps(inter) * kHStep + (size_t)pairs * hidden * sizeof(float);
 }
 
 hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
                           const uint16_t* gate_up_scales, const uint32_t* down, const uint16_t* down_scales,
                           const uint16_t* residual, uint16_t* y, int tokens, int topk, int experts, int hidden,
-                          int inter, int group, void* workspace, hipStream_t stream) {
+                          int inter, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   const int pairs = tokens * topk;
-  uint32_t* link = reinterpret_cast<uint32_t*>(behind_counters(workspace));
-  uint16_t* h = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(link) +
-                                            (((size_t)pairs * sizeof(uint32_t) + 255) & ~(size_t)255));
-  auto up = group == 32 ? (pairs <= 64 ? moe_gate_up_kernel<32, 1> : moe_gate_up_kernel<32, kMoeFfnPairs / 64>)
-                        : (pairs <= 64 ? moe_gate_up_kernel<128, 1> : moe_gate_up_kernel<128, kMoeFfnPairs / 64>);
-  const hipError_t err =
-      launch_kernel(up, dim3((unsigned)((2 * inter + kUpRows - 1) / kUpRows), (unsigned)pairs), dim3(kUpThreads), 0,
-                    stream, x, ids, gate_up, gate_up_scales, h, link, pairs, topk, experts, 2 * inter, hidden);
-  if (err != hipSuccess) return err;
-  return launch_kernel(group == 32 ? moe_down_kernel<32> : moe_down_kernel<128>, dim3((unsigned)((hidden + 7) / 8)),
-                       dim3(kDownThreads), 0, stream, h, link, ids, weights, down, down_scales, residual, y, pairs, topk,
-                       tokens, experts, hidden, inter);
+  uint16_t* h = reinterpret_cast<uint16_t*>(behind_counters(workspace));
+  const int up_bands = (2 * inter + kBandRows - 1) / kBandRows;
+  const bool g32 = group == 32;
+  if (pairs <= kDirectPairs) {
+    const hipError_t e = launch_kernel(g32 ? moe_gate_up_direct_kernel<32> : moe_gate_up_direct_kernel<128>,
+                                       dim3((unsigned)up_bands, (unsigned)pairs), dim3(kThreads), 0, stream, x, ids, gate_up,
+                                       gate_up_scales, h, topk, experts, 2 * inter, hidden);
+    if (e != hipSuccess) return e;
+    return launch_kernel(g32 ? moe_down_direct_kernel<32> : moe_down_direct_kernel<128>, dim3((unsigned)((hidden + 7) / 8)),
+                         dim3(kThreads), 0, stream, h, ids, weights, down, down_scales, residual, y, pairs, topk, tokens,
+                         experts, hidden, inter);
+  }
+  float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + (size_t)pairs * h_steps(inter) * kHStep);
+  const int down_bands = (hidden + kDownCols - 1) / kDownCols;
+  // two workgroups per CU, fewer where there are fewer work items
+  auto grid = [&](int bands) {
+    const int64_t items = (int64_t)pairs * bands;
+    return dim3((unsigned)(items < 2 * dev.num_cu ? items : 2 * dev.num_cu));
+  };
+  hipError_t e = launch_kernel(g32 ? moe_gate_up_kernel<32> : moe_gate_up_kernel<128>, grid(up_bands), dim3(kThreads), 0, stream,
+                               x, ids, gate_up, gate_up_scales, h, pairs, topk, experts, 2 * inter, hidden, up_bands);
+  if (e != hipSuccess) return e;
+  e = launch_kernel(g32 ? moe_down_kernel<32> : moe_down_kernel<128>, grid(down_bands), dim3(kThreads), 0, stream, h, ids, down,
+                    down_scales, part, pairs, experts, hidden, inter, down_bands);
+  if (e != hipSuccess) return e;
+  return launch_kernel(moe_ffn_combine_kernel, dim3((unsigned)((hidden + 1023) / 1024), (unsigned)tokens), dim3(256), 0, stream,
+                       part, ids, weights, residual, y, topk, experts, hidden);
 }
 
 }  // namespace w4a16
