@@ -201,7 +201,7 @@ def test_ffn_abi_refusals():
     assert ffn(group=64) == w4.ERR_GROUP
     assert ffn(t=-1) == ffn(t=65) == ffn(k=0) == ffn(t=64, k=9) == ffn(k=513) == ffn(k=2 ** 31 - 1) == w4.ERR_SHAPE
     assert ffn(e=0) == ffn(e=-1) == ffn(h=-32) == ffn(h=100) == ffn(i=0) == ffn(i=48) == ffn(i=-32) == w4.ERR_SHAPE
-    assert ffn(h=1 << 20, i=1 << 11) == ffn(i=1 << 20) == w4.ERR_SHAPE       # 2 GiB of an expert's; of what is handed on
+    assert ffn(h=1 << 20, i=1 << 11) == w4.ERR_SHAPE                         # 2 GiB of an expert's weights
     assert ffn(t=0) == ffn(h=0) == w4.OK
     for a in ("x", "ids", "w", "gu", "gs", "dn", "ds", "y"):
         assert ffn(**{a: NULL}) == w4.ERR_NULL, a
