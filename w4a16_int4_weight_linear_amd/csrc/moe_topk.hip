@@ -24,9 +24,9 @@ constexpr uint32_t kMaskedKey = 0x007FFFFFu;     // the key of -inf; 0 is no log
 
 // Floats as integers in the same order: -0 as +0, every NaN above +inf.
 __device__ inline uint32_t key_of(float x) {
-  if (x != x) return 0xFFFFFFFFu;
   const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return x != x ? 0xFFFFFFFFu : k;
 }
 __device__ inline float value_of(uint32_t key) {
   return __builtin_bit_cast(float, key & 0x80000000u ? key ^ 0x80000000u : ~key);
@@ -72,22 +72,32 @@ __device__ inline int expert_of(int lane, int v) { return 4 * lane + 4 * LANES *
 __device__ inline float to_float(float x) { return x; }
 __device__ inline float to_float(_Float16 x) { return (float)x; }
 
-// A lane's logits of row x (e >= experts: none).  VEC: rows start on four elements.
+// An expert to read in place of one that does not exist (the empty asm keeps the choice a value, not a
+// branch around each load).
+__device__ inline int readable(int e, int experts) {
+  int r = e < experts ? e : 0;
+  asm("" : "+v"(r));
+  return r;
+}
+
+// A lane's logits of row x, all loads in flight together (e >= experts: expert 0's, to be passed over).  VEC:
+// rows start on four elements.
 template <int LANES, int V, bool VEC, typename T>
 __device__ inline void load_row(const T* x, int lane, int experts, float (&val)[V]) {
   typedef T t4 __attribute__((ext_vector_type(4)));
+  if constexpr (VEC) {
+    t4 q[V / 4];
 #pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    const int e = expert_of<LANES>(lane, j);
-    if constexpr (VEC) {
-      t4 q = {};
-      if (e < experts) q = *reinterpret_cast<const t4*>(x + e);
+    for (int j = 0; j < V / 4; ++j)
+      q[j] = *reinterpret_cast<const t4*>(x + readable(expert_of<LANES>(lane, 4 * j), experts));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) val[j + i] = to_float(q[i]);
-    } else {
+    for (int v = 0; v < V; ++v) val[v] = to_float(q[v / 4][v % 4]);
+  } else {
+    T q[V];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) val[j + i] = e + i < experts ? to_float(x[e + i]) : 0.0f;
-    }
+    for (int v = 0; v < V; ++v) q[v] = x[readable(expert_of<LANES>(lane, v), experts)];
+#pragma unroll
+    for (int v = 0; v < V; ++v) val[v] = to_float(q[v]);
   }
 }
 
@@ -104,45 +114,33 @@ moe_topk_kernel(const T* __restrict__ logits, int32_t* __restrict__ ids, float* 
 #pragma unroll
   for (int v = 0; v < V; ++v) key[v] = expert_of<LANES>(lane, v) < experts ? key_of(val[v]) : 0u;
 
-  uint32_t mine = 0;                               // this lane's largest key and its place
-  int at = 0;
-  auto scan = [&]() {
-    mine = 0;
-    at = 0;
+  auto largest = [&]() {
+    uint32_t m = key[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] > mine) {
-        mine = key[v];
-        at = v;
-      }
+    for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
+    return row_max<LANES>(m);
   };
-  scan();
-  const uint32_t top = row_max<LANES>(mine);
-  const float peak = value_of(top);
+  uint32_t won = largest();
+  const float peak = value_of(won);
   float total = 0.0f;
   if (!renormalize) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] > kMaskedKey) total += expf(val[v] - peak);
+    for (int v = 0; v < V; ++v) total += key[v] > kMaskedKey ? expf(val[v] - peak) : 0.0f;
     total = row_sum<LANES>(total);
   }
-  uint32_t won = top;
   int my_id = -1;                                  // slot `lane`'s choice
   uint32_t my_key = 0;
   for (int s = 0; s < topk; ++s) {
-    const int e = expert_of<LANES>(lane, at);
-    const int best = (int)row_min<LANES>(mine == won ? (uint32_t)e : 0xFFFFFFFFu);
-    if (lane == s && won > kMaskedKey) {
-      my_id = best;
-      my_key = won;
-    }
-    if (mine == won && e == best) {
+    uint32_t first = 0xFFFFFFFFu;                  // the lowest expert with that key
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == at) key[v] = 0;
-      scan();
-    }
-    won = row_max<LANES>(mine);
+    for (int v = V - 1; v >= 0; --v) first = key[v] == won ? (uint32_t)expert_of<LANES>(lane, v) : first;
+    first = row_min<LANES>(first);
+    const bool mine = lane == s && won > kMaskedKey;
+    my_id = mine ? (int)first : my_id;
+    my_key = mine ? won : my_key;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = first == (uint32_t)expert_of<LANES>(lane, v) ? 0u : key[v];
+    won = largest();
   }
   const float p = my_id >= 0 ? expf(value_of(my_key) - peak) : 0.0f;
   if (renormalize) total = row_sum<LANES>(p);
@@ -222,7 +220,9 @@ moe_topk_backward_kernel(const float* __restrict__ dweights, const T* __restrict
   }
 }
 
-// Lanes and values per lane: a DPP row per token for up to 256 experts and 16 slots, else a wave.
+// Lanes and values per lane: a DPP row per token for up to 256 experts and 16 slots, else a wave; and a wave per token
+// where there are few tokens (a round's chain of instructions is shorter).
+constexpr int kWaveTokens = 1024;
 struct Forward {
   template <int LANES, int V, bool VEC, typename T>
   static hipError_t launch(const T* logits, int32_t* ids, float* weights, int tokens, int experts, int topk,
@@ -243,8 +243,8 @@ struct Backward {
   }
 };
 template <typename K, bool VEC, typename T, typename... A>
-hipError_t by_size(int experts, int topk, A... a) {
-  if (topk <= 16) {
+hipError_t by_size(int tokens, int experts, int topk, A... a) {
+  if (topk <= 16 && tokens > kWaveTokens) {
     if (experts <= 64) return K::template launch<16, 4, VEC, T>(a...);
     if (experts <= 128) return K::template launch<16, 8, VEC, T>(a...);
     if (experts <= 256) return K::template launch<16, 16, VEC, T>(a...);
@@ -255,8 +255,8 @@ hipError_t by_size(int experts, int topk, A... a) {
 }
 // rows that start on four elements are read four at a time
 template <typename K, typename T, typename... A>
-hipError_t by_layout(int experts, int topk, A... a) {
-  return experts % 4 ? by_size<K, false, T>(experts, topk, a...) : by_size<K, true, T>(experts, topk, a...);
+hipError_t by_layout(int tokens, int experts, int topk, A... a) {
+  return experts % 4 ? by_size<K, false, T>(tokens, experts, topk, a...) : by_size<K, true, T>(tokens, experts, topk, a...);
 }
 
 }  // namespace
@@ -264,9 +264,9 @@ hipError_t by_layout(int experts, int topk, A... a) {
 hipError_t launch_moe_topk(const void* logits, bool half, int32_t* ids, float* weights, int tokens, int experts,
                            int topk, bool renormalize, hipStream_t stream) {
   if (half)
-    return by_layout<Forward, _Float16>(experts, topk, static_cast<const _Float16*>(logits), ids, weights, tokens,
+    return by_layout<Forward, _Float16>(tokens, experts, topk, static_cast<const _Float16*>(logits), ids, weights, tokens,
                                         experts, topk, (int)renormalize, stream);
-  return by_layout<Forward, float>(experts, topk, static_cast<const float*>(logits), ids, weights, tokens, experts,
+  return by_layout<Forward, float>(tokens, experts, topk, static_cast<const float*>(logits), ids, weights, tokens, experts,
                                    topk, (int)renormalize, stream);
 }
 
@@ -274,10 +274,10 @@ hipError_t launch_moe_topk_backward(const float* dweights, const void* logits, b
                                     const float* weights, void* dlogits, int tokens, int experts, int topk,
                                     bool renormalize, hipStream_t stream) {
   if (half)
-    return by_layout<Backward, _Float16>(experts, topk, dweights, static_cast<const _Float16*>(logits), ids, weights,
+    return by_layout<Backward, _Float16>(tokens, experts, topk, dweights, static_cast<const _Float16*>(logits), ids, weights,
                                          static_cast<_Float16*>(dlogits), tokens, experts, topk, (int)renormalize,
                                          stream);
-  return by_layout<Backward, float>(experts, topk, dweights, static_cast<const float*>(logits), ids, weights,
+  return by_layout<Backward, float>(tokens, experts, topk, dweights, static_cast<const float*>(logits), ids, weights,
                                     static_cast<float*>(dlogits), tokens, experts, topk, (int)renormalize, stream);
 }
 
