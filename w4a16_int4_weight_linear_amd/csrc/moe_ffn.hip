@@ -116,34 +116,50 @@ __device__ inline int group_pairs(Blocks& s, const int32_t* __restrict__ ids, in
 }
 
 // The eight codes of a packed word as fp16 integers u - 8, in the order of permute_a: a nibble
-// under the exponent of 1024 (mantissa bits 0-3) or of 64 (bits 4-7), less 1032 or 72.
-__device__ inline void decode_codes(uint32_t q, f16x4& a, f16x4& b) {
-  const uint32_t q8 = q >> 8;
-  const f16x2 c1 = {(_Float16)-1032.f, (_Float16)-1032.f}, c2 = {(_Float16)-72.f, (_Float16)-72.f};
-  const f16x2 p0 = __builtin_bit_cast(f16x2, (q & 0x000F000Fu) | 0x64006400u) + c1;    // (0, 4)
-  const f16x2 p1 = __builtin_bit_cast(f16x2, (q8 & 0x000F000Fu) | 0x64006400u) + c1;   // (2, 6)
-  const f16x2 p2 = __builtin_bit_cast(f16x2, (q & 0x00F000F0u) | 0x54005400u) + c2;    // (1, 5)
-  const f16x2 p3 = __builtin_bit_cast(f16x2, (q8 & 0x00F000F0u) | 0x54005400u) + c2;   // (3, 7)
-  a = f16x4{p0[0], p0[1], p1[0], p1[1]};
-  b = f16x4{p2[0], p2[1], p3[0], p3[1]};
-}
+// under the exponent of 1024 (mantissa bits 0-3) or of 64 (bits 4-7), less 1032 or 72.  Masks (scalar) and
+// exponents (vector) are held in registers, so each pair is one v_and_or_b32 and one packed addition.
+struct Decoder {
+  uint32_t m_lo, m_hi, e_lo, e_hi;
+  __device__ inline Decoder() {
+    m_lo = __builtin_amdgcn_readfirstlane(0x000F000Fu);
+    m_hi = __builtin_amdgcn_readfirstlane(0x00F000F0u);
+    e_lo = 0x64006400u;
+    e_hi = 0x54005400u;
+    asm volatile("" : "+v"(e_lo), "+v"(e_hi));
+  }
+  __device__ inline void operator()(uint32_t q, f16x4& a, f16x4& b) const {
+    const uint32_t q8 = q >> 8;
+    const f16x2 c1 = {(_Float16)-1032.f, (_Float16)-1032.f}, c2 = {(_Float16)-72.f, (_Float16)-72.f};
+    const f16x2 p0 = __builtin_bit_cast(f16x2, (q & m_lo) | e_lo) + c1;      // (0, 4)
+    const f16x2 p1 = __builtin_bit_cast(f16x2, (q8 & m_lo) | e_lo) + c1;     // (2, 6)
+    const f16x2 p2 = __builtin_bit_cast(f16x2, (q & m_hi) | e_hi) + c2;      // (1, 5)
+    const f16x2 p3 = __builtin_bit_cast(f16x2, (q8 & m_hi) | e_hi) + c2;     // (3, 7)
+    a = f16x4{p0[0], p0[1], p1[0], p1[1]};
+    b = f16x4{p2[0], p2[1], p3[0], p3[1]};
+  }
+};
 
-// Four activation rows times a lane's four weight rows over its chunk of 32 k: a[w] is the lane's
-// activations of word w, in permute_a's order.  With two sets of rows the codes are decoded once.
+// Four activation rows times a lane's four weight rows over a word's eight k: a[q] is set q of the rows' activations in
+// permute_a's order (two sets: the codes are decoded once).
 template <int SETS>
-__device__ inline void chunk_product(const u32x4& wv, const u32x4 (&a)[SETS][4], f32x4 (&t)[SETS]) {
+__device__ inline void word_product(const Decoder& decode, uint32_t word, const u32x4 (&a)[SETS], f32x4 (&t)[SETS]) {
+  f16x4 b0, b1;
+  decode(word, b0, b1);
 #pragma unroll
-  for (int q = 0; q < SETS; ++q) t[q] = f32x4{};
+  for (int q = 0; q < SETS; ++q) {
+    t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q].x, a[q].y}), b0, t[q], 0, 0, 0);
+    t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q].z, a[q].w}), b1, t[q], 0, 0, 0);
+  }
+}
+// ... over the lane's chunk of 32 k.
+__device__ inline f32x4 chunk_product(const Decoder& decode, const u32x4& wv, const u32x4 (&a)[4]) {
+  f32x4 t[1] = {f32x4{}};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    f16x4 b0, b1;
-    decode_codes(wv[w], b0, b1);
-#pragma unroll
-    for (int q = 0; q < SETS; ++q) {
-      t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q][w].x, a[q][w].y}), b0, t[q], 0, 0, 0);
-      t[q] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(f16x4, u32x2{a[q][w].z, a[q][w].w}), b1, t[q], 0, 0, 0);
-    }
+    const u32x4 aw[1] = {a[w]};
+    word_product(decode, wv[w], aw, t);
   }
+  return t[0];
 }
 
 // From the lane that loaded it (row l / 16, chunk l % 16) to the one that multiplies it (row l % 4, chunk l / 4).
@@ -228,6 +244,7 @@ moe_gate_up_direct_kernel(const uint16_t* __restrict__ x, const int32_t* __restr
   const uint32_t lrow = (uint32_t)(wave * 4 + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
   const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
   const uint16_t* xp = x + (size_t)(p / topk) * K;
+  const Decoder decode;
   float acc = 0.0f;
   for (int k0 = 0, buf = 0; k0 < K; k0 += kXK, buf ^= 1) {
     // every thread stages 8 bytes of the piece's 4 KB (and permutes them with its neighbour's)
@@ -252,13 +269,12 @@ moe_gate_up_direct_kernel(const uint16_t* __restrict__ x, const int32_t* __restr
 #pragma unroll
     for (int s = 0; s < kXSteps; ++s) {
       if (k0 + s * kStepK >= K) break;
-      u32x4 a[1][4];
+      u32x4 a[4];
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        a[0][w] = *reinterpret_cast<const u32x4*>(xs[buf] + s * (2 * kStepK) + 64 * c + 16 * w);
-      f32x4 t[1];
-      chunk_product(spread_rows(wv[s], lane), a, t);
-      acc = __builtin_fmaf(half_bits_to_float(spread_rows(sc[s], lane)), t[0][0], acc);
+        a[w] = *reinterpret_cast<const u32x4*>(xs[buf] + s * (2 * kStepK) + 64 * c + 16 * w);
+      const f32x4 t = chunk_product(decode, spread_rows(wv[s], lane), a);
+      acc = __builtin_fmaf(half_bits_to_float(spread_rows(sc[s], lane)), t[0], acc);
     }
   }
   const float gate = chunk_sums(f32x4{acc, 0.f, 0.f, 0.f}), up = next_row(gate);
@@ -298,7 +314,7 @@ moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict
     int pair, s;
   };
   struct Data {
-    u32x4 w[2], a[1][4];
+    u32x4 w[2], a[4];
     uint32_t sc[2];
   };
   auto advance = [&](Step& st) {
@@ -328,17 +344,17 @@ moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict
     const uint32_t a_off = offset_if(k0 + 32 * c < K, 32u * c + 16u * (li & 1));
 #pragma unroll
     for (int w = 0; w < 4; ++w)
-      d.a[0][w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, a_off + 512u * w, 0, 0));
+      d.a[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, a_off + 512u * w, 0, 0));
   };
+  const Decoder decode;
   f32x4 acc = f32x4{};                           // upper and lower parts' sums, columns 0-3 and 4-7
   auto compute = [&](const Step& st, const Data& d) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      f32x4 t[1];
-      chunk_product(spread_rows(d.w[g], lane), d.a, t);
+      const f32x4 t = chunk_product(decode, spread_rows(d.w[g], lane), d.a);
       const float f = half_bits_to_float(spread_rows(d.sc[g], lane));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[2 * g + i] = __builtin_fmaf(f, t[0][i], acc[2 * g + i]);
+      for (int i = 0; i < 2; ++i) acc[2 * g + i] = __builtin_fmaf(f, t[i], acc[2 * g + i]);
     }
     if (st.s + 1 < steps) return;
     const int e = __builtin_amdgcn_readlane(id, st.pair);
@@ -380,11 +396,11 @@ constexpr uint32_t kHStep = 2 * kBlock * kStepK * 2;   // bytes of a block's h p
 // h: [block][step][part] (h_place, four rows).  A workgroup's work items are blockIdx.x, + gridDim.x, ...: item = block * bands
 // + band (32 weight rows); a piece of one, 2048 k, is what is loaded and computed at a time.
 template <int G>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 8)
 moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
                    const uint16_t* __restrict__ scales, uint16_t* __restrict__ h, int pairs, int topk, int experts,
                    int rows, int K, int bands) {
-  __shared__ __attribute__((aligned(16))) uint8_t xs[2 * kXBuf];
+  __shared__ __attribute__((aligned(16))) uint8_t xs[kXBuf];
   __shared__ __attribute__((aligned(16))) Blocks bl;
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
@@ -449,6 +465,7 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
       d.sc[s] = __builtin_amdgcn_raw_buffer_load_b16(sres, offset_if(in, s_off) + (uint32_t)(kStepK / G * 2) * s, 0, 0);
     }
   };
+  const Decoder decode;
   f32x4 acc = f32x4{};
   auto stage = [&](const Data& d, uint8_t* buf) {
 #pragma unroll
@@ -461,14 +478,13 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
 #pragma unroll
     for (int s = 0; s < kXSteps; ++s) {
       if (k.piece * kXK + s * kStepK >= K) break;
-      u32x4 a[1][4];
+      u32x4 a[4];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) a[0][w] = *reinterpret_cast<const u32x4*>(xa + s * (2 * kStepK) + 16 * w);
-      f32x4 t[1];
-      chunk_product(spread_rows(d.w[s], lane), a, t);
+      for (int w = 0; w < 4; ++w) a[w] = *reinterpret_cast<const u32x4*>(xa + s * (2 * kStepK) + 16 * w);
+      const f32x4 t = chunk_product(decode, spread_rows(d.w[s], lane), a);
       const float f = half_bits_to_float(spread_rows(d.sc[s], lane));
 #pragma unroll
-      for (int i = 0; i < kBlock; ++i) acc[i] = __builtin_fmaf(f, t[0][i], acc[i]);
+      for (int i = 0; i < kBlock; ++i) acc[i] = __builtin_fmaf(f, t[i], acc[i]);
     }
     if (k.piece + 1 < pieces) return;
     // the first four lanes of each row of sixteen have one pair's sums; the even ones (gate rows) store
@@ -484,39 +500,29 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
       dst[kHStep / 4] = lo;
     }
   };
-  // Two sets of registers and of staged rows in turn: the next item's loads are out while one is computed, and
-  // a buffer is written again after the barrier that follows its readers.
-  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0}, ahead = cur;
-  Data d[2];
-  load(ahead, d[0]);
-  advance(ahead);
-  auto phase = [&](auto u_tag) __attribute__((always_inline)) {
-    constexpr int u = decltype(u_tag)::value;
-    uint8_t* buf = xs + u * kXBuf;
-    stage(d[u], buf);
-    load(ahead, d[1 - u]);
-    advance(ahead);
+  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0};
+  Data d;
+  while (cur.block < total) {
+    load(cur, d);
+    lds_barrier();                               // (the rows staged before are read)
+    stage(d, xs);
     lds_barrier();
-    compute(cur, d[u], buf);
+    compute(cur, d, xs);
     advance(cur);
-    return cur.block < total;
-  };
-  if (cur.block >= total) return;
-  while (phase(std::integral_constant<int, 0>{}) && phase(std::integral_constant<int, 1>{})) {
   }
 }
 
-// Down: a work item is (block, band of 128 columns), sixteen columns per wave; a piece of one is 512 k.  part
+// Down: a work item is (block, band of 64 columns), eight columns per wave; a piece of one is 512 k.  part
 // [pair][N] fp32 receives the pairs' results.
-constexpr int kDownGroups = 4;                   // groups of four columns per wave
+constexpr int kDownGroups = 2;                   // groups of four columns per wave
 constexpr int kDownCols = 4 * kDownGroups * kWaves;
 
 template <int G>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 8)
 moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
                 const uint16_t* __restrict__ scales, float* __restrict__ part, int pairs, int experts, int N, int K,
                 int bands) {
-  __shared__ __attribute__((aligned(16))) uint8_t hs[2 * kHStep];
+  __shared__ __attribute__((aligned(16))) uint8_t hs[kHStep];
   __shared__ __attribute__((aligned(16))) Blocks bl;
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
@@ -525,7 +531,7 @@ moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids,
 
   const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
   const int steps = h_steps(K);
-  const uint32_t lrow = (uint32_t)(16 * wave + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
+  const uint32_t lrow = (uint32_t)(4 * kDownGroups * wave + (lane >> 4)), lchunk = (uint32_t)(lane & 15);
   const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
   struct Work {
     int block, band, s;
@@ -567,23 +573,32 @@ moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids,
       d.sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, so + 8u * g * spr, 0, 0);
     }
   };
+  const Decoder decode;
   f32x4 acc[kDownGroups];
 #pragma unroll
   for (int g = 0; g < kDownGroups; ++g) acc[g] = f32x4{};
   auto compute = [&](const Work& k, const Data& d, const uint8_t* buf) {
-    u32x4 a[2][4];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) a[q][w] = *reinterpret_cast<const u32x4*>(buf + (4 * q + w) * 1024 + 16 * lane);
+    f32x4 t[kDownGroups][2];
+    u32x4 wv[kDownGroups];
 #pragma unroll
     for (int g = 0; g < kDownGroups; ++g) {
-      f32x4 t[2];
-      chunk_product(spread_rows(d.w[g], lane), a, t);
+      t[g][0] = t[g][1] = f32x4{};
+      wv[g] = spread_rows(d.w[g], lane);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      u32x4 a[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) a[q] = *reinterpret_cast<const u32x4*>(buf + (4 * q + w) * 1024 + 16 * lane);
+#pragma unroll
+      for (int g = 0; g < kDownGroups; ++g) word_product(decode, wv[g][w], a, t[g]);
+    }
+#pragma unroll
+    for (int g = 0; g < kDownGroups; ++g) {
       const float f = half_bits_to_float(spread_rows(d.sc[g], lane));
 #pragma unroll
       for (int i = 0; i < kBlock; ++i)
-        acc[g][i] = __builtin_fmaf(f, __builtin_fmaf(t[1][i], 1.0f / kLoScale, t[0][i]), acc[g][i]);
+        acc[g][i] = __builtin_fmaf(f, __builtin_fmaf(t[g][1][i], 1.0f / kLoScale, t[g][0][i]), acc[g][i]);
     }
     if (k.s + 1 < steps) return;
     // a row of sixteen lanes has one pair's sums, column li of each group in all its lanes: lane 4 g + li stores group g's
@@ -594,26 +609,19 @@ moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids,
       if ((c & 3) == g) r = v;
       acc[g] = f32x4{};
     }
-    const int i = sum_index(lane), n = k.band * kDownCols + 16 * wave + (lane & 15);
-    if (i < bl.size[k.block] && n < N) part[(size_t)bl.pair[kBlock * k.block + i] * N + n] = r * (1.0f / kHScale);
+    const int i = sum_index(lane), n = k.band * kDownCols + 4 * kDownGroups * wave + (lane & 15);
+    if (i < bl.size[k.block] && (lane & 15) < 4 * kDownGroups && n < N)
+      part[(size_t)bl.pair[kBlock * k.block + i] * N + n] = r * (1.0f / kHScale);
   };
-  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0}, ahead = cur;
-  Data d[2];
-  load(ahead, d[0]);
-  advance(ahead);
-  auto phase = [&](auto u_tag) __attribute__((always_inline)) {
-    constexpr int u = decltype(u_tag)::value;
-    uint8_t* buf = hs + u * kHStep;
-    *reinterpret_cast<u32x4*>(buf + 1024 * wave + 16 * lane) = d[u].h;
-    load(ahead, d[1 - u]);
-    advance(ahead);
+  Work cur = {(int)blockIdx.x / bands, (int)blockIdx.x % bands, 0};
+  Data d;
+  while (cur.block < total) {
+    load(cur, d);
+    lds_barrier();                               // (the rows staged before are read)
+    *reinterpret_cast<u32x4*>(hs + 1024 * wave + 16 * lane) = d.h;
     lds_barrier();
-    compute(cur, d[u], buf);
+    compute(cur, d, hs);
     advance(cur);
-    return cur.block < total;
-  };
-  if (cur.block >= total) return;
-  while (phase(std::integral_constant<int, 0>{}) && phase(std::integral_constant<int, 1>{})) {
   }
 }
 
@@ -675,10 +683,10 @@ hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* we
   }
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + (size_t)pairs * h_steps(inter) * kHStep);
   const int down_bands = (hidden + kDownCols - 1) / kDownCols;
-  // two workgroups per CU, fewer where there are fewer work items
+  // four workgroups per CU, fewer where there are fewer work items
   auto grid = [&](int bands) {
     const int64_t items = (int64_t)pairs * bands;
-    return dim3((unsigned)(items < 2 * dev.num_cu ? items : 2 * dev.num_cu));
+    return dim3((unsigned)(items < 4 * dev.num_cu ? items : 4 * dev.num_cu));
   };
   hipError_t e = launch_kernel(g32 ? moe_gate_up_kernel<32> : moe_gate_up_kernel<128>, grid(up_bands), dim3(kThreads), 0, stream,
                                x, ids, gate_up, gate_up_scales, h, pairs, topk, experts, 2 * inter, hidden, up_bands);
