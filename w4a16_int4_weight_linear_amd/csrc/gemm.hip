@@ -572,16 +572,30 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
     // the linear layer's other operands, ahead of the next item's loads, which they would wait behind (4096
     // rows 5120 -> 17408: a residual costs 19 instead of 28 us); lane l's 16-byte chunk l % 4 of rows 16 j + l / 4
     float bias = 0.0f;
-    f16x8 res[sizeof...(Epi) ? 2 * kMB : 1];
+    u32x4 res[2 * kMB > 4 ? 2 * kMB : 4];
+    // (rows of any alignment: elements of a 32-row block, the next block's loaded while one is used; a 1024 x 17407
+    // layer's residual costs a few instead of 40 us)
+    auto load_odd = [&](const LinearEpilogue& le, int mb, bool live, u32x4* r) {
+      const __amdgpu_buffer_rsrc_t rres = make_rsrc(le.residual, le.residual && live ? (uint32_t)M * (uint32_t)N * 2u : 0u);
+      const bool in = nw + li < N;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        uint32_t off = in && mb + 2 * j + h < M ? ((uint32_t)(mb + 2 * j + h) * (uint32_t)N + (uint32_t)(nw + li)) * 2u
+                                                : kOutOfRange;
+        asm("" : "+v"(off));          // (a value, not a branch around the load)
+        r[j / 4][j % 4] = __builtin_amdgcn_raw_buffer_load_b16(rres, off, 0, 0);
+      }
+    };
     auto load_operands = [&](const LinearEpilogue& le) {
       if (le.bias && nw + li < N) bias = half_bits_to_float(le.bias[nw + li]);
 #pragma unroll
       for (int j = 0; j < 2 * kMB; ++j) {
         const int m = m0 + 16 * j + (lane >> 2), n = nw + 8 * (lane & 3);
-        res[j] = f16x8{};
+        res[j] = u32x4{};
         if (dp && le.residual && (N & 7) == 0 && m < M && n < N)
-          res[j] = *reinterpret_cast<const f16x8*>(le.residual + (size_t)m * N + n);
+          res[j] = *reinterpret_cast<const u32x4*>(le.residual + (size_t)m * N + n);
       }
+      if (N & 7) load_odd(le, m0, dp, res);
     };
     (load_operands(epi), ...);
 
@@ -611,24 +625,23 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
           for (int i = 0; i + 1 < kMB; ++i) acc[i][0] = acc[i + 1][0];
           // (a wave's LDS accesses complete in order: its own writes are visible)
           if (N & 7) {          // rows of any alignment: two rows of 32 columns per access
-#pragma unroll 1
-            for (int j0 = 0; j0 < 32; j0 += 8) {
-              float v[4];
+            u32x4 next[4];
+            load_odd(le, mb + 32, mb + 32 < m0 + BM, next);
+            float v[16];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float*>(ep + (j0 + 2 * j + h) * kPitch + li * 4);
-              if (le.pre) {
+            for (int j = 0; j < 16; ++j) v[j] = *reinterpret_cast<const float*>(ep + (2 * j + h) * kPitch + li * 4);
+            const size_t at = (size_t)(mb + h) * N + nw + li;
+            if (le.pre) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (mb + j0 + 2 * j + h < M && nw + li < N)
-                    le.pre[(size_t)(mb + j0 + 2 * j + h) * N + nw + li] = float_to_half_bits(v[j]);
-              }
-              activate(le.act, v);
+              for (int j = 0; j < 16; ++j)
+                if (mb + 2 * j + h < M && nw + li < N) le.pre[at + (size_t)(2 * j) * N] = float_to_half_bits(v[j]);
+            }
+            activate(le.act, v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const size_t at = (size_t)(mb + j0 + 2 * j + h) * N + nw + li;
-                if (mb + j0 + 2 * j + h < M && nw + li < N)
-                  y[at] = float_to_half_bits(le.residual ? v[j] + half_bits_to_float(le.residual[at]) : v[j]);
-              }
+            for (int j = 0; j < 16; ++j) {
+              if (mb + 2 * j + h < M && nw + li < N)
+                y[at + (size_t)(2 * j) * N] = float_to_half_bits(v[j] + half_bits_to_float(res[j / 4][j % 4]));
+              res[j / 4][j % 4] = next[j / 4][j % 4];
             }
             continue;
           }
@@ -652,7 +665,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             }
             activate(le.act, v);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) o[u] = (_Float16)(v[u] + (float)res[0][u]);
+            for (int u = 0; u < 8; ++u) o[u] = (_Float16)(v[u] + (float)__builtin_bit_cast(f16x8, res[0])[u]);
             if (in) *reinterpret_cast<f16x8*>(y + at) = o;
 #pragma unroll
             for (int i = 0; i + 1 < 2 * kMB; ++i) res[i] = res[i + 1];
