@@ -343,6 +343,14 @@ def _check_ffn(what, specs):
     """specs: (name, tensor, dtypes, shape or None).  As _check_tensors, for these calls; returns the device."""
     tensor = _torch_preload.Tensor
     device, other = specs[0][1].device, None
+    # everything as it should be, on a device: nothing to name
+    for _, t, dtypes, shape in specs:
+        if t.__class__ is not tensor or t.dtype not in dtypes or (shape is not None and t.shape != shape) or \
+                t.device != device or not t.is_contiguous():
+            break
+    else:
+        if device.type == "cuda":
+            return device
     for name, t, dtypes, shape in specs:
         if not isinstance(t, tensor):
             raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
@@ -392,7 +400,7 @@ def _launch_on(what, device, stream, call, specs=()):
     operands in specs is held until the call has run on a stream given, which need not be theirs."""
     cuda = _torch_preload.cuda
     if stream is None:
-        if device.index == cuda.current_device():
+        if device.index == _current_device():
             return call(_current_handle(device.index))
         with cuda.device(device):
             return call(_current_handle(device.index))
@@ -404,10 +412,12 @@ def _launch_on(what, device, stream, call, specs=()):
         return call(stream.cuda_stream)
 
 
-def _current_handle(index):
-    """Handle of a device's current stream (torch's raw getter, where it has one, builds no Stream object)."""
-    raw = getattr(_torch_preload._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else _torch_preload.cuda.current_stream(index).cuda_stream
+if _torch_preload is not None:
+    # The current device's index, and the handle of a device's current stream: torch's raw getters, where it has them,
+    # build no objects and skip the initialisation that a device tensor has behind it.
+    _current_device = getattr(_torch_preload._C, "_cuda_getDevice", None) or _torch_preload.cuda.current_device
+    _current_handle = getattr(_torch_preload._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: _torch_preload.cuda.current_stream(index).cuda_stream)
 
 
 class _Kept(dict):
@@ -733,6 +743,11 @@ def _logits_dtype(what, logits):
     return 1 if logits.dtype == _torch_preload.float16 else 0
 
 
+def _check_topk(what, topk, experts):
+    if not 1 <= topk <= experts or topk > 64 or experts > 1024:
+        raise ValueError(f"{what}: topk = {topk} of {experts} experts: 1 <= topk <= min(experts, 64), experts <= 1024")
+
+
 def moe_topk(logits, topk: int, renormalize: bool = True, ids=None, weights=None, stream=None):
     """The router's choice: (ids int32 [tokens, topk], weights fp32 [tokens, topk]) from logits [tokens, experts]
     (fp32 or fp16), the largest first, equal ones by expert; weights are the softmax over all experts, or over the
@@ -740,8 +755,7 @@ def moe_topk(logits, topk: int, renormalize: bool = True, ids=None, weights=None
     what = "moe_topk"
     dtype = _logits_dtype(what, logits)
     tokens, experts = logits.shape
-    if not 1 <= topk <= min(experts, 64) or experts > 1024:
-        raise ValueError(f"{what}: topk = {topk} of {experts} experts: 1 <= topk <= min(experts, 64), experts <= 1024")
+    _check_topk(what, topk, experts)
     specs = [("logits", logits, _F32 + _F16, None)]
     if ids is not None:
         specs.append(("ids", ids, _I32, (tokens, topk)))
@@ -752,11 +766,13 @@ def moe_topk(logits, topk: int, renormalize: bool = True, ids=None, weights=None
     def call(handle):
         nonlocal ids, weights
         if ids is None:
-            ids = _torch_preload.empty((tokens, topk), dtype=_torch_preload.int32, device=device)
+            ids = logits.new_empty((tokens, topk), dtype=_I32[0])
         if weights is None:
-            weights = _torch_preload.empty((tokens, topk), dtype=_torch_preload.float32, device=device)
-        _check(lib.w4a16_moe_topk(logits.data_ptr(), dtype, ids.data_ptr(), weights.data_ptr(), tokens, experts, topk,
-                                  bool(renormalize), handle), "w4a16_moe_topk")
+            weights = logits.new_empty((tokens, topk), dtype=_F32[0])
+        status = lib.w4a16_moe_topk(logits.data_ptr(), dtype, ids.data_ptr(), weights.data_ptr(), tokens, experts, topk,
+                                    1 if renormalize else 0, handle)
+        if status:
+            _check(status, "w4a16_moe_topk")
 
     _launch_on(what, device, stream, call, specs)
     return ids, weights
@@ -770,10 +786,10 @@ def moe_topk_backward(dweights, logits, ids, weights, renormalize: bool = True, 
     if not isinstance(ids, _torch_preload.Tensor) or ids.dim() != 2:
         raise ValueError(f"{what}: ids must be a [tokens, topk] tensor")
     topk = ids.shape[1]
-    if not 1 <= topk <= min(experts, 64) or experts > 1024:
-        raise ValueError(f"{what}: topk = {topk} of {experts} experts: 1 <= topk <= min(experts, 64), experts <= 1024")
-    specs = [("logits", logits, _F32 + _F16, None), ("dweights", dweights, _F32, (tokens, topk)),
-             ("ids", ids, _I32, (tokens, topk)), ("weights", weights, _F32, (tokens, topk))]
+    _check_topk(what, topk, experts)
+    slots = (tokens, topk)
+    specs = [("logits", logits, _F32 + _F16, None), ("dweights", dweights, _F32, slots), ("ids", ids, _I32, slots),
+             ("weights", weights, _F32, slots)]
     if out is not None:
         specs.append(("out", out, (logits.dtype,), (tokens, experts)))
     device = _check_ffn(what, specs)
@@ -781,10 +797,12 @@ def moe_topk_backward(dweights, logits, ids, weights, renormalize: bool = True, 
     def call(handle):
         nonlocal out
         if out is None:
-            out = _torch_preload.empty((tokens, experts), dtype=logits.dtype, device=device)
-        _check(lib.w4a16_moe_topk_backward(dweights.data_ptr(), logits.data_ptr(), dtype, ids.data_ptr(),
-                                           weights.data_ptr(), out.data_ptr(), tokens, experts, topk, bool(renormalize),
-                                           handle), "w4a16_moe_topk_backward")
+            out = logits.new_empty((tokens, experts))
+        status = lib.w4a16_moe_topk_backward(dweights.data_ptr(), logits.data_ptr(), dtype, ids.data_ptr(),
+                                             weights.data_ptr(), out.data_ptr(), tokens, experts, topk,
+                                             1 if renormalize else 0, handle)
+        if status:
+            _check(status, "w4a16_moe_topk_backward")
 
     _launch_on(what, device, stream, call, specs)
     return out
