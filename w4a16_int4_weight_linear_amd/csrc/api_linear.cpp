@@ -146,6 +146,11 @@ w4a16_status w4a16_linear_backward(const uint16_t* dy, const uint16_t* pre, cons
                       {{dy, plane}, {pre, slope ? plane : 0}, {packed, n * (k / 2)}, {scales, 2 * n * (k / group)}}))
     return W4A16_ERR_OVERLAP;
   const bool product = k > 0;
+  const bool tw = product && w4a16::t_workspace_bytes(m, n, k, group, dev) != 0;
+  if (product && (slope || dbias) && w4a16::t_skinny(m, n, k, group, dev) &&
+      w4a16::linear_backward_skinny_fits((int)m, (int)n, (int)k, group, dev))
+    return status_of(w4a16::launch_linear_backward_skinny(dy, pre, dpre, dbias, packed, scales, dx, (int)m, (int)n, (int)k,
+                                                          group, activation, tw ? workspace : nullptr, dev, st));
   // (the tiled product's padded copy of its left side, where it needs one, is filled on the way)
   uint16_t* padded = product && slope && !w4a16::t_skinny(m, n, k, group, dev)
                          ? w4a16::gemm_t_padded((int)n, workspace)
@@ -159,7 +164,6 @@ w4a16_status w4a16_linear_backward(const uint16_t* dy, const uint16_t* pre, cons
     if (e != hipSuccess) return W4A16_ERR_HIP;
   }
   if (!product) return W4A16_OK;
-  const bool tw = w4a16::t_workspace_bytes(m, n, k, group, dev) != 0;
   return status_of(w4a16::launch_t(padded ? nullptr : (slope ? dpre : dy), packed, scales, dx, m, n, k, group,
                                    tw ? workspace : nullptr, dev, st));
 }

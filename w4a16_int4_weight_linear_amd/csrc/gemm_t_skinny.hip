@@ -40,6 +40,7 @@
 #include "gemm_t_skinny_plan.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "linear_epilogue.hpp"
 #include "swiglu_grad.hpp"
 
 namespace w4a16 {
@@ -57,6 +58,12 @@ constexpr int kF = CW / 16;                     // operands (columns) per lane a
 // (4) 15.3 / 15.7, 32 rows 24576 x 2048 (3) 20.6 / 21.5, 1 row 34816 x 5120 (12) 30.3 / 27.5, 32
 // rows 47.1 / 39.4; it also saves 2.7 us of the host's time per call.
 constexpr int kGradUnits = 4;
+// The same for the gradient of a linear layer's activation and bias (Slope); for rows off eight elements 1.
+// What it adds to the product against the kernel in front of it: 19 rows, 1024 x 2048 (1 unit) 2.4 / 4.8 us,
+// 1 row 2048 x 16384 (2) 2.4 / 4.7, 32 rows 4.1 / 4.8, 32 rows 5120 x 5120 (2) 4.2 / 4.8, 1 row 2048 x 32768 (4)
+// 4.6 / 4.7, 1 row 5120 x 17408 (3) 7.3 / 4.8, 32 rows 14.4 / 4.8; odd rows: 19 rows 1120 x 1001 (1) 3.8 / 4.7,
+// 32 rows 5120 x 5119 (2) 7.6 / 4.9.
+constexpr int kSlopeUnits = 2;
 
 // The same four columns of two neighbouring n.
 __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
@@ -70,12 +77,20 @@ __device__ inline uint32_t pair_perm(uint32_t w0, uint32_t w1, bool hi) {
 // the products h [M, N / 2], every wave makes its operands of d from the two, and the first
 // strip's workgroups write them to dgate_up.  One launch less than with the elementwise
 // kernel in front; see kGradUnits.
-template <int G, int MB, bool VEC, bool GRAD>
+// Slope (not GRAD): d is the gradient of act(z), gate_up holds z [M, N] and dgate_up receives d act'(z), which
+// is the operand (both null: without an activation); the first strip also writes the column sums of its
+// unrounded values, the bias's gradient: a wave has all rows of its n.
+struct SlopeArgs {
+  int act;
+  float* dbias;            // or null
+};
+template <int G, int MB, bool VEC, bool GRAD, typename... Slope>
 __global__ void __launch_bounds__(kThreads, 2)   // (two waves per SIMD: one workgroup per CU)
 gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict__ packed,
                      const uint16_t* __restrict__ scales, uint16_t* __restrict__ y, int M, int N, int K,
                      SkinnyPlan plan, float* __restrict__ partials, uint32_t* __restrict__ counters,
-                     const uint16_t* __restrict__ gate_up, uint16_t* __restrict__ dgate_up) {
+                     const uint16_t* __restrict__ gate_up, uint16_t* __restrict__ dgate_up, Slope... slope) {
+  constexpr bool kSlope = sizeof...(Slope) > 0;
   static_assert(VEC || !GRAD, "pairs are read eight elements at a time");
   constexpr int kGroups = CW / G;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -113,8 +128,12 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     u32x4 x[MB];
     u32x2 dh[GRAD ? MB : 1];
     uint32_t x4[VEC ? 1 : MB];
+    u32x4 z[kSlope ? MB : 1];
+    uint32_t z4[kSlope && !VEC ? MB : 1];
     uint16_t s[kS];
   };
+  const __amdgpu_buffer_rsrc_t zres =
+      make_rsrc(gate_up, kSlope && gate_up ? ((uint32_t)M * (uint32_t)N * 2u + 3u) & ~3u : 0u);
   auto load_unit = [&](int u, Unit& t) {
     const bool live = u < units;                                // wave-uniform
     const int n0 = n_lo + kUnit * u;
@@ -135,6 +154,9 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
       if constexpr (VEC) {
         t.x[b] = __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(dres, ok && n < N ? at : kOutOfRange, 0, 0));
+        if constexpr (kSlope)
+          t.z[b] = __builtin_bit_cast(
+              u32x4, __builtin_amdgcn_raw_buffer_load_b128(zres, ok && n < N ? at : kOutOfRange, 0, 0));
       } else {
         // the dwords that hold the eight elements, from one down to a multiple of four bytes, turned in
         // use_unit; elements past N (the next row's) are cleared there
@@ -144,6 +166,12 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
         for (int j = 0; j < 5; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b32(dres, from, 4 * j, 0);
         t.x[b] = u32x4{e[0], e[1], e[2], e[3]};
         t.x4[b] = e[4];
+        if constexpr (kSlope) {
+#pragma unroll
+          for (int j = 0; j < 5; ++j) e[j] = __builtin_amdgcn_raw_buffer_load_b32(zres, from, 4 * j, 0);
+          t.z[b] = u32x4{e[0], e[1], e[2], e[3]};
+          t.z4[b] = e[4];
+        }
       }
     }
     const uint32_t off = live ? w_v : kOutOfRange;
@@ -178,21 +206,43 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
     for (int g = 0; g < kS; ++g) *reinterpret_cast<uint16_t*>(s_w + g * kUnit * 2) = t.s[g];
     const f16x8 sc = *reinterpret_cast<const f16x8*>(s_r);
     f16x8 xv[MB];
-#pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      xv[b] = __builtin_bit_cast(f16x8, t.x[b]);
+    float sums[8] = {};                          // (Slope) over the lane's rows
+    // the eight elements of block b's row, turned and cleared past N where they came as dwords
+    auto eight = [&](const u32x4& x, uint32_t x4, int b) {
+      u32x4 v = x;
       if constexpr (!VEC) {
         const int n = n_lo + kUnit * u + 8 * lq, left = N - n;
         const uint32_t turn = ((uint32_t)(x_row + 16 * b) * (uint32_t)N & 1u) * 16u;      // n is even
-        const uint32_t from[5] = {t.x[b].x, t.x[b].y, t.x[b].z, t.x[b].w, t.x4[b]};
-        u32x4 v;
+        const uint32_t from[5] = {x.x, x.y, x.z, x.w, x4};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t e = __builtin_amdgcn_alignbit(from[j + 1], from[j], turn);
           v[j] = left >= 2 * j + 2 ? e : (left == 2 * j + 1 ? e & 0xFFFFu : 0u);
         }
-        xv[b] = __builtin_bit_cast(f16x8, v);
       }
+      return __builtin_bit_cast(f16x8, v);
+    };
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      xv[b] = eight(t.x[b], t.x4[VEC ? 0 : b], b);
+      auto times = [&](const SlopeArgs& a) {
+        const f16x8 z16 = eight(t.z[kSlope ? b : 0], t.z4[kSlope && !VEC ? b : 0], b);
+        float d[8], z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          d[e] = (float)xv[b][e];
+          z[e] = (float)z16[e];
+        }
+        times_slope(a.act, z, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          xv[b][e] = (_Float16)d[e];
+          sums[e] += d[e];
+        }
+        const int r = x_row + 16 * b, n = n_lo + kUnit * u + 8 * lq;
+        if (strip == 0 && dgate_up && r < M && n < N) store_eight<VEC>(dgate_up + (size_t)r * N + n, N - n, xv[b]);
+      };
+      (times(slope), ...);
       if constexpr (GRAD) {
         const f16x8 z = xv[b];
         using f16x4 = _Float16 __attribute__((ext_vector_type(4)));
@@ -207,6 +257,22 @@ gemm_t_skinny_kernel(const uint16_t* __restrict__ d, const uint32_t* __restrict_
         if (strip == 0 && r < M && n < N) *reinterpret_cast<f16x8*>(dgate_up + (size_t)r * N + n) = xv[b];
       }
     }
+    auto add_rows = [&](const SlopeArgs& a) {
+      if (strip != 0 || !a.dbias) return;
+      // over the sixteen lanes of a row of n (each has other rows of d); lane e < 8 stores element e
+      float mine = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float v = dpp_add<0xB1>(sums[e]);    // quad_perm [1,0,3,2]
+        v = dpp_add<0x4E>(v);                // quad_perm [2,3,0,1]
+        v = dpp_add<0x124>(v);               // row_ror:4
+        v = dpp_add<0x128>(v);               // row_ror:8
+        mine = li == e ? v : mine;
+      }
+      const int n = n_lo + kUnit * u + 8 * lq + li;
+      if (li < 8 && n < N) a.dbias[n] = mine;
+    };
+    (add_rows(slope), ...);
 #pragma unroll
     for (int wd = 0; wd < kWords; ++wd)
 #pragma unroll
@@ -354,17 +420,25 @@ auto kernel_of(int m, int n, bool grad) {
   if (n % 8 == 0) return one ? gemm_t_skinny_kernel<G, 1, true, false> : gemm_t_skinny_kernel<G, 2, true, false>;
   return one ? gemm_t_skinny_kernel<G, 1, false, false> : gemm_t_skinny_kernel<G, 2, false, false>;
 }
+template <int G>
+auto kernel_of(int m, int n, bool, const SlopeArgs&) {
+  const bool one = blocks_of(m) == 1;
+  if (n % 8 == 0)
+    return one ? gemm_t_skinny_kernel<G, 1, true, false, SlopeArgs> : gemm_t_skinny_kernel<G, 2, true, false, SlopeArgs>;
+  return one ? gemm_t_skinny_kernel<G, 1, false, false, SlopeArgs> : gemm_t_skinny_kernel<G, 2, false, false, SlopeArgs>;
+}
 
-// With gate_up: d is the gradient of h, and the pairs' gradient is written to dgate_up.
+// With gate_up: d is the gradient of h, and the pairs' gradient is written to dgate_up; with slope: see SlopeArgs.
+template <typename... Slope>
 hipError_t launch_any(const uint16_t* d, const uint16_t* gate_up, uint16_t* dgate_up, const uint32_t* packed,
                       const uint16_t* scales, uint16_t* y, int m, int n, int k, int group, void* workspace,
-                      const DeviceInfo& dev, hipStream_t stream) {
+                      const DeviceInfo& dev, hipStream_t stream, const Slope&... slope) {
   const SkinnyPlan p = skinny_plan(m, n, k, dev);
   float* partials = p.splits > 1 ? reinterpret_cast<float*>(behind_counters(workspace)) : nullptr;
   uint32_t* counters = static_cast<uint32_t*>(workspace);
-  auto kern = group == 128 ? kernel_of<128>(m, n, gate_up) : kernel_of<32>(m, n, gate_up);
+  auto kern = group == 128 ? kernel_of<128>(m, n, gate_up, slope...) : kernel_of<32>(m, n, gate_up, slope...);
   const hipError_t e = launch_kernel(kern, dim3((unsigned)(p.strips * p.splits)), dim3(kThreads), p.lds, stream, d,
-                                     packed, scales, y, m, n, k, p, partials, counters, gate_up, dgate_up);
+                                     packed, scales, y, m, n, k, p, partials, counters, gate_up, dgate_up, slope...);
   if (e != hipSuccess || p.splits == 1 || p.fused) return e;
   const int count = m * k;
   return launch_kernel(gemm_t_skinny_join_kernel, dim3((unsigned)((count / 2 + 63) / 64)), dim3(64), 0, stream,
@@ -396,6 +470,18 @@ hipError_t launch_swiglu_backward_skinny(const uint16_t* dh, const uint16_t* gat
                                          const uint32_t* packed, const uint16_t* scales, uint16_t* dx, int m, int n,
                                          int k, int group, void* workspace, const DeviceInfo& dev, hipStream_t stream) {
   return launch_any(dh, gate_up, dgate_up, packed, scales, dx, m, n, k, group, workspace, dev, stream);
+}
+
+bool linear_backward_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev) {
+  return gemm_t_skinny_fits(m, n, k, group, dev) &&
+         skinny_plan(m, n, k, dev).range <= (n % 8 == 0 ? kSlopeUnits : 1) * kWaves * kUnit;
+}
+
+hipError_t launch_linear_backward_skinny(const uint16_t* dy, const uint16_t* pre, uint16_t* dpre, float* dbias,
+                                         const uint32_t* packed, const uint16_t* scales, uint16_t* dx, int m, int n,
+                                         int k, int group, int act, void* workspace, const DeviceInfo& dev,
+                                         hipStream_t stream) {
+  return launch_any(dy, pre, dpre, packed, scales, dx, m, n, k, group, workspace, dev, stream, SlopeArgs{act, dbias});
 }
 
 }  // namespace w4a16

@@ -116,6 +116,13 @@ size_t linear_grad_workspace_bytes(int m, int n, bool bias);
 hipError_t launch_linear_grad(const uint16_t* dy, const uint16_t* pre, uint16_t* dpre, uint16_t* padded, float* dbias,
                               int m, int n, int act, uint32_t* counters, float* partials, hipStream_t stream);
 
+// The same within the weight-streaming product that follows it (gemm_t_skinny.hip), for few rows and short ranges.
+bool linear_backward_skinny_fits(int m, int n, int k, int group, const DeviceInfo& dev);
+hipError_t launch_linear_backward_skinny(const uint16_t* dy, const uint16_t* pre, uint16_t* dpre, float* dbias,
+                                         const uint32_t* packed, const uint16_t* scales, uint16_t* dx, int m, int n,
+                                         int k, int group, int act, void* workspace, const DeviceInfo& dev,
+                                         hipStream_t stream);
+
 // ---- workspaces of the feed-forward block's operators ----
 // A workspace begins with arrival counters, all 0 between calls (zero-filled once by the
 // caller); the sizes below include them.  Everything behind holds nothing between calls.

@@ -107,6 +107,29 @@ __device__ inline void times_slope(int act, const float (&z)[N], float (&d)[N]) 
   });
 }
 
+// Eight elements of a row (left: how many of them there are).  VEC: on 16 bytes; else two-byte alignment.
+template <bool VEC>
+__device__ inline void store_eight(uint16_t* p, int left, const f16x8& o) {
+  if constexpr (VEC) {
+    *reinterpret_cast<f16x8*>(p) = o;
+  } else {
+    const u32x4 v = __builtin_bit_cast(u32x4, o);
+    if (left < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
+    } else if (reinterpret_cast<uintptr_t>(p) & 2) {
+      p[0] = (uint16_t)v[0];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) *reinterpret_cast<uint32_t*>(p + 1 + 2 * j) = __builtin_amdgcn_alignbit(v[j + 1], v[j], 16);
+      p[7] = (uint16_t)(v[3] >> 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(p + 2 * j) = v[j];
+    }
+  }
+}
+
 // One output: element `at` of y (and of residual and pre), column n, from the product's sum v.
 __device__ inline void store_result(uint16_t* y, size_t at, int, float v) { y[at] = float_to_half_bits(v); }
 __device__ inline void store_result(uint16_t* y, size_t at, int n, float v, const LinearEpilogue& ep) {

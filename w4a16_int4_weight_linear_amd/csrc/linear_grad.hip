@@ -1,6 +1,7 @@
 // linear_grad.hip -- gradient of the linear layer's epilogue on gfx950: dz = dy act'(z) in fp32, rounded
 // once to fp16 (an output, and the fp16 operand of the product that follows), and the bias's
-// gradient, the column sums of the unrounded dz in fp32.
+// gradient, the column sums of the unrounded dz in fp32.  (Few rows and short ranges: within the
+// product itself, gemm_t_skinny.hip.)
 //
 // Bound by memory: 6 bytes per element.  A workgroup takes 128 columns of kRowsWG rows, sixteen
 // threads of eight columns side by side, sixteen rows at a time; column sums meet in LDS, and the
@@ -74,28 +75,6 @@ __device__ inline void turn_eight(const Eight& e, uint32_t at, int left, float (
 #pragma unroll
   for (int i = 0; i < 8; ++i) out[i] = VEC || i < left ? (float)h[i] : 0.0f;
 }
-template <bool VEC>
-__device__ inline void store_eight(uint16_t* p, int left, const f16x8& o) {
-  if constexpr (VEC) {
-    *reinterpret_cast<f16x8*>(p) = o;
-  } else {
-    const u32x4 v = __builtin_bit_cast(u32x4, o);
-    if (left < 8) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
-    } else if (reinterpret_cast<uintptr_t>(p) & 2) {
-      p[0] = (uint16_t)v[0];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) *reinterpret_cast<uint32_t*>(p + 1 + 2 * j) = __builtin_amdgcn_alignbit(v[j + 1], v[j], 16);
-      p[7] = (uint16_t)(v[3] >> 16);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(p + 2 * j) = v[j];
-    }
-  }
-}
-
 // VEC: rows of n start on eight elements.  SLOPE: dz is written (pre given); else only the sums of dy.
 template <bool VEC, bool SLOPE>
 __global__ void __launch_bounds__(kThreads)
