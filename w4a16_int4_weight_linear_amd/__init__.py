@@ -413,8 +413,11 @@ def _launch_on(what, device, stream, call, specs=()):
 
 
 if _torch_preload is not None:
-    # The current device's index, and the handle of a device's current stream: torch's raw getters, where it has them,
-    # build no objects and skip the initialisation that a device tensor has behind it.
+    # Whether the current stream is being captured, the current device's index, and the handle of a device's current
+    # stream: torch's raw getters, where it has them, build no objects and skip the initialisation that a device
+    # tensor has behind it.
+    _capturing = getattr(_torch_preload._C, "_cuda_isCurrentStreamCapturing", None) or \
+        _torch_preload.cuda.is_current_stream_capturing
     _current_device = getattr(_torch_preload._C, "_cuda_getDevice", None) or _torch_preload.cuda.current_device
     _current_handle = getattr(_torch_preload._C, "_cuda_getCurrentRawStream", None) or \
         (lambda index: _torch_preload.cuda.current_stream(index).cuda_stream)
@@ -464,7 +467,7 @@ def _kept_workspace(nbytes, device, handle):
     """A workspace of at least nbytes for a call on stream `handle` of the current device."""
     if nbytes == 0:
         return 0, 0, None
-    if _torch_preload.cuda.is_current_stream_capturing():
+    if _capturing():
         ws = _new_workspace(nbytes, device)
         return ws.data_ptr(), nbytes, ws     # freed to the graph's pool, whose later work is ordered behind this call
     key = (device.index, handle)
@@ -820,16 +823,19 @@ def moe_ffn(x, ids, weights, gate_up, gate_up_scales, down, down_scales, group: 
     gate and up rows, down [experts, hidden, inter/8]; ids and weights [tokens, topk] as moe_topk gives them;
     residual may be `out`."""
     what = "moe_ffn"
-    tensor = _torch_preload.Tensor
-    for name, t, dims in (("x", x, 2), ("ids", ids, 2), ("gate_up", gate_up, 3), ("down", down, 3)):
-        if not isinstance(t, tensor):
-            raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}")
-        if t.dim() != dims:
-            raise ValueError(f"{what}: {name} must be {dims}-D")
+    try:
+        (tokens, hidden), (_, topk) = x.shape, ids.shape
+        (experts, _, _), (_, _, words) = gate_up.shape, down.shape
+    except (AttributeError, TypeError, ValueError):
+        for name, t, dims in (("x", x, 2), ("ids", ids, 2), ("gate_up", gate_up, 3), ("down", down, 3)):
+            if not isinstance(t, _torch_preload.Tensor):
+                raise TypeError(f"{what}: {name} must be a torch.Tensor, not {type(t).__name__}") from None
+            if t.dim() != dims:
+                raise ValueError(f"{what}: {name} must be {dims}-D") from None
+        raise
+    inter = words * 8
     if group not in (32, 128):
         raise ValueError(f"{what}: the group size must be 32 or 128 (got {group})")
-    (tokens, hidden), topk = x.shape, ids.shape[1]
-    experts, inter = gate_up.shape[0], down.shape[2] * 8
     if hidden % group or inter % group:
         raise ValueError(f"{what}: hidden = {hidden} and inter = {inter} must be multiples of the group size {group}")
     specs = [("x", x, _F16, None), ("ids", ids, _I32, (tokens, topk)), ("weights", weights, _F32, (tokens, topk)),
