@@ -454,7 +454,7 @@ w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, 
                                      int32_t topk, int32_t renormalize, w4a16_stream_t stream);
 
 /*
- * The routed experts' whole feed-forward for a few tokens (decoding), in two kernels:
+ * The routed experts' whole feed-forward for a few tokens (decoding), in two or three kernels:
  *
  *     y[t] = residual[t] + sum_s weights[t, s] * W2[e] . (SiLU(g) * u),  (g, u) = W1[e] . x[t],  e = ids[t, s]
  *
@@ -462,9 +462,10 @@ w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, 
  * fp32 [tokens, topk] as w4a16_moe_topk writes them (an id outside [0, experts) contributes nothing; a token
  * may name an expert twice); gate_up [experts, 2 inter, hidden/8] and its scales interleave gate (even) and up
  * rows as for w4a16_grouped_gemm_swiglu, down [experts, hidden, inter/8] and its scales as for
- * w4a16_grouped_gemm.  Each used expert's weights are read once, and exactly; sums are fp32; SiLU(g) u
- * is kept to 22 bits between the kernels (up to 2^24 in size); slots are added in order, with the
- * residual, and y is rounded once.  A not finite x leaves its own token's outputs alone not finite.
+ * w4a16_grouped_gemm.  Weights are exact; up to 64 pairs (tokens * topk) each reads its expert's for
+ * itself, beyond that every four pairs of an expert share one read.  Sums are fp32; SiLU(g) u is kept to
+ * 22 bits between the kernels (up to 2^24 in size); slots are added in order, with the residual, and y is
+ * rounded once.  A not finite x leaves its own token's outputs alone not finite.
  * 1 <= tokens <= 64 and tokens * topk <= 512, hidden and inter multiples of group and at least one group,
  * one expert's weights below 2 GiB (else W4A16_ERR_SHAPE; banks may be larger than that).  For more tokens:
  * w4a16_moe_route, w4a16_grouped_gemm_swiglu, w4a16_grouped_gemm, w4a16_moe_combine.  Workspace

@@ -1,4 +1,4 @@
-// moe_ffn.hip -- the routed experts' feed-forward for a few tokens, in two kernels on gfx950.
+// moe_ffn.hip -- the routed experts' feed-forward for a few tokens, in two or three kernels on gfx950.
 //
 //     y[t] = residual[t] + sum_s w[t, s] * W2[e] h(t, s),   e = ids[t, s],
 //     h(t, s) = SiLU(g) u,   (g, u) = W1[e] x[t]
@@ -22,6 +22,15 @@
 // the scale is applied to the fp32 result: weights are exact.  The MFMA wants neighbouring lanes on
 // different weight rows; loaded so, every four lanes touch four cache lines.  So weights and scales are loaded
 // with sixteen lanes side by side on a row and the lanes are permuted afterwards (spread_rows).
+//
+// The grouped products take one workgroup's loads at a time and hide them behind three others on the CU
+// (64 VGPRs, four workgroups of 512 threads); with the next piece in registers instead and fewer of them 64
+// tokens take 62 + 37 us instead of 56 + 38.  Weight loads bypass the caches' retention (kStream): 66 against 104 us.
+//
+// Measured (MI355X, operands from memory; 2048 x 512, group 32, 256 experts, 8 slots a token): 1 token 5.2 + 5.4 us
+// (launch and one trip to memory each), 8 tokens 15.6 + 12.3, 16 tokens 28 + 20 + 5, 32 tokens 42 + 29 + 5, 64
+// tokens 56 + 38 + 5 us: 391 MB of used experts' weights at 4.2 TB/s, against 4.9 of a large copy.  What is
+// left is the fixed part (launch, sorting the pairs, the last work items) and the third kernel.
 //
 // h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11 (22 bits, |h| up to 2^24):
 // rounded once to fp16 it would add as much error again as the rounding of y.
@@ -198,7 +207,6 @@ __device__ inline uint32_t offset_if(bool in, uint32_t off) {
   return v;
 }
 
-
 // A value as the two parts of h.
 __device__ inline void split_h(float v, uint16_t& hi, uint16_t& lo) {
   const _Float16 h = (_Float16)v;
@@ -221,6 +229,9 @@ __device__ inline uint32_t h_place(uint32_t k, uint32_t rows, uint32_t row) {
 __host__ __device__ inline int h_steps(int inter) { return (inter + kStepK - 1) / kStepK; }
 
 // ---- few pairs: each by itself ----
+// Up to this many: two launches and no sorting.  Direct against grouped, 64 pairs: of experts that are nearly all
+// different 15.6 + 12.3 against 21.0 + 15.5 + 4.8 us, of twelve experts 14.8 + 12.0 against 12.4 + 10.1 + 4.8.  (Also
+// what moe_down_direct_kernel holds: an id per lane, a result per pair in LDS.)
 constexpr int kDirectPairs = 64;
 constexpr int kBandRows = 4 * kWaves;            // gate/up rows of a workgroup: four per wave
 constexpr int kXSteps = 4;                       // steps of a staged piece of x
@@ -514,7 +525,7 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
 
 // Down: a work item is (block, band of 64 columns), eight columns per wave; a piece of one is 512 k.  part
 // [pair][N] fp32 receives the pairs' results.
-constexpr int kDownGroups = 2;                   // groups of four columns per wave
+constexpr int kDownGroups = 2;                   // groups of four columns per wave (4: 64 tokens 41.2 against 38.2 us)
 constexpr int kDownCols = 4 * kDownGroups * kWaves;
 
 template <int G>
