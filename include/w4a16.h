@@ -432,8 +432,9 @@ w4a16_status w4a16_moe_combine(const uint16_t* y_pairs, const int32_t* pair_row,
  * with j over all experts, or over the chosen ones if `renormalize` is not 0.  An expert whose logit is
  * -inf is masked out: it is never chosen, and a slot that is left without an expert gets id -1 and weight
  * 0, which w4a16_moe_route and w4a16_moe_ffn pass over (so a token may have none).  NaN counts as the
- * largest logit; a NaN or +inf among the logits that the sum covers leaves the token's weights NaN.  1 <= topk <= experts <= 1024, topk
- * <= 64 (else W4A16_ERR_SHAPE); an unknown dtype is W4A16_ERR_RANGE.  No workspace.
+ * largest logit; a NaN or +inf among the logits that the sum covers leaves the token's weights NaN.
+ * tokens < 2^26, 1 <= topk <= experts <= 1024, topk <= 64 (else W4A16_ERR_SHAPE); an unknown dtype is
+ * W4A16_ERR_RANGE.  No workspace.
  */
 w4a16_status w4a16_moe_topk(const void* logits, int32_t dtype, int32_t* ids, float* weights, int64_t tokens,
                             int32_t experts, int32_t topk, int32_t renormalize, w4a16_stream_t stream);

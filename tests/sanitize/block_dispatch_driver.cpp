@@ -214,6 +214,7 @@ static void moe() {
   EXPECT(topk(l, ids, at<float>(1, 156), 10, 64, 4, W4A16_F32) == kNo && topk(l, ids, at<float>(1, 160), 10, 64, 4, W4A16_F32) == kOk);
   // 8 Mi tokens of 1024 experts: 32 GiB of logits are past the next operands
   EXPECT(topk(l, ids, wt, 1 << 23, 1024, 4, W4A16_F32) == kNo && topk(l, at<int32_t>(7), at<float>(8), 1 << 23, 1024, 4, W4A16_F32) == kOk);
+  EXPECT(topk(l, at<int32_t>(7), at<float>(8), (1 << 26) - 1, 8, 4, W4A16_F16) == kOk && topk(l, ids, wt, 1 << 26, 8, 4, W4A16_F16) == W4A16_ERR_SHAPE);
   auto grad = [&](float* d, const void* l_, void* o, int32_t renorm) {
     return ran(w4a16_moe_topk_backward(d, l_, W4A16_F32, ids, wt, o, 10, 64, 4, renorm, nullptr));
   };

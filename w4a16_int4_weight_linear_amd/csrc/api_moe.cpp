@@ -22,7 +22,7 @@ using w4a16::valid_group;
 
 int topk_checks(int32_t dtype, int64_t tokens, int32_t experts, int32_t topk) {
   if (dtype != W4A16_F32 && dtype != W4A16_F16) return W4A16_ERR_RANGE;
-  if (tokens < 0 || tokens > kMaxDim || topk < 1 || topk > experts || topk > w4a16::kMoeTopkSlots ||
+  if (tokens < 0 || tokens > w4a16::kMoeTopkTokens || topk < 1 || topk > experts || topk > w4a16::kMoeTopkSlots ||
       experts > w4a16::kMoeTopkExperts)
     return W4A16_ERR_SHAPE;
   return W4A16_OK;
