@@ -55,71 +55,97 @@ constexpr float kHScale = 0x1p-8f, kLoScale = 0x1p11f;
 
 // The pairs in blocks of up to four of one expert each.
 struct Blocks {
-  unsigned long long val[2 * kMoeFfnPairs];      // of the expert in this place: its pairs per wave (a byte
-                                                 // each), then its first block
-  int key[2 * kMoeFfnPairs];                     // an expert's place (open addressing; -1: free)
   int expert[kMoeFfnPairs];                      // of block b
   uint16_t size[kMoeFfnPairs];                   // its pairs: 1 .. 4,
   uint16_t pair[kMoeFfnPairs * kBlock];          // pair[4 b + i]
-  uint32_t wave_sum[kWaves];
+  int total, unused[3];
 };
+static_assert(sizeof(Blocks) % 16 == 0 && sizeof(Blocks) / 16 <= kThreads, "copied in one go, 16 bytes per thread");
+// What sorting them needs: an expert's place (open addressing) has
+struct Places {
+  unsigned long long count[2 * kMoeFfnPairs];    // its pairs in each wave, a byte each
+  uint32_t key[2 * kMoeFfnPairs];                // the expert (kFree: none); then its first block among those of the wave
+                                                 // that has its first pair (low half), and that wave
+  uint32_t wave_blocks[kWaves];                  // blocks whose expert's first pair is in this wave
+};
+constexpr uint32_t kFree = 0xFFFFFFFFu;
+constexpr int kPlaceBits = 10;
+static_assert(2 * kMoeFfnPairs == 1 << kPlaceBits, "places");
 
-// Sum of eight bytes (up to 512).
-__device__ inline uint32_t byte_sum(unsigned long long v) {
-  v = (v & 0x00FF00FF00FF00FFull) + ((v >> 8) & 0x00FF00FF00FF00FFull);
-  return (uint32_t)((v * 0x0001000100010001ull) >> 48);
+// Sum over a wave's lanes up to and with this one (DPP: shifts within rows, then whole rows).
+__device__ inline uint32_t wave_scan(uint32_t v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});      // row_shr:1, 2, 4, 8
+  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});      // row_bcast:15 to rows 1 and 3
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});      // row_bcast:31 to rows 2 and 3
+  return v;
 }
 
 // Sorts the pairs; returns the number of blocks.  Blocks and their pairs are in the pairs' order, the same in
-// every workgroup (which share the blocks out).  Pairs whose id is no expert are in no block.
-__device__ inline int group_pairs(Blocks& s, const int32_t* __restrict__ ids, int pairs, int experts) {
+// every workgroup (which share the blocks out), whatever order the atomics take.  Pairs whose id is no expert are in
+// no block.  All waves do this at once, so its instructions count (the first form, a loop over the lanes for a pair's
+// rank and counters in 64-bit atomics, cost 600 a wave, as much as a third of the weights' arithmetic).
+__device__ inline int group_pairs(Blocks& s, Places& q, const int32_t* __restrict__ ids, int pairs, int experts) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = tid < pairs ? ids[tid] : -1;
   const bool known = e >= 0 && e < experts;
 #pragma unroll
   for (int i = 0; i < 2 * kMoeFfnPairs; i += kThreads) {
-    s.key[tid + i] = -1;
-    s.val[tid + i] = 0;
+    q.key[tid + i] = kFree;
+    q.count[tid + i] = 0;
   }
   __syncthreads();
-  uint32_t at = 0, rank = 0;
+  uint32_t at = 0;
   if (known) {
     // (512 pairs at most in 1024 places: a free one is found)
-    at = ((uint32_t)e * 0x9E3779B1u) >> 22;
-    for (int k = atomicCAS(&s.key[at], -1, e); k != -1 && k != e; k = atomicCAS(&s.key[at], -1, e)) at = (at + 1) & 1023u;
-    atomicAdd(&s.val[at], 1ull << (8 * wave));
+    const uint32_t want = (uint32_t)e;
+    at = (want * 0x9E3779B1u) >> (32 - kPlaceBits);
+    for (uint32_t k = atomicCAS(&q.key[at], kFree, want); k != kFree && k != want; k = atomicCAS(&q.key[at], kFree, want))
+      at = (at + 1) & (2 * kMoeFfnPairs - 1);
   }
-  for (int l = 0; l < pairs - 64 * wave && l < 63; ++l)     // the wave's pairs of this expert before this one
-    rank += lane > l && __builtin_amdgcn_readlane(e, l) == e ? 1u : 0u;
-  __syncthreads();
-  const unsigned long long counts = known ? s.val[at] : 0ull;
-  const uint32_t count = byte_sum(counts);
-  if (known) rank += byte_sum(counts & ((1ull << (8 * wave)) - 1));    // (and those of the waves before: eight at most)
-  const uint32_t mine = known && rank == 0 ? (count + kBlock - 1) / kBlock : 0u;      // blocks of the expert
-  uint32_t upto = mine;                                     // sum over this wave's lanes so far
+  unsigned long long same = __ballot(known);                // the wave's pairs of this expert
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t v = (uint32_t)__shfl_up((int)upto, d, 64);
-    if (lane >= d) upto += v;
+  for (int b = 0; b < kPlaceBits; ++b) {
+    const int bit = (int)(at << (31 - b)) >> 31;            // 0 or -1
+    same &= ~(__ballot(bit != 0) ^ (unsigned long long)(long long)bit);
   }
-  if (lane == 63) s.wave_sum[wave] = upto;
+  uint32_t rank = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0));
+  if (known && rank == 0) reinterpret_cast<uint8_t*>(&q.count[at])[wave] = (uint8_t)__popcll(same);
   __syncthreads();
-  uint32_t before = 0, total = 0;
+  const unsigned long long counts = known ? q.count[at] : 0ull, ahead = counts & ((1ull << (8 * wave)) - 1);
+  auto bytes = [](unsigned long long v) {
+    return __builtin_amdgcn_sad_u8((uint32_t)(v >> 32), 0, __builtin_amdgcn_sad_u8((uint32_t)v, 0, 0));
+  };
+  const uint32_t count = bytes(counts);
+  rank += bytes(ahead);
+  const uint32_t mine = known && rank == 0 ? (count + kBlock - 1) / kBlock : 0u;      // blocks of the expert
+  const uint32_t upto = wave_scan(mine);
+  if (lane == 63) q.wave_blocks[wave] = upto;
+  if (mine) q.key[at] = (upto - mine) | (uint32_t)wave << 16;
+  __syncthreads();
+  const uint32_t place = known ? q.key[at] : 0u;
+  uint32_t before = place & 0xFFFFu, total = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? s.wave_sum[w] : 0u;
-    total += s.wave_sum[w];
+    const uint32_t n = q.wave_blocks[w];
+    before += (uint32_t)w < place >> 16 ? n : 0u;
+    total += n;
   }
-  if (mine) s.val[at] = before + upto - mine;
-  __syncthreads();
   if (known) {
-    const uint32_t b = (uint32_t)s.val[at] + rank / kBlock;
+    const uint32_t b = before + rank / kBlock;
     s.pair[kBlock * b + rank % kBlock] = (uint16_t)tid;
     if (rank % kBlock == 0) {
       s.expert[b] = e;
       s.size[b] = (uint16_t)min((uint32_t)kBlock, count - rank);
     }
   }
+  if (tid == 0) s.total = (int)total;
   __syncthreads();
   return __builtin_amdgcn_readfirstlane((int)total);
 }
@@ -400,6 +426,7 @@ moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict
 }
 
 // ---- more pairs: an expert's blocks ----
+constexpr size_t kBlocksBytes = (sizeof(Blocks) + 255) & ~(size_t)255;
 constexpr int kXPitch = kXK * 2 + 16;            // bytes per staged row of x: rows shift by 4 banks
 constexpr int kXBuf = kBlock * kXPitch;
 constexpr uint32_t kHStep = 2 * kBlock * kStepK * 2;   // bytes of a block's h per step: upper parts, then lower parts
@@ -409,14 +436,18 @@ constexpr uint32_t kHStep = 2 * kBlock * kStepK * 2;   // bytes of a block's h p
 template <int G>
 __global__ void __launch_bounds__(kThreads, 8)
 moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
-                   const uint16_t* __restrict__ scales, uint16_t* __restrict__ h, int pairs, int topk, int experts,
-                   int rows, int K, int bands) {
+                   const uint16_t* __restrict__ scales, uint16_t* __restrict__ h, Blocks* __restrict__ blocks, int pairs,
+                   int topk, int experts, int rows, int K, int bands) {
   __shared__ __attribute__((aligned(16))) uint8_t xs[kXBuf];
   __shared__ __attribute__((aligned(16))) Blocks bl;
+  __shared__ Places places;
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int li = lane & 3, c = lane >> 2;        // weight row (and A row), chunk
-  const int total = group_pairs(bl, ids, pairs, experts);
+  const int total = group_pairs(bl, places, ids, pairs, experts);
+  // for the down product (the last workgroup: the others have as many work items or one more)
+  if (blockIdx.x + 1 == gridDim.x && threadIdx.x < sizeof(Blocks) / 16)
+    reinterpret_cast<u32x4*>(blocks)[threadIdx.x] = reinterpret_cast<const u32x4*>(&bl)[threadIdx.x];
 
   const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
   const int pieces = (K + kXK - 1) / kXK;
@@ -530,15 +561,17 @@ constexpr int kDownCols = 4 * kDownGroups * kWaves;
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 8)
-moe_down_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const uint32_t* __restrict__ packed,
-                const uint16_t* __restrict__ scales, float* __restrict__ part, int pairs, int experts, int N, int K,
-                int bands) {
+moe_down_kernel(const uint16_t* __restrict__ h, const Blocks* __restrict__ blocks, const uint32_t* __restrict__ packed,
+                const uint16_t* __restrict__ scales, float* __restrict__ part, int N, int K, int bands) {
   __shared__ __attribute__((aligned(16))) uint8_t hs[kHStep];
   __shared__ __attribute__((aligned(16))) Blocks bl;
   const int lane = threadIdx.x & 63;
   const int wave = uniform(threadIdx.x >> 6);
   const int c = lane >> 2;
-  const int total = group_pairs(bl, ids, pairs, experts);
+  if (threadIdx.x < sizeof(Blocks) / 16)
+    reinterpret_cast<u32x4*>(&bl)[threadIdx.x] = reinterpret_cast<const u32x4*>(blocks)[threadIdx.x];
+  __syncthreads();
+  const int total = uniform(bl.total);
 
   const uint32_t row_w = (uint32_t)K >> 1, spr = (uint32_t)K / G;
   const int steps = h_steps(K);
@@ -672,7 +705,7 @@ moe_ffn_combine_kernel(const float* __restrict__ part, const int32_t* __restrict
 size_t moe_ffn_workspace_bytes(int pairs, int hidden, int inter) {
   if (pairs <= kDirectPairs) return kCounterBytes + (size_t)pairs * h_steps(inter) * kDirectStep;
   // (as many blocks as pairs at most)
-  return kCounterBytes + (size_t)pairs * h_steps(inter) * kHStep + (size_t)pairs * hidden * sizeof(float);
+  return kCounterBytes + kBlocksBytes + (size_t)pairs * h_steps(inter) * kHStep + (size_t)pairs * hidden * sizeof(float);
 }
 
 hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
@@ -692,6 +725,8 @@ hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* we
                          dim3(kThreads), 0, stream, h, ids, weights, down, down_scales, residual, y, pairs, topk, tokens,
                          experts, hidden, inter);
   }
+  Blocks* blocks = reinterpret_cast<Blocks*>(behind_counters(workspace));
+  h += kBlocksBytes / sizeof(uint16_t);
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + (size_t)pairs * h_steps(inter) * kHStep);
   const int down_bands = (hidden + kDownCols - 1) / kDownCols;
   // four workgroups per CU, fewer where there are fewer work items
@@ -700,10 +735,10 @@ hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* we
     return dim3((unsigned)(items < 4 * dev.num_cu ? items : 4 * dev.num_cu));
   };
   hipError_t e = launch_kernel(g32 ? moe_gate_up_kernel<32> : moe_gate_up_kernel<128>, grid(up_bands), dim3(kThreads), 0, stream,
-                               x, ids, gate_up, gate_up_scales, h, pairs, topk, experts, 2 * inter, hidden, up_bands);
+                               x, ids, gate_up, gate_up_scales, h, blocks, pairs, topk, experts, 2 * inter, hidden, up_bands);
   if (e != hipSuccess) return e;
-  e = launch_kernel(g32 ? moe_down_kernel<32> : moe_down_kernel<128>, grid(down_bands), dim3(kThreads), 0, stream, h, ids, down,
-                    down_scales, part, pairs, experts, hidden, inter, down_bands);
+  e = launch_kernel(g32 ? moe_down_kernel<32> : moe_down_kernel<128>, grid(down_bands), dim3(kThreads), 0, stream, h,
+                    blocks, down, down_scales, part, hidden, inter, down_bands);
   if (e != hipSuccess) return e;
   return launch_kernel(moe_ffn_combine_kernel, dim3((unsigned)((hidden + 1023) / 1024), (unsigned)tokens), dim3(256), 0, stream,
                        part, ids, weights, residual, y, topk, experts, hidden);
