@@ -467,8 +467,8 @@ w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, 
  * itself, beyond that every four pairs of an expert share one read.  Sums are fp32; SiLU(g) u is kept to
  * 22 bits between the kernels (up to 2^24 in size); slots are added in order, with the residual, and y is
  * rounded once.  A not finite x leaves its own token's outputs alone not finite.
- * 1 <= tokens <= 64 and tokens * topk <= 512, hidden and inter multiples of group and at least one group,
- * one expert's weights below 2 GiB (else W4A16_ERR_SHAPE; banks may be larger than that).  For more tokens:
+ * 1 <= tokens <= 64 and tokens * topk <= 512, hidden and inter multiples of group and at least one group, hidden
+ * <= 2^24, one expert's weights below 2 GiB (else W4A16_ERR_SHAPE; banks may be larger than that).  For more tokens:
  * w4a16_moe_route, w4a16_grouped_gemm_swiglu, w4a16_grouped_gemm, w4a16_moe_combine.  Workspace
  * (w4a16_moe_ffn_workspace_bytes) as for w4a16_gemm_swiglu, which may share one with it; sharing
  * of memory other than residual = y is W4A16_ERR_OVERLAP; tokens == 0 or hidden == 0 is a no-op.

@@ -200,6 +200,7 @@ static void moe() {
   EXPECT(ffn(res, at<uint16_t>(4, words / 8 - 16), 4, 2, 4096, 1024, 1024) == kNo);
   EXPECT(ffn(res, at<uint16_t>(4, words / 8), 4, 2, 4096, 1024, 1024) == kOk);
   EXPECT(ffn(res, out, 4, 2, 8, 65536, 32768) == W4A16_ERR_SHAPE);                              // an expert of 2 GiB
+  EXPECT(ffn(res, out, 4, 2, 8, 1 << 24, 32) == kOk && ffn(res, out, 4, 2, 8, (1 << 24) + 32, 32) == W4A16_ERR_SHAPE);
   g_ans = {};
 
   int32_t* const ids = at<int32_t>(1);

@@ -32,7 +32,7 @@ int ffn_sizes(int64_t tokens, int32_t topk, int64_t hidden, int64_t inter, int32
   if (!valid_group(group)) return W4A16_ERR_GROUP;
   if (tokens < 0 || tokens > kMoeFfnTokens || topk < 1 || topk > kMoeFfnPairs || tokens * topk > kMoeFfnPairs)
     return W4A16_ERR_SHAPE;
-  if (hidden < 0 || hidden > kMaxDim || hidden % group || inter < group || inter > kMaxDim || inter % group)
+  if (hidden < 0 || hidden > w4a16::kMoeFfnHidden || hidden % group || inter < group || inter > kMaxDim || inter % group)
     return W4A16_ERR_SHAPE;
   // one expert's weights in 32-bit offsets
   if (inter * hidden >= kMaxBufferBytes) return W4A16_ERR_SHAPE;

@@ -207,6 +207,7 @@ hipError_t launch_moe_topk_backward(const float* dweights, const void* logits, b
 // ---- the routed experts' feed-forward for a few tokens (moe_ffn.hip) ----
 // residual may be null, or y itself.  The workspace needs no initial state behind its counters.
 constexpr int kMoeFfnTokens = 64, kMoeFfnPairs = 512;          // most tokens, most (token, slot) pairs
+constexpr int kMoeFfnHidden = 1 << 24;                         // widest: 1024 threads per 8 columns, below 2^32
 size_t moe_ffn_workspace_bytes(int pairs, int hidden, int inter);
 hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* weights, const uint32_t* gate_up,
                           const uint16_t* gate_up_scales, const uint32_t* down, const uint16_t* down_scales,

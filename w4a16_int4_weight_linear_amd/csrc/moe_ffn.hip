@@ -10,9 +10,9 @@
 //   rows).  Down and combine: a workgroup per 8 output columns, a wave per pair; the pairs' results meet
 //   in LDS and the router's weights add them in slot order with the residual.
 // * More pairs: three kernels.  In both products the workgroups walk over (block of up to four pairs of one
-//   expert, band of weight rows), the next one's loads in flight while this one is computed, so an expert's
-//   weights are read once for every four of its pairs; each workgroup sorts the pairs into blocks
-//   itself (group_pairs).  A third kernel adds a token's results with the router's weights.
+//   expert, band of weight rows), so an expert's weights are read once for every four of its pairs; each workgroup
+//   of the first sorts the pairs into blocks itself (group_pairs), the second reads the lists.  A third kernel adds a
+//   token's results with the router's weights.
 // No atomics on results and no order that depends on timing: a token's output has the same bits in any batch
 // of the same kind.
 //
@@ -25,12 +25,13 @@
 //
 // The grouped products take one workgroup's loads at a time and hide them behind three others on the CU
 // (64 VGPRs, four workgroups of 512 threads); with the next piece in registers instead and fewer of them 64
-// tokens take 62 + 37 us instead of 56 + 38.  Weight loads bypass the caches' retention (kStream): 66 against 104 us.
+// tokens took 62 + 37 us instead of 56 + 38 (as they were then).  Weight loads bypass the caches' retention (kStream):
+// the first product 66 instead of 104 us, both as they were then.
 //
-// Measured (MI355X, operands from memory; 2048 x 512, group 32, 256 experts, 8 slots a token): 1 token 5.2 + 5.4 us
-// (launch and one trip to memory each), 8 tokens 15.6 + 12.3, 16 tokens 28 + 20 + 5, 32 tokens 42 + 29 + 5, 64
-// tokens 56 + 38 + 5 us: 391 MB of used experts' weights at 4.2 TB/s, against 4.9 of a large copy.  What is
-// left is the fixed part (launch, sorting the pairs, the last work items) and the third kernel.
+// Measured (MI355X, operands from memory; 2048 x 512, group 32, 256 experts, 8 slots a token): 1 token 5.2 + 5.0 us
+// (launch and one trip to memory each), 8 tokens 15.3 + 10.3, 16 tokens 25 + 15.5 + 5, 32 tokens 37 + 23 + 5, 64
+// tokens 51 + 31.5 + 5 us: 391 MB of used experts' weights at 4.7 TB/s over both products, against 4.9 of a large
+// copy.  What is left is the fixed part (launch, sorting the pairs, the last work items) and the third kernel.
 //
 // h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11 (22 bits, |h| up to 2^24):
 // rounded once to fp16 it would add as much error again as the rounding of y.
@@ -255,9 +256,10 @@ __device__ inline uint32_t h_place(uint32_t k, uint32_t rows, uint32_t row) {
 __host__ __device__ inline int h_steps(int inter) { return (inter + kStepK - 1) / kStepK; }
 
 // ---- few pairs: each by itself ----
-// Up to this many: two launches and no sorting.  Direct against grouped, 64 pairs: of experts that are nearly all
-// different 15.6 + 12.3 against 21.0 + 15.5 + 4.8 us, of twelve experts 14.8 + 12.0 against 12.4 + 10.1 + 4.8.  (Also
-// what moe_down_direct_kernel holds: an id per lane, a result per pair in LDS.)
+// Up to this many: two launches and no sorting.  Direct against grouped: 32 pairs of experts that are nearly all
+// different 9.4 + 6.7 against 10.9 + 6.9 + 4.8 us, 64 pairs 15.3 + 10.3 against 17.2 + 10.9 + 4.9; of twelve experts 32 pairs 9.1
+// + 6.7 against 7.7 + 5.2 + 4.9, 64 pairs 14.0 + 9.7 against 9.3 + 5.7 + 4.9 (the host cannot know which).  Also what
+// moe_down_direct_kernel holds: an id per lane, a result per pair in LDS.
 constexpr int kDirectPairs = 64;
 constexpr int kBandRows = 4 * kWaves;            // gate/up rows of a workgroup: four per wave
 constexpr int kXSteps = 4;                       // steps of a staged piece of x
@@ -325,10 +327,12 @@ moe_gate_up_direct_kernel(const uint16_t* __restrict__ x, const int32_t* __restr
   }
 }
 
-constexpr int kDepth = 3;                        // steps in flight per wave
+// (sixteen waves, a step of one pair at a time each: 2 tokens 5.1, 8 tokens 10.3 us; eight waves with three steps in
+// flight 6.4 and 12.3, with two 5.6 and 10.8; sixteen with three, more code than they save, 8.3 and 14.2)
+constexpr int kDirectWaves = 16;
 
 template <int G>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(64 * kDirectWaves)
 moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict__ ids, const float* __restrict__ weights,
                        const uint32_t* __restrict__ packed, const uint16_t* __restrict__ scales, const uint16_t* residual,
                        uint16_t* y, int pairs, int topk, int tokens, int experts, int N, int K) {
@@ -347,76 +351,46 @@ moe_down_direct_kernel(const uint16_t* __restrict__ h, const int32_t* __restrict
   const int steps = h_steps(K);
   const uint32_t lrow = (uint32_t)lane >> 4, lchunk = (uint32_t)(lane & 15);
   const uint32_t w_off = lrow * row_w + 16u * lchunk, s_off = (lrow * spr + 32u * lchunk / G) * 2u;
-  struct Step {
-    int pair, s;
-  };
-  struct Data {
-    u32x4 w[2], a[4];
-    uint32_t sc[2];
-  };
-  auto advance = [&](Step& st) {
-    if (++st.s < steps) return;
-    st.s = 0;
-    st.pair += kWaves;
-  };
-  auto load = [&](const Step& st, Data& d) __attribute__((always_inline)) {
-    const int p = st.pair < pairs ? st.pair : 0, k0 = st.s * kStepK;
-    const int e = __builtin_amdgcn_readlane(id, p);
-    const bool live = st.pair < pairs && e >= 0 && e < experts;
-    const size_t first = (size_t)(live ? e : 0) * N + n0;
-    const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
-                                                  live ? (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2 : 0u);
-    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
-                                                  live ? ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u : 0u);
-    const bool in = (uint32_t)k0 + 32u * lchunk < (uint32_t)K;
-    const uint32_t wo = offset_if(in, w_off), so = offset_if(in, s_off);
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      d.w[g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres, wo + 4u * g * row_w, 0, kStream));
-      d.sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, so + 8u * g * spr, 0, 0);
-    }
-    // A rows: upper and lower parts, twice; chunks past K were never written
-    const __amdgpu_buffer_rsrc_t hres = make_rsrc(
-        reinterpret_cast<const uint8_t*>(h) + (size_t)(p * steps + st.s) * kDirectStep, live ? kDirectStep : 0u);
-    const uint32_t a_off = offset_if(k0 + 32 * c < K, 32u * c + 16u * (li & 1));
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-      d.a[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, a_off + 512u * w, 0, 0));
-  };
   const Decoder decode;
-  f32x4 acc = f32x4{};                           // upper and lower parts' sums, columns 0-3 and 4-7
-  auto compute = [&](const Step& st, const Data& d) {
+  for (int p = wave; p < pairs; p += kDirectWaves) {
+    const int e = __builtin_amdgcn_readlane(id, p);
+    const bool live = e >= 0 && e < experts;
+    const size_t first = (size_t)(live ? e : 0) * N + n0;
+    f32x4 acc = f32x4{};                         // upper and lower parts' sums, columns 0-3 and 4-7
+    for (int k0 = 0; k0 < K; k0 += kStepK) {
+      const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
+                                                    live ? (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2 : 0u);
+      const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
+                                                    live ? ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+      const bool in = (uint32_t)k0 + 32u * lchunk < (uint32_t)K;
+      const uint32_t wo = offset_if(in, w_off), so = offset_if(in, s_off);
+      u32x4 wv[2], a[4];
+      uint32_t sc[2];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const f32x4 t = chunk_product(decode, spread_rows(d.w[g], lane), d.a);
-      const float f = half_bits_to_float(spread_rows(d.sc[g], lane));
+      for (int g = 0; g < 2; ++g) {
+        wv[g] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres, wo + 4u * g * row_w, 0, kStream));
+        sc[g] = __builtin_amdgcn_raw_buffer_load_b16(sres, so + 8u * g * spr, 0, 0);
+      }
+      // A rows: upper and lower parts, twice; chunks past K were never written
+      const __amdgpu_buffer_rsrc_t hres =
+          make_rsrc(reinterpret_cast<const uint8_t*>(h) + ((size_t)p * steps + k0 / kStepK) * kDirectStep, live ? kDirectStep : 0u);
+      const uint32_t a_off = offset_if(k0 + 32 * c < K, 32u * c + 16u * (li & 1));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) acc[2 * g + i] = __builtin_fmaf(f, t[i], acc[2 * g + i]);
+      for (int w = 0; w < 4; ++w)
+        a[w] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(hres, a_off + 512u * w, 0, 0));
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const f32x4 t = chunk_product(decode, spread_rows(wv[g], lane), a);
+        const float f = half_bits_to_float(spread_rows(sc[g], lane));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[2 * g + i] = __builtin_fmaf(f, t[i], acc[2 * g + i]);
+      }
     }
-    if (st.s + 1 < steps) return;
-    const int e = __builtin_amdgcn_readlane(id, st.pair);
-    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), st.pair));
+    const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, weight), p));
     const float r = chunk_sums(f32x4{__builtin_fmaf(acc[1], 1.0f / kLoScale, acc[0]),
                                      __builtin_fmaf(acc[3], 1.0f / kLoScale, acc[2]), 0.f, 0.f}) * (1.0f / kHScale);
     const int at = sum_index(lane);
-    if (at < 2 && (lane & 12) == 0) part[st.pair][4 * at + li] = e >= 0 && e < experts ? w * r : 0.0f;
-    acc = f32x4{};
-  };
-  Step cur = {wave, 0}, ahead = cur;
-  Data d[kDepth];
-#pragma unroll
-  for (int u = 0; u < kDepth; ++u) {
-    load(ahead, d[u]);
-    advance(ahead);
-  }
-  while (cur.pair < pairs) {
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
-      if (cur.pair < pairs) compute(cur, d[u]);
-      advance(cur);
-      load(ahead, d[u]);
-      advance(ahead);
-    }
+    if (at < 2 && (lane & 12) == 0) part[p][4 * at + li] = live ? w * r : 0.0f;
   }
   __syncthreads();
   if (!out) return;
@@ -722,8 +696,8 @@ hipError_t launch_moe_ffn(const uint16_t* x, const int32_t* ids, const float* we
                                        gate_up_scales, h, topk, experts, 2 * inter, hidden);
     if (e != hipSuccess) return e;
     return launch_kernel(g32 ? moe_down_direct_kernel<32> : moe_down_direct_kernel<128>, dim3((unsigned)((hidden + 7) / 8)),
-                         dim3(kThreads), 0, stream, h, ids, weights, down, down_scales, residual, y, pairs, topk, tokens,
-                         experts, hidden, inter);
+                         dim3(64 * kDirectWaves), 0, stream, h, ids, weights, down, down_scales, residual, y, pairs, topk,
+                         tokens, experts, hidden, inter);
   }
   Blocks* blocks = reinterpret_cast<Blocks*>(behind_counters(workspace));
   h += kBlocksBytes / sizeof(uint16_t);
