@@ -96,3 +96,12 @@ def test_rows_do_not_see_their_neighbours_in_blocks(w4):
     order = layer.rng.permutation(30)[:23]
     again = host(layer(dev(x[order]), dev(ids[order]), dev(w[order])))
     assert np.array_equal(again.view(np.uint16), y[order].view(np.uint16))
+
+
+# more than one step of h (512) and piece of x (2048), ragged ones; columns that end inside a band; few and many experts
+@pytest.mark.parametrize("tokens,topk,experts,hidden,inter,group,spread",
+                         [(24, 4, 30, 160, 544, 32, 30), (20, 4, 11, 2176, 1152, 128, 11), (33, 2, 40, 4128, 1600, 32, 40),
+                          (64, 8, 9, 32, 2080, 32, 9), (64, 2, 128, 1056, 512, 32, 100), (22, 3, 3, 2048, 1024, 128, 3)])
+def test_long_rows_in_blocks(w4, tokens, topk, experts, hidden, inter, group, spread):
+    layer = Layer(w4, experts, hidden, inter, group, 99400 + tokens + inter)
+    check(layer, tokens, topk, spread=spread, residual=tokens % 2 == 0)
