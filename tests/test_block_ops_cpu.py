@@ -216,3 +216,8 @@ def test_ffn_abi_refusals():
     assert ffn(res=P(A[8].value + 16)) == w4.ERR_OVERLAP                     # the residual over part of y
     for sizes in ((0, 2, 128, 64, 32), (65, 2, 128, 64, 32), (4, 2, 128, 64, 48), (4, 2, 100, 64, 32)):
         assert w4.lib.w4a16_moe_ffn_workspace_bytes(*sizes) == 0
+
+
+def test_the_experts_workspace_is_device_memory():
+    with pytest.raises(ValueError, match="HIP device"):
+        w4.moe_ffn_workspace(4, 2, 256, 128, 32, device="cpu")

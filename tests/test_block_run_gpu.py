@@ -295,3 +295,30 @@ def test_given_workspace_of_the_experts(w4, tokens):
     with pytest.raises(w4.W4A16Error, match="WORKSPACE"):
         layer(x, ids, w, workspace=buf[:words - 4])
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_workspace_made_for_the_experts(w4, tokens):
+    """moe_ffn_workspace's tensor serves calls on another stream, and within a capture that makes it."""
+    torch = torch_mod()
+    layer = Layer(w4, 7, 256, 128, 32, 99500 + tokens)
+    x = dev(synth.activations(layer.rng, tokens, 256))
+    ids = dev(layer.rng.integers(0, 7, (tokens, 3)).astype(np.int32))
+    w = dev(layer.rng.random((tokens, 3)).astype(np.float32))
+    want = layer(x, ids, w)
+    ws = w4.moe_ffn_workspace(tokens, 3, 256, 128, 32)
+    assert ws.numel() * 4 >= w4.lib.w4a16_moe_ffn_workspace_bytes(tokens, 3, 256, 128, 32) > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [layer(x, ids, w, workspace=ws, stream=side) for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    assert w4.moe_ffn_workspace(65, 3, 256, 128, 32) is None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, ids, w, workspace=w4.moe_ffn_workspace(tokens, 3, 256, 128, 32))
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

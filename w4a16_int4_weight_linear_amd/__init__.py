@@ -499,16 +499,22 @@ def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None, st
     are ordered behind this one)."""
     if call not in ("gemm_swiglu", "gemm_swiglu_backward", "gemm_t", "gemm_dscales", "linear", "linear_backward"):
         raise ValueError(f"ffn_workspace: no workspace for {call!r}")
+    return _made_workspace("ffn_workspace", lambda: getattr(lib, f"w4a16_{call}_workspace_bytes")(m, n, k, group), device,
+                           stream)
+
+
+def _made_workspace(what, size, device, stream):
+    """A workspace of size() bytes, asked for with its device current, as ffn_workspace describes it."""
     cuda = _torch_preload.cuda
     device = _torch_preload.device(device) if device is not None else stream.device if stream is not None \
         else _torch_preload.device("cuda")
     if device.type != "cuda":
-        raise ValueError(f"ffn_workspace: a workspace lives on a HIP device, not on {device}")
+        raise ValueError(f"{what}: a workspace lives on a HIP device, not on {device}")
     if device.index is None:
         device = _torch_preload.device("cuda", cuda.current_device())
 
     def make(handle):
-        nbytes = getattr(lib, f"w4a16_{call}_workspace_bytes")(m, n, k, group)
+        nbytes = size()
         if not nbytes:
             return None
         ws = _new_workspace(nbytes, device)
@@ -516,7 +522,7 @@ def ffn_workspace(call: str, m: int, n: int, k: int, group: int, device=None, st
             cuda.current_stream().synchronize()
         return ws
 
-    return _launch_on("ffn_workspace", device, stream, make)
+    return _launch_on(what, device, stream, make)
 
 
 def gemm_swiglu(x, packed, scales, group: int, gate_up=None, out=None, workspace=None, stream=None):
@@ -816,12 +822,18 @@ def _moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group):
     return lib.w4a16_moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group)
 
 
+def moe_ffn_workspace(tokens: int, topk: int, hidden: int, inter: int, group: int, device=None, stream=None):
+    """A workspace tensor for moe_ffn of these sizes, as ffn_workspace makes them; None for sizes that moe_ffn refuses."""
+    return _made_workspace("moe_ffn_workspace", lambda: _moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group), device,
+                           stream)
+
+
 def moe_ffn(x, ids, weights, gate_up, gate_up_scales, down, down_scales, group: int, residual=None, out=None,
             workspace=None, stream=None):
     """The routed experts' feed-forward for up to 64 tokens and 512 (token, slot) pairs: out [tokens, hidden] =
     residual + sum over a token's slots of weight * down(SiLU(g) u).  gate_up [experts, 2 inter, hidden/8] interleaves
     gate and up rows, down [experts, hidden, inter/8]; ids and weights [tokens, topk] as moe_topk gives them;
-    residual may be `out`."""
+    residual may be `out`.  workspace: moe_ffn_workspace's, or None for one of the binding's own."""
     what = "moe_ffn"
     try:
         (tokens, hidden), (_, topk) = x.shape, ids.shape
