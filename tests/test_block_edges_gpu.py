@@ -1,0 +1,46 @@
+"""The edges of the linear layer's, the router's and the few-token experts' calls, on the device."""
+
+import numpy as np
+import pytest
+
+from gpu_util import dev, host, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def w4():
+    torch_mod()
+    import w4a16_int4_weight_linear_amd as w4
+    return w4
+
+
+def test_the_most_tokens_of_a_router(w4):
+    """2^26 - 1 tokens with a wave each (17 slots): past 2^32 threads, so two rows of workgroups.  Choice and gradient of every token of
+    a repeating batch; a permutation of all experts each, so their sum says that every row was written."""
+    torch = torch_mod()
+    tokens, experts, few = (1 << 26) - 1, 17, 8191
+    rng = np.random.default_rng(87000)
+    some = torch.from_numpy(rng.standard_normal((few, experts)).astype(np.float16)).cuda()
+    logits = torch.empty((tokens, experts), dtype=torch.float16, device="cuda")
+    for a in range(0, tokens, few * 1024):
+        b = min(a + few * 1024, tokens)
+        logits[a:b] = some.repeat(1024, 1)[:b - a]
+    ids = torch.full((tokens, experts), -7, dtype=torch.int32, device="cuda")
+    weights = torch.full((tokens, experts), -7.0, device="cuda")
+    want_ids, want_w = w4.moe_topk(some, experts)
+    w4.moe_topk(logits, experts, ids=ids, weights=weights)
+    dw = torch.from_numpy(rng.standard_normal((few, experts)).astype(np.float32)).cuda()
+    want_d = w4.moe_topk_backward(dw, some, want_ids, want_w)
+    for a in range(0, tokens, few * 1024):
+        b = min(a + few * 1024, tokens)
+        assert torch.equal(ids[a:b], want_ids.repeat(1024, 1)[:b - a]), a
+        assert torch.equal(weights[a:b], want_w.repeat(1024, 1)[:b - a]), a
+    dws = torch.empty_like(weights)
+    for a in range(0, tokens, few * 1024):
+        b = min(a + few * 1024, tokens)
+        dws[a:b] = dw.repeat(1024, 1)[:b - a]
+    w4.moe_topk_backward(dws, logits, ids, weights, out=logits.fill_(7))
+    for a in range(0, tokens, few * 1024):
+        b = min(a + few * 1024, tokens)
+        assert torch.equal(logits[a:b], want_d.repeat(1024, 1)[:b - a]), a

@@ -7,6 +7,7 @@
 #include "../../include/w4a16.h"
 #include "checks.hpp"
 #include "kernels.hpp"
+#include "moe_topk_plan.hpp"
 
 namespace {
 
@@ -22,8 +23,8 @@ using w4a16::valid_group;
 
 int topk_checks(int32_t dtype, int64_t tokens, int32_t experts, int32_t topk) {
   if (dtype != W4A16_F32 && dtype != W4A16_F16) return W4A16_ERR_RANGE;
-  if (tokens < 0 || tokens > w4a16::kMoeTopkTokens || topk < 1 || topk > experts || topk > w4a16::kMoeTopkSlots ||
-      experts > w4a16::kMoeTopkExperts)
+  namespace plan = w4a16::topk_plan;
+  if (tokens < 0 || tokens > plan::kTokens || topk < 1 || topk > experts || topk > plan::kSlots || experts > plan::kExperts)
     return W4A16_ERR_SHAPE;
   return W4A16_OK;
 }

@@ -196,8 +196,6 @@ hipError_t launch_moe_combine(const uint16_t* y_pairs, const int32_t* pair_row, 
 
 // ---- router's choice and its gradient (moe_topk.hip) ----
 // logits [tokens, experts], fp16 (half) or fp32; ids and weights [tokens, topk].
-constexpr int kMoeTopkExperts = 1024, kMoeTopkSlots = 64;      // most experts, most slots
-constexpr int kMoeTopkTokens = (1 << 26) - 1;                  // most tokens: 64 threads each, below 2^32
 hipError_t launch_moe_topk(const void* logits, bool half, int32_t* ids, float* weights, int tokens, int experts,
                            int topk, bool renormalize, hipStream_t stream);
 hipError_t launch_moe_topk_backward(const float* dweights, const void* logits, bool half, const int32_t* ids,

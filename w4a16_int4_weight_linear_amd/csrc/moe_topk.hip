@@ -15,11 +15,12 @@
 #include "device.hpp"
 #include "kernels.hpp"
 #include "launch.hpp"
+#include "moe_topk_plan.hpp"
 
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 256;
+using topk_plan::kThreads;
 constexpr uint32_t kMaskedKey = 0x007FFFFFu;     // the key of -inf; 0 is no logit at all
 
 // Floats as integers in the same order: -0 as +0, every NaN above +inf.
@@ -65,6 +66,12 @@ __device__ inline float row_sum(float v) {
   }));
 }
 
+// The token of a thread (the grid may have several rows of workgroups).
+template <int LANES>
+__device__ inline int64_t token_of() {
+  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
+}
+
 // The expert of a lane's value v: runs of four, so that a lane reads 16 (or 8) bytes at a time.
 template <int LANES>
 __device__ inline int expert_of(int lane, int v) { return 4 * lane + 4 * LANES * (v >> 2) + (v & 3); }
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kThreads)
 moe_topk_kernel(const T* __restrict__ logits, int32_t* __restrict__ ids, float* __restrict__ weights, int tokens,
                 int experts, int topk, int renormalize) {
   const int lane = threadIdx.x & (LANES - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const int64_t t = token_of<LANES>();
   const bool live = t < tokens;                    // (all lanes run: the reductions cross them)
   float val[V];
   load_row<LANES, V, VEC>(logits + (live ? t : 0) * experts, lane, experts, val);
@@ -158,7 +165,7 @@ moe_topk_backward_kernel(const float* __restrict__ dweights, const T* __restrict
   // a token's gradient is put together in LDS: a wave's own LDS accesses keep their order
   __shared__ float rows[kThreads / LANES][LANES * V];
   const int lane = threadIdx.x & (LANES - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+  const int64_t t = token_of<LANES>();
   const bool live = t < tokens;
   float* row = rows[threadIdx.x / LANES];
   int id = -1;
@@ -220,36 +227,33 @@ moe_topk_backward_kernel(const float* __restrict__ dweights, const T* __restrict
   }
 }
 
-// Lanes and values per lane: a DPP row per token for up to 256 experts and 16 slots, else a wave; and a wave per token
-// where there are few tokens (a round's chain of instructions is shorter).  A wave against a row, 256 experts, 8
-// slots, fp32: 64 tokens 4.9 / 5.2 us, 1024 tokens 4.9 / 5.3, 2048 tokens 5.0 / 5.4, 4096 tokens 6.1 / 5.6, 16384 tokens
-// 14.5 / 9.7.
-constexpr int kWaveTokens = 2048;
+template <int LANES>
+dim3 grid_of(int tokens) {
+  const topk_plan::Grid g = topk_plan::grid_of(tokens, LANES);
+  return dim3(g.x, g.y);
+}
 struct Forward {
   template <int LANES, int V, bool VEC, typename T>
   static hipError_t launch(const T* logits, int32_t* ids, float* weights, int tokens, int experts, int topk,
                            int renormalize, hipStream_t stream) {
-    const int per = kThreads / LANES;
-    return launch_kernel(moe_topk_kernel<LANES, V, VEC, T>, dim3((unsigned)((tokens + per - 1) / per)), dim3(kThreads),
-                         0, stream, logits, ids, weights, tokens, experts, topk, renormalize);
+    return launch_kernel(moe_topk_kernel<LANES, V, VEC, T>, grid_of<LANES>(tokens), dim3(kThreads), 0, stream, logits, ids,
+                         weights, tokens, experts, topk, renormalize);
   }
 };
 struct Backward {
   template <int LANES, int V, bool VEC, typename T>
   static hipError_t launch(const float* dweights, const T* logits, const int32_t* ids, const float* weights, T* dlogits,
                            int tokens, int experts, int topk, int renormalize, hipStream_t stream) {
-    const int per = kThreads / LANES;
-    return launch_kernel(moe_topk_backward_kernel<LANES, V, VEC, T>, dim3((unsigned)((tokens + per - 1) / per)),
-                         dim3(kThreads), 0, stream, dweights, logits, ids, weights, dlogits, tokens, experts, topk,
-                         renormalize);
+    return launch_kernel(moe_topk_backward_kernel<LANES, V, VEC, T>, grid_of<LANES>(tokens), dim3(kThreads), 0, stream,
+                         dweights, logits, ids, weights, dlogits, tokens, experts, topk, renormalize);
   }
 };
 template <typename K, bool VEC, typename T, typename... A>
 hipError_t by_size(int tokens, int experts, int topk, A... a) {
-  if (topk <= 16 && tokens > kWaveTokens) {
+  if (topk_plan::lanes_of(tokens, experts, topk) == 16) {
     if (experts <= 64) return K::template launch<16, 4, VEC, T>(a...);
     if (experts <= 128) return K::template launch<16, 8, VEC, T>(a...);
-    if (experts <= 256) return K::template launch<16, 16, VEC, T>(a...);
+    return K::template launch<16, 16, VEC, T>(a...);
   }
   if (experts <= 256) return K::template launch<64, 4, VEC, T>(a...);
   if (experts <= 512) return K::template launch<64, 8, VEC, T>(a...);
