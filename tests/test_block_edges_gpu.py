@@ -44,3 +44,15 @@ def test_the_most_tokens_of_a_router(w4):
     for a in range(0, tokens, few * 1024):
         b = min(a + few * 1024, tokens)
         assert torch.equal(logits[a:b], want_d.repeat(1024, 1)[:b - a]), a
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("tokens", [500, 4096])
+def test_equal_logits_have_equal_weights(w4, tokens, renormalize):
+    """A token's slots are divided by one total, whichever lane holds them (six equal logits lie in lanes of different fours)."""
+    rng = np.random.default_rng(87100)
+    x = np.repeat(rng.standard_normal((tokens, 20)).astype(np.float32), 6, axis=1)
+    ids, w = (host(t) for t in w4.moe_topk(dev(x), 16, renormalize=renormalize))
+    picked = np.take_along_axis(x, ids, 1)
+    same = picked[:, 1:] == picked[:, :-1]
+    assert same.sum() >= 13 * tokens and np.array_equal(w[:, 1:][same], w[:, :-1][same])

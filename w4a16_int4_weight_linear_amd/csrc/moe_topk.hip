@@ -33,7 +33,8 @@ __device__ inline float value_of(uint32_t key) {
   return __builtin_bit_cast(float, key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// Reductions over the LANES lanes of a token (16: a DPP row, or the whole wave); every lane gets the result.
+// Reductions over the LANES lanes of a token (16: a DPP row, or the whole wave); every lane gets the same result, of sums
+// too: after the turn by 8 values have a period of 8 lanes, so the turn by 4 adds the same two everywhere.
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
@@ -42,8 +43,8 @@ template <int LANES, typename F>
 __device__ inline uint32_t row_reduce(uint32_t v, F f) {
   v = f(v, dpp<0xB1>(v));    // quad_perm [1,0,3,2]
   v = f(v, dpp<0x4E>(v));    // quad_perm [2,3,0,1]
-  v = f(v, dpp<0x124>(v));   // row_ror:4
   v = f(v, dpp<0x128>(v));   // row_ror:8
+  v = f(v, dpp<0x124>(v));   // row_ror:4
   if constexpr (LANES == 64) {
     const uint32_t a = __builtin_amdgcn_readlane(v, 0), b = __builtin_amdgcn_readlane(v, 16);
     const uint32_t c = __builtin_amdgcn_readlane(v, 32), d = __builtin_amdgcn_readlane(v, 48);
