@@ -73,6 +73,13 @@ __device__ inline int64_t token_of() {
   return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
 }
 
+// What any lane of the wave wrote to LDS before is there for every lane after (no instruction: LDS serves a wave in order).
+__device__ inline void lanes_meet() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // The expert of a lane's value v: runs of four, so that a lane reads 16 (or 8) bytes at a time.
 template <int LANES>
 __device__ inline int expert_of(int lane, int v) { return 4 * lane + 4 * LANES * (v >> 2) + (v & 3); }
@@ -163,7 +170,8 @@ __global__ void __launch_bounds__(kThreads)
 moe_topk_backward_kernel(const float* __restrict__ dweights, const T* __restrict__ logits,
                          const int32_t* __restrict__ ids, const float* __restrict__ weights, T* __restrict__ dlogits,
                          int tokens, int experts, int topk, int renormalize) {
-  // a token's gradient is put together in LDS: a wave's own LDS accesses keep their order
+  // a token's gradient is put together in LDS, by one wave: its own LDS accesses keep their order, and the fences keep
+  // the compiler from moving a lane's own past what the other lanes do
   __shared__ float rows[kThreads / LANES][LANES * V];
   const int lane = threadIdx.x & (LANES - 1);
   const int64_t t = token_of<LANES>();
@@ -208,9 +216,9 @@ moe_topk_backward_kernel(const float* __restrict__ dweights, const T* __restrict
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) row[expert_of<LANES>(lane, v)] = val[v];
-  __builtin_amdgcn_wave_barrier();
+  lanes_meet();
   if (id >= 0) atomicAdd(row + id, w * (renormalize ? dw - mean : dw));
-  __builtin_amdgcn_wave_barrier();
+  lanes_meet();
   if (!live) return;
   T* out = dlogits + t * experts;
   typedef T t4 __attribute__((ext_vector_type(4)));
