@@ -17,7 +17,9 @@ def test_sizes_at_the_edges(tmp_path):
     if gxx is None:
         pytest.fail("g++ is required for the sanitizer build")
     exe = tmp_path / "block_edges_driver"
-    srcs = [os.path.join(ROOT, p) for p in ("tests/sanitize/block_edges_driver.cpp",)]
+    srcs = [os.path.join(ROOT, p) for p in ("tests/sanitize/block_edges_driver.cpp",
+                                            "tests/sanitize/block_recording_launchers.cpp", f"{CSRC}/api_moe.cpp",
+                                            f"{CSRC}/api_linear.cpp")]
     cmd = [gxx, "-std=c++17", "-g", "-O1", "-Wall", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
            "-fno-omit-frame-pointer", "-D__HIP_PLATFORM_AMD__", f"-I{ROCM}/include", *srcs, "-o", str(exe)]
     r = subprocess.run(cmd, capture_output=True, text=True, timeout=300)

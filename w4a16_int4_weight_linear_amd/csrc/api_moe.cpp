@@ -103,11 +103,11 @@ w4a16_status w4a16_moe_ffn(const uint16_t* x, const int32_t* ids, const float* w
   if (!workspace || workspace_bytes < need) return W4A16_ERR_WORKSPACE;
   // (the residual's elements are read by the threads that then write y's: it may be y itself; an
   // expert's weights are below 2 GiB and experts below 2^31: the banks' sizes fit 64 bits)
-  const int64_t rows = 2 * tokens * hidden, pairs = 4 * tokens * topk;
+  const int64_t rows = 2 * tokens * hidden, pairs = 4 * tokens * topk, banks = experts;
   if (outputs_overlap({{y, rows}, {workspace, (int64_t)need}},
                       {{x, rows}, {residual, residual && residual != y ? rows : 0}, {ids, pairs}, {weights, pairs},
-                       {gate_up, experts * inter * hidden}, {gate_up_scales, experts * 4 * inter * (hidden / group)},
-                       {down, experts * hidden * (inter / 2)}, {down_scales, experts * 2 * hidden * (inter / group)}}))
+                       {gate_up, banks * inter * hidden}, {gate_up_scales, banks * 4 * inter * (hidden / group)},
+                       {down, banks * hidden * (inter / 2)}, {down_scales, banks * 2 * hidden * (inter / group)}}))
     return W4A16_ERR_OVERLAP;
   w4a16::DeviceInfo dev;
   if (w4a16::current_device_info(&dev) != hipSuccess) return W4A16_ERR_HIP;
