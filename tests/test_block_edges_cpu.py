@@ -28,3 +28,13 @@ def test_sizes_at_the_edges(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300, env=env)
     assert r.returncode == 0, (r.stdout + r.stderr)[-4000:]
     assert "block edges driver: ok" in r.stdout
+
+
+def test_every_call_is_exported():
+    """`from ... import *` brings each function of the binding that has no underscore."""
+    import inspect
+
+    import w4a16_int4_weight_linear_amd as w4
+    calls = {n for n, f in inspect.getmembers(w4, inspect.isfunction) if not n.startswith("_") and f.__module__ == w4.__name__}
+    assert calls - set(w4.__all__) == set()
+    assert all(hasattr(w4, n) or hasattr(w4.lib, n) for n in w4.__all__)

@@ -984,4 +984,4 @@ __all__ = ["lib", "LIB_PATH", "SIGNATURES", "W4A16Error", "quantize", "pack", "u
            "hbm_read_probe", "grouped_gemm_swiglu", "grouped_gemm", "interleave_rows", "gemv_swiglu", "moe_route",
            "grouped_gemm_gather", "moe_combine", "gemm_swiglu", "gemm_t",
            "gemm_swiglu_backward", "gemm_dscales", "ffn_workspace", "ffn_release_workspaces", "ACTIVATIONS", "linear",
-           "linear_backward", "moe_topk", "moe_topk_backward", "moe_ffn"] + list(SIGNATURES)
+           "linear_backward", "moe_topk", "moe_topk_backward", "moe_ffn", "moe_ffn_workspace"] + list(SIGNATURES)
