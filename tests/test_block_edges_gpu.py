@@ -56,3 +56,44 @@ def test_equal_logits_have_equal_weights(w4, tokens, renormalize):
     picked = np.take_along_axis(x, ids, 1)
     same = picked[:, 1:] == picked[:, :-1]
     assert same.sum() >= 13 * tokens and np.array_equal(w[:, 1:][same], w[:, :-1][same])
+
+
+def graph_nodes(w4, graph):
+    """How many nodes a captured graph has."""
+    import ctypes
+    get, count = w4.lib.hipGraphGetNodes, ctypes.c_size_t(0)       # (of the runtime that the library is linked with)
+    get.restype, get.argtypes = ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]
+    assert get(graph.raw_cuda_graph(), None, ctypes.byref(count)) == 0
+    return count.value
+
+
+@pytest.mark.parametrize("call,kernels", [("experts of one token", 2), ("experts of 40 tokens", 3), ("split tiles", 2)])
+def test_a_captured_call_is_its_kernels(w4, call, kernels):
+    """No fill of counters that a call does not use in front of it; replays give the eager result."""
+    torch = torch_mod()
+    from test_moe_ffn_gpu import Layer
+    rng = np.random.default_rng(87200)
+    if call == "split tiles":
+        p = torch.randint(-2 ** 31, 2 ** 31 - 1, (520, 256), dtype=torch.int32, device="cuda")
+        s, x = torch.rand(520, 16, device="cuda").half() * 0.01, torch.randn(300, 2048, device="cuda").half()
+        assert w4.ffn_workspace("linear", 300, 520, 2048, 128) is not None
+        step = lambda: w4.linear(x, p, s, 128, activation="silu")  # noqa: E731
+    else:
+        tokens = 1 if "one" in call else 40
+        layer = Layer(w4, 9, 256, 128, 32, 87201)
+        x, ids = dev(rng.standard_normal((tokens, 256)).astype(np.float16)), dev(rng.integers(0, 9, (tokens, 3)).astype(np.int32))
+        w = dev(rng.random((tokens, 3)).astype(np.float32))
+        step = lambda: layer(x, ids, w)  # noqa: E731
+    want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        out = step()
+    assert graph_nodes(w4, graph) == kernels
+    graph.instantiate()
+    for _ in range(3):
+        out.fill_(float("nan"))
+        torch.full((1 << 20,), -1, dtype=torch.int32, device="cuda")
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)

@@ -332,7 +332,7 @@ def gemv_swiglu(x, packed, scales, group: int, out=None, stream=None):
 # grown to the largest size asked for (a call is up to three kernels, so the calls of two
 # threads on one stream must not share one).  A workspace begins with counters that are 0
 # between calls.  Under graph capture each call takes one from the graph's own pool and
-# clears its counters in the graph, so captured graphs share none.  A smallest call is bound
+# clears its counters in the graph if it uses them, so captured graphs share none.  A smallest call is bound
 # by what the host does before it launches, so the checks here walk the arguments once; memory
 # shared between an output and another operand is refused by the library (ERR_OVERLAP).
 # As everywhere in this module, autograd does not see the calls: results carry no history, whatever
@@ -460,15 +460,17 @@ def _ffn_workspace(entry, m, n, k, group, device, handle, given):
         # it may be another stream's memory: not to be handed out again before this call is done
         given.record_stream(_torch_preload.cuda.current_stream())
         return given.data_ptr(), given.numel() * 4, given
-    return _kept_workspace(_ffn_workspace_bytes(entry, m, n, k, group, device.index), device, handle)
+    return _kept_workspace(_ffn_workspace_bytes(entry, m, n, k, group, device.index), device, handle,
+                           entry != "w4a16_linear")
 
 
-def _kept_workspace(nbytes, device, handle):
-    """A workspace of at least nbytes for a call on stream `handle` of the current device."""
+def _kept_workspace(nbytes, device, handle, counts):
+    """A workspace of at least nbytes for a call on stream `handle` of the current device.  counts: the call uses the
+    counters, so a captured one clears them (a kernel more in the graph; what is kept serves every call)."""
     if nbytes == 0:
         return 0, 0, None
     if _capturing():
-        ws = _new_workspace(nbytes, device)
+        ws = _new_workspace(nbytes, device, counts)
         return ws.data_ptr(), nbytes, ws     # freed to the graph's pool, whose later work is ordered behind this call
     key = (device.index, handle)
     kept = _FFN_WORKSPACES.of.get(key)
@@ -485,9 +487,10 @@ def _kept_workspace(nbytes, device, handle):
 _COUNTER_WORDS = 4096        # the counters a workspace begins with
 
 
-def _new_workspace(nbytes, device):
+def _new_workspace(nbytes, device, counts=True):
     ws = _torch_preload.empty((nbytes + 3) // 4, dtype=_torch_preload.int32, device=device)
-    ws[:_COUNTER_WORDS].zero_()
+    if counts:
+        ws[:_COUNTER_WORDS].zero_()
     return ws
 
 
@@ -871,7 +874,8 @@ def moe_ffn(x, ids, weights, gate_up, gate_up_scales, down, down_scales, group: 
             workspace.record_stream(_torch_preload.cuda.current_stream())
             ws, nbytes, held = workspace.data_ptr(), workspace.numel() * 4, workspace
         else:
-            ws, nbytes, held = _kept_workspace(_moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group), device, handle)
+            ws, nbytes, held = _kept_workspace(_moe_ffn_workspace_bytes(tokens, topk, hidden, inter, group), device, handle,
+                                               False)
         _check(lib.w4a16_moe_ffn(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), gate_up.data_ptr(),
                                  gate_up_scales.data_ptr(), down.data_ptr(), down_scales.data_ptr(),
                                  0 if residual is None else residual.data_ptr(), out.data_ptr(), tokens, topk, experts,
