@@ -335,6 +335,7 @@ size_t w4a16_linear_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t gro
  *     dbias[n] = sum over rows of dy act'(pre)   fp32 [n], of the unrounded values, in a fixed order
  *     dx = dpre . deq(W)   fp16 [m, k], the product of that fp16 output, as w4a16_gemm_t
  *
+ * (an infinite pre, a z past fp16's range, has slope 0 or 1: the activation's at that end).
  * dbias may be NULL (not computed).  With W4A16_ACT_NONE dpre is dy: pre and dpre must be NULL, and dx is
  * the product of dy.  All 16-byte aligned.  The gradient of the scales is w4a16_gemm_dscales of dpre
  * (or dy).  Outputs that share memory with another operand are W4A16_ERR_OVERLAP; m, n or k of 0 is as

@@ -97,3 +97,30 @@ def test_a_captured_call_is_its_kernels(w4, call, kernels):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("m,n,k,group", [(1, 40, 64, 32), (21, 131, 64, 32), (30, 3001, 2560, 32), (70, 264, 128, 128), (70, 33, 64, 32)])
+def test_gradient_of_pre_activations_past_fp16(w4, m, n, k, group, act):
+    """A pre-activation past 65504 is kept as infinity: y is finite (0 at that end), or infinite as fp16 has it, and the
+    gradient is dy times 0 or 1, not NaN; in the product, in front of it, on odd rows and tiles."""
+    torch = torch_mod()
+    from test_linear_gpu import weights
+    rng = np.random.default_rng(87300 + m + n)
+    q, s = weights(rng, n, k, group)
+    # through the call itself: codes of 7, scales of 16 and x of +-1000 give z = +-7 16 1000 k
+    x = np.full((m, k), 1000, np.float16)
+    x[::2] = -1000
+    pre = torch.empty((m, n), dtype=torch.float16, device="cuda")
+    big = dev(w4.pack(np.full((n, k), 7, np.int8))), dev(np.full((n, k // group), 16, np.float16))
+    y = host(w4.linear(dev(x), *big, group, activation=act, pre=pre))
+    z = host(pre)
+    assert np.all(np.isneginf(z[::2])) and np.all(np.isposinf(z[1::2])) and np.all(np.abs(y[::2]) == 0) and np.all(np.isposinf(y[1::2]))
+    z[:, ::3] = rng.standard_normal(z[:, ::3].shape)
+    z[m - 1, n - 1] = np.nan
+    dy = rng.standard_normal((m, n)).astype(np.float16)
+    dx, dpre, dbias = (host(t) for t in w4.linear_backward(dev(dy), dev(w4.pack(q)), dev(s), group, pre=dev(z), activation=act, dbias=True))
+    assert np.array_equal(dpre[np.isneginf(z)], 0 * dy[np.isneginf(z)]) and np.array_equal(dpre[np.isposinf(z)], dy[np.isposinf(z)])
+    rest = ~np.isnan(z)
+    assert np.all(np.isfinite(dpre[rest])) and np.isnan(dpre[m - 1, n - 1])
+    assert np.all(np.isfinite(dx[:m - 1])) and np.all(np.isfinite(dbias[:n - 1])) and np.isnan(dbias[n - 1])

@@ -60,9 +60,15 @@ __device__ inline float activation_of(float z) {
   }
 }
 
-// act'(z); relu' is 0 at 0
+// act'(z); relu' is 0 at 0.  z is what the forward pass kept in fp16, where a pre-activation past 65504 is infinite
+// (the forward pass took it as it was): its slope is that of fp16's largest value, 0 or 1 in every activation, as
+// infinity times the 0 that the formulas have there would be NaN.  (NaN stays.)
+__device__ inline float finite_of(float z) {
+  return __builtin_isinf(z) ? __builtin_copysignf(65504.0f, z) : z;
+}
 template <int ACT>
 __device__ inline float slope_of(float z) {
+  if constexpr (ACT == W4A16_ACT_SILU || ACT == W4A16_ACT_GELU || ACT == W4A16_ACT_GELU_TANH) z = finite_of(z);
   if constexpr (ACT == W4A16_ACT_RELU) {
     return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
   } else if constexpr (ACT == W4A16_ACT_SILU) {
