@@ -314,8 +314,7 @@ size_t w4a16_gemm_dscales_workspace_bytes(int64_t m, int64_t n, int64_t k, int32
  * is computed from the unrounded z.  residual may be y itself (y += act(z)); any other sharing of
  * memory between an output and another operand is W4A16_ERR_OVERLAP.  Kernels as w4a16_gemm_swiglu's
  * (m = 1 and 2-4: the decode kernels; up to 16 rows, or 32 and up to 32 MB of weights, the
- * weight-streaming kernel; beyond, tiles), with their weights: exact on the decode kernels, and at group 128
- * on the others where the scales' alignment allows (K / 128 even, or the tiles), else fp16(s q).
+ * weight-streaming kernel; beyond, tiles).  Weights are exact, but on the tiles at group 32, where they are fp16(s q).
  * Workspace (w4a16_linear_workspace_bytes) and errors as w4a16_gemm_swiglu, also W4A16_ERR_RANGE for an
  * unknown activation; k == 0 is refused (W4A16_ERR_SHAPE): there is no product to fold into.
  */

@@ -124,3 +124,25 @@ def test_gradient_of_pre_activations_past_fp16(w4, m, n, k, group, act):
     rest = ~np.isnan(z)
     assert np.all(np.isfinite(dpre[rest])) and np.isnan(dpre[m - 1, n - 1])
     assert np.all(np.isfinite(dx[:m - 1])) and np.all(np.isfinite(dbias[:n - 1])) and np.isnan(dbias[n - 1])
+
+
+# decode kernels, weight-streaming kernel (scales that come in one load and that do not), tiles where weights are exact
+@pytest.mark.parametrize("m,k,group", [(1, 416, 32), (1, 640, 128), (3, 416, 32), (4, 512, 128), (5, 416, 32), (9, 512, 32), (16, 640, 128),
+                                       (16, 512, 128), (17, 416, 32), (32, 512, 32), (32, 640, 128), (40, 512, 128), (70, 640, 128)])
+def test_linear_has_exact_weights(w4, m, k, group):
+    """Each output is the difference of two weights that nearly cancel, 2048 (s1 q1 - s2 q2): exact in fp32, and far off if a
+    weight was rounded to fp16."""
+    torch = torch_mod()
+    rng = np.random.default_rng(87400 + m + k)
+    n = 131
+    q = rng.integers(5, 8, (n, 1)).astype(np.int8) * np.ones((1, k), np.int8) * rng.choice([-1, 1], (n, 1)).astype(np.int8)
+    # scales in 1..2 (ulp 2^-10), neighbours up to three ulps apart
+    s = (1 + (rng.integers(0, 1000, (n, 1)) + rng.integers(0, 4, (n, k // group))) / 1024).astype(np.float16)
+    x = np.zeros((m, k), np.float16)
+    for r in range(m):
+        a, b = rng.choice(k // group, 2, replace=False) * group + rng.integers(0, group, 2)
+        x[r, a], x[r, b] = 2048, -2048
+    pre = torch.empty((m, n), dtype=torch.float16, device="cuda")
+    y = host(w4.linear(dev(x), dev(w4.pack(q)), dev(s), group, pre=pre))
+    want = x.astype(np.float64) @ (q * np.repeat(s.astype(np.float64), group, axis=1)).T
+    assert np.array_equal(y, want.astype(np.float16)) and np.array_equal(host(pre), want.astype(np.float16))

@@ -87,6 +87,8 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
   // per group to the MFMA results; otherwise each word is dequantised with its
   // scale before the MFMA.
   constexpr bool kEnc = G == 128 && ALIGNED;
+  // Otherwise what is kept for a backward pass, and the linear layer, have exact weights by a second MFMA.
+  constexpr bool kExact = KEEP || sizeof...(Epi) > 0;
 
   // rows_base / rows_extra count whole rows, or whole (gate, up) row pairs
   constexpr int kUnit = SWIGLU ? 2 : 1;
@@ -312,11 +314,11 @@ gemm_skinny_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ 
           for (int w = 0; w < 4; ++w) {
             const f16x8 xf = __builtin_bit_cast(f16x8, *reinterpret_cast<const u32x4*>(xb + 256 * h + 16 * w));
             const uint32_t q = w == 0 ? wv.x : (w == 1 ? wv.y : (w == 2 ? wv.z : wv.w));
-            if constexpr (KEEP) {
-              // what is kept for a backward pass has exact weights: the scale's upper seven bits
-              // and its rest, each times a code, fit fp16 (0.13% instead of 40% of the kept values
-              // not the nearest; 17 rows 2048 -> 512 5.0 against 4.85 us, 16 rows 5120 -> 17408 at
-              // g32 48.7 against 40.9)
+            if constexpr (kExact) {
+              // the scale's upper seven bits and its rest, each times a code, fit fp16 (0.13% instead
+              // of 40% of the kept values not the nearest; 17 rows 2048 -> 512 5.0 against 4.85 us, 16
+              // rows 5120 -> 17408 pairs at g32 48.7 against 40.9; the linear layer at g32: 8 rows 1024 -> 1024 5.2
+              // against 5.0 us, 27 rows 2080 -> 2003 8.2 / 7.9, 16 rows 5120 -> 17408 21.9 / 19.1)
               const f16x2 hi = __builtin_bit_cast(f16x2, __builtin_bit_cast(uint32_t, sv[h]) & 0xFFF0FFF0u);
               part = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant_word(q, hi), xf, part, 0, 0, 0);
               part = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant_word(q, sv[h] - hi), xf, part, 0, 0, 0);
