@@ -640,7 +640,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               if (mb + 2 * j + h < M && nw + li < N)
-                y[at + (size_t)(2 * j) * N] = float_to_half_bits(v[j] + half_bits_to_float(res[j / 4][j % 4]));
+                le.y[at + (size_t)(2 * j) * N] = float_to_half_bits(v[j] + half_bits_to_float(res[j / 4][j % 4]));
               res[j / 4][j % 4] = next[j / 4][j % 4];
             }
             continue;
@@ -666,7 +666,7 @@ gemm_kernel(const uint16_t* __restrict__ x, const uint32_t* __restrict__ packed,
             activate(le.act, v);
 #pragma unroll
             for (int u = 0; u < 8; ++u) o[u] = (_Float16)(v[u] + (float)__builtin_bit_cast(f16x8, res[0])[u]);
-            if (in) *reinterpret_cast<f16x8*>(y + at) = o;
+            if (in) *reinterpret_cast<f16x8*>(le.y + at) = o;
 #pragma unroll
             for (int i = 0; i + 1 < 2 * kMB; ++i) res[i] = res[i + 1];
           }
@@ -932,7 +932,7 @@ swiglu_join_kernel(const float* __restrict__ partials, uint16_t* __restrict__ y,
 // The same for the linear layer.
 template <int MB>
 __global__ void __launch_bounds__(256)
-linear_join_kernel(const float* __restrict__ partials, uint16_t* y, int M, int N, SplitPlan plan, LinearEpilogue ep) {
+linear_join_kernel(const float* __restrict__ partials, int M, int N, SplitPlan plan, LinearEpilogue ep) {
   constexpr int BM = 32 * MB, kQuads = tile_quads(MB);
   constexpr size_t kPartialBytes = partial_bytes(MB);
   const int tile = blockIdx.x / (kQuads / 256), c = (blockIdx.x % (kQuads / 256)) * 256 + threadIdx.x;
@@ -949,7 +949,7 @@ linear_join_kernel(const float* __restrict__ partials, uint16_t* y, int M, int N
     v += *reinterpret_cast<const f32x4*>(base + (size_t)cs.slot(l) * kPartialBytes);
 #pragma unroll
   for (int r = 0; r < 4; ++r)
-    if (m0 + r < M) store_result(y, (size_t)(m0 + r) * N + n, n, v[r], ep);
+    if (m0 + r < M) store_result(nullptr, (size_t)(m0 + r) * N + n, n, v[r], ep);
 }
 
 // ---- scratch of the allocation-free entry point (w4a16_gemm_noalloc) ----
@@ -1031,7 +1031,7 @@ hipError_t launch_epi(const uint16_t* x, const uint32_t* packed, const uint16_t*
   if (EPI == kEpiProduct || e != hipSuccess || p.sk_tiles == 0) return e;
   const dim3 grid((unsigned)p.sk_tiles * (tile_quads(MB) / 256));
   if constexpr (EPI == kEpiLinear)
-    return launch_kernel(linear_join_kernel<MB>, grid, dim3(256), 0, stream, partials, y, m, n, split_of(p), epi...);
+    return launch_kernel(linear_join_kernel<MB>, grid, dim3(256), 0, stream, partials, m, n, split_of(p), epi...);
   else
     return launch_kernel(swiglu_join_kernel<MB>, grid, dim3(256), 0, stream, partials, y, z, m, n, split_of(p));
 }
@@ -1065,7 +1065,7 @@ hipError_t launch_gemm_linear(const uint16_t* x, const uint32_t* packed, const u
                               int n, int k, int group, const LinearEpilogue& ep, void* workspace, const DeviceInfo& dev,
                               hipStream_t stream) {
   auto launch = swiglu_blocks(m) == 2 ? launch_epi<kEpiLinear, 2, LinearEpilogue> : launch_epi<kEpiLinear, kMB, LinearEpilogue>;
-  return launch(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream, ep);
+  return launch(x, packed, scales, y, nullptr, m, n, k, group, workspace, dev, stream, ep.into(y));
 }
 
 }  // namespace w4a16

@@ -439,7 +439,7 @@ hipError_t launch_swiglu_skinny_keep(const uint16_t* x, const uint32_t* packed, 
 hipError_t launch_linear_skinny(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int m,
                                 int n, int k, int group, const LinearEpilogue& ep, const DeviceInfo& dev,
                                 hipStream_t stream) {
-  return launch_s<false, false>(x, packed, scales, y, nullptr, m, n, k, group, dev, stream, ep);
+  return launch_s<false, false>(x, packed, scales, y, nullptr, m, n, k, group, dev, stream, ep.into(y));
 }
 
 }  // namespace w4a16

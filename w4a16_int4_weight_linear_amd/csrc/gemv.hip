@@ -615,7 +615,7 @@ hipError_t launch_gemv(const uint16_t* x, const uint32_t* packed, const uint16_t
 hipError_t launch_gemv_linear(const uint16_t* x, const uint32_t* packed, const uint16_t* scales, uint16_t* y, int n,
                               int k, int group, const LinearEpilogue& ep, const GemvPlan& plan, const DeviceInfo& dev,
                               hipStream_t stream) {
-  return launch_gemv_m<1, false>(x, packed, scales, y, n, k, group, plan, dev, stream, ep);
+  return launch_gemv_m<1, false>(x, packed, scales, y, n, k, group, plan, dev, stream, ep.into(y));
 }
 
 }  // namespace w4a16

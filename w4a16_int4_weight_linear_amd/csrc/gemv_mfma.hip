@@ -464,9 +464,9 @@ hipError_t launch_gemv_mfma_linear(const uint16_t* x, const uint32_t* packed, co
                                    int m, int n, int k, int group, const LinearEpilogue& ep, int blocks, size_t lds,
                                    const DeviceInfo& dev, hipStream_t stream) {
   switch (m) {
-    case 2: return launch_g<2, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
-    case 3: return launch_g<3, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
-    case 4: return launch_g<4, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep);
+    case 2: return launch_g<2, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep.into(y));
+    case 3: return launch_g<3, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep.into(y));
+    case 4: return launch_g<4, false>(x, packed, scales, y, n, k, group, blocks, lds, dev, stream, ep.into(y));
     default: return hipErrorInvalidValue;
   }
 }

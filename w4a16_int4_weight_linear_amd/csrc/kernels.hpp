@@ -87,8 +87,13 @@ struct LinearEpilogue {
   const uint16_t* residual;
   uint16_t* pre;
   int act;                 // W4A16_ACT_*
+  // The output, through which these instances write it: the kernels' own y argument is __restrict__, and the
+  // residual may be y.  Set by the launchers.
+  uint16_t* y = nullptr;
+  LinearEpilogue into(uint16_t* out) const { return {bias, residual, pre, act, out}; }
 #ifdef __HIPCC__
   __device__ void skip_rows(int rows, int n) {
+    y += (size_t)rows * n;
     if (residual) residual += (size_t)rows * n;
     if (pre) pre += (size_t)rows * n;
   }

@@ -136,15 +136,15 @@ __device__ inline void store_eight(uint16_t* p, int left, const f16x8& o) {
   }
 }
 
-// One output: element `at` of y (and of residual and pre), column n, from the product's sum v.
+// One output: element `at` of y (ep.y; and of residual and pre), column n, from the product's sum v.
 __device__ inline void store_result(uint16_t* y, size_t at, int, float v) { y[at] = float_to_half_bits(v); }
-__device__ inline void store_result(uint16_t* y, size_t at, int n, float v, const LinearEpilogue& ep) {
+__device__ inline void store_result(uint16_t*, size_t at, int n, float v, const LinearEpilogue& ep) {
   const float z = ep.bias ? v + half_bits_to_float(ep.bias[n]) : v;
   if (ep.pre) ep.pre[at] = float_to_half_bits(z);
   float o[1] = {z};
   activate(ep.act, o);
   if (ep.residual) o[0] += half_bits_to_float(ep.residual[at]);
-  y[at] = float_to_half_bits(o[0]);
+  ep.y[at] = float_to_half_bits(o[0]);
 }
 
 }  // namespace w4a16
