@@ -146,3 +146,35 @@ def test_linear_has_exact_weights(w4, m, k, group):
     y = host(w4.linear(dev(x), dev(w4.pack(q)), dev(s), group, pre=pre))
     want = x.astype(np.float64) @ (q * np.repeat(s.astype(np.float64), group, axis=1)).T
     assert np.array_equal(y, want.astype(np.float16)) and np.array_equal(host(pre), want.astype(np.float16))
+
+
+# More tiles (128 x 256; up to 64 rows: 64 x 256) than workgroups, so that one takes a second whole tile while its first one's
+# outputs are on their way: rows that are whole 16-byte pieces and odd ones; leftover tiles whole (short k) and split
+@pytest.mark.parametrize("m,n,k,group,split", [(2177, 4104, 256, 32, False), (2177, 4099, 256, 128, False), (2177, 4104, 2560, 128, True),
+                                               (2177, 4099, 2560, 32, True), (2177, 4104, 2208, 32, True), (50, 66000, 256, 32, False),
+                                               (61, 66001, 256, 128, False), (4400, 8197, 96, 32, False)])
+@pytest.mark.parametrize("act,residual,keep", [("relu", "in place", True), ("none", "apart", False), ("silu", "in place", True)])
+def test_linear_of_many_tiles(w4, m, n, k, group, split, act, residual, keep):
+    """Integers, so z is exact (relu, none: y too) and any element that went astray shows."""
+    torch = torch_mod()
+    tiles = -(-m // (64 if m <= 64 else 128)) * -(-n // 256)
+    assert tiles > torch.cuda.get_device_properties(0).multi_processor_count
+    assert (w4.lib.w4a16_linear_workspace_bytes(m, n, k, group) > 0) == split
+    gen = torch.Generator(device="cuda").manual_seed(87500 + m + n + k)
+    ints = lambda lo, hi, *shape: torch.randint(lo, hi + 1, shape, generator=gen, device="cuda")  # noqa: E731
+    codes = ints(-8, 7, n, k // 8, 8)
+    packed = ((codes + 8) << torch.arange(0, 32, 4, device="cuda")).sum(dim=2).to(torch.int32)
+    scales = torch.ones((n, k // group), dtype=torch.float16, device="cuda")
+    scales[:, ::2] = 0.5
+    x, bias, res = ints(-2, 2, m, k).half(), ints(-8, 8, n).half(), ints(-64, 64, m, n).half()
+    w = codes.view(n, k).float() * scales.float().repeat_interleave(group, dim=1)
+    z = x.float() @ w.t() + bias.float()
+    want = {"relu": z.clamp(min=0), "none": z, "silu": z.double() * torch.sigmoid(z.double())}[act] + res.double()
+    pre = torch.full((m, n), float("nan"), dtype=torch.float16, device="cuda") if keep else None
+    y = w4.linear(x, packed, scales, group, bias=bias, activation=act, residual=res, pre=pre, out=res if residual == "in place" else None)
+    if act == "silu":         # y's one rounding, and the exponential's and reciprocal's (some fp32 units in the last place)
+        assert bool(((y.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -20 * (z.abs() + 1)).all())
+    else:
+        assert torch.equal(y, want.half())
+    if keep:
+        assert torch.equal(pre, z.half())
