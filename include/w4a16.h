@@ -465,8 +465,8 @@ w4a16_status w4a16_moe_topk_backward(const float* dweights, const void* logits, 
  * rows as for w4a16_grouped_gemm_swiglu, down [experts, hidden, inter/8] and its scales as for
  * w4a16_grouped_gemm.  Weights are exact; up to 64 pairs (tokens * topk) each reads its expert's for
  * itself, beyond that every four pairs of an expert share one read.  Sums are fp32; SiLU(g) u is kept to
- * 22 bits between the kernels (up to 2^24 in size); slots are added in order, with the residual, and y is
- * rounded once.  A not finite x leaves its own token's outputs alone not finite.
+ * within 2^-23 of its size between the kernels, or 2^-28 where that is more (below 2^-5), up to 2^24 in size; slots
+ * are added in order, with the residual, and y is rounded once.  A not finite x leaves its own token's outputs alone not finite.
  * 1 <= tokens <= 64 and tokens * topk <= 512, hidden and inter multiples of group and at least one group, hidden
  * <= 2^24, one expert's weights below 2 GiB (else W4A16_ERR_SHAPE; banks may be larger than that).  For more tokens:
  * w4a16_moe_route, w4a16_grouped_gemm_swiglu, w4a16_grouped_gemm, w4a16_moe_combine.  Workspace

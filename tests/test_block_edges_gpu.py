@@ -178,3 +178,37 @@ def test_linear_of_many_tiles(w4, m, n, k, group, split, act, residual, keep):
         assert torch.equal(y, want.half())
     if keep:
         assert torch.equal(pre, z.half())
+
+
+@pytest.mark.parametrize("tokens,topk", [(2, 3), (7, 9), (40, 4)])
+@pytest.mark.parametrize("size", [2.0 ** -3, 2.0 ** -8, 2.0 ** -13, 2.0 ** -18])
+def test_small_products_between_the_experts_kernels(w4, tokens, topk, size):
+    """h = SiLU(g) u about `size` and down scales about 1: y is as far off as an h within 2^-23 of its size or 2^-28 makes it.
+    Bar: gate/up weights are sums of one term each and h's own arithmetic is fp32 (g u sigmoid: 2^-20 |h|, as the
+    exponential and reciprocal are within some units in the last place); then |w2| times that, fp32 sums, one rounding."""
+    torch = torch_mod()
+    from test_moe_ffn_gpu import Layer
+    experts, hidden, inter, group = 5, 64, 96, 32
+    layer = Layer(w4, experts, hidden, inter, group, 87600 + tokens)
+    rng = layer.rng
+    # g near 1 (gate rows: code 4, scale 1/4, at x[0] = 1), u near size (up rows: at x[1] = size)
+    gu, gs = np.zeros((experts, 2 * inter, hidden), np.int8), np.full((experts, 2 * inter, hidden // group), 0.25, np.float16)
+    gu[:, 0::2, 0], gu[:, 1::2, 1] = 4, rng.integers(2, 8, (experts, inter))
+    ds = (0.5 + rng.random((experts, hidden, inter // group))).astype(np.float16)
+    x = np.zeros((tokens, hidden), np.float16)
+    x[:, 0], x[:, 1] = 0.5 + rng.random(tokens), size * (0.5 + rng.random(tokens))
+    ids = rng.integers(0, experts, (tokens, topk)).astype(np.int32)
+    w = rng.random((tokens, topk)).astype(np.float32)
+    pack = lambda b: dev(np.stack([w4.pack(c) for c in b]))  # noqa: E731
+    y = host(w4.moe_ffn(dev(x), dev(ids), dev(w), pack(gu), dev(gs), pack(layer.dn[0]), dev(ds), group)).astype(np.float64)
+    want, bar = np.zeros((tokens, hidden)), np.zeros((tokens, hidden))
+    for t in range(tokens):
+        for e, ws in zip(ids[t], w[t].astype(np.float64)):
+            w2 = layer.dn[0][e] * np.repeat(ds[e].astype(np.float64), group, axis=1)
+            g = float(x[t, 0])
+            u = gu[e, 1::2, 1] * 0.25 * float(x[t, 1])
+            h = g / (1 + np.exp(-g)) * u
+            want[t] += ws * (w2 @ h)
+            bar[t] += ws * (np.abs(w2) @ (2.0 ** -20 * np.abs(h) + np.maximum(2.0 ** -23 * np.abs(h), 2.0 ** -28)
+                                          + (inter + topk + 8) * 2.0 ** -24 * np.abs(h)))
+    assert np.all(np.abs(y - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + bar)

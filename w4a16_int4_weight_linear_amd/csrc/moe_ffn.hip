@@ -33,8 +33,9 @@
 // tokens 51 + 31.5 + 5 us: 391 MB of used experts' weights at 4.7 TB/s over both products, against 4.9 of a large
 // copy.  What is left is the fixed part (launch, sorting the pairs, the last work items) and the third kernel.
 //
-// h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11 (22 bits, |h| up to 2^24):
-// rounded once to fp16 it would add as much error again as the rounding of y.
+// h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11: off by at most 2^-23 |h|, or by 2^-28 where that
+// is more (|h| below 2^-5: lo is subnormal there), for |h| up to 2^24.  Rounded once to fp16 it would add as much error
+// again as the rounding of y; 2^-28 is an eighth of what fp16 is off by in its smallest numbers.
 #include <type_traits>
 
 #include "device.hpp"
@@ -286,7 +287,7 @@ moe_gate_up_direct_kernel(const uint16_t* __restrict__ x, const int32_t* __restr
   const Decoder decode;
   float acc = 0.0f;
   for (int k0 = 0, buf = 0; k0 < K; k0 += kXK, buf ^= 1) {
-    // every thread stages 8 bytes of the piece's 4 KB (and permutes them with its neighbour's)
+    // the first four waves stage the piece's 4 KB, 16 bytes a thread
     const __amdgpu_buffer_rsrc_t xres = make_rsrc(xp + k0, (uint32_t)(K - k0) * 2u);
     u32x4 xv = u32x4{};
     if (wave < 4) xv = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xres, 16u * threadIdx.x, 0, 0));
