@@ -454,9 +454,7 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
   // descriptors, in scalar registers: they begin at the piece and end with the expert's last row, or
   // with the row of x, or are empty.
   auto load = [&](const Work& k, Data& d) __attribute__((always_inline)) {
-    const bool live = k.block < total;
-    const int b = live ? k.block : 0;
-    const int e = uniform(bl.expert[b]), n = live ? uniform(bl.size[b]) : 0;
+    const int b = k.block, e = uniform(bl.expert[b]), n = uniform(bl.size[b]);
     // waves 2 r and 2 r + 1 stage the halves of row r
     const int row = wave >> 1, k0 = k.piece * kXK;
     const int pair = row < n ? uniform(bl.pair[kBlock * b + row]) : 0;
@@ -471,9 +469,9 @@ moe_gate_up_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ i
     const int r0 = k.band * kBandRows;
     const size_t first = (size_t)e * rows + r0;
     const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
-                                                  live ? (uint32_t)(rows - r0) * row_w - (uint32_t)k0 / 2 : 0u);
-    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
-                                                  live ? ((uint32_t)(rows - r0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+                                                  (uint32_t)(rows - r0) * row_w - (uint32_t)k0 / 2);
+    const __amdgpu_buffer_rsrc_t sres =
+        make_rsrc(scales + first * spr + k0 / G, ((uint32_t)(rows - r0) * spr - (uint32_t)k0 / G) * 2u);
 #pragma unroll
     for (int s = 0; s < kXSteps; ++s) {
       const bool in = (uint32_t)(k0 + s * kStepK) + 32u * lchunk < (uint32_t)K;     // (else: the next row's)
@@ -571,19 +569,18 @@ moe_down_kernel(const uint16_t* __restrict__ h, const Blocks* __restrict__ block
     }
   };
   auto load = [&](const Work& k, Data& d) __attribute__((always_inline)) {
-    const bool live = k.block < total;
-    const int b = live ? k.block : 0, k0 = k.s * kStepK, n0 = k.band * kDownCols;
+    const int b = k.block, k0 = k.s * kStepK, n0 = k.band * kDownCols;
     // wave w stages the w-th KB: word w % 4 of the upper (w < 4) or lower parts; chunks past K were never written
     const __amdgpu_buffer_rsrc_t hres =
-        make_rsrc(reinterpret_cast<const uint8_t*>(h) + (size_t)(b * steps + k.s) * kHStep, live ? kHStep : 0u);
+        make_rsrc(reinterpret_cast<const uint8_t*>(h) + (size_t)(b * steps + k.s) * kHStep, kHStep);
     d.h = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                         hres, offset_if(k0 + 32 * c < K, 1024u * wave + 16u * lane), 0, 0));
     __builtin_amdgcn_sched_barrier(0);
     const size_t first = (size_t)uniform(bl.expert[b]) * N + n0;
     const __amdgpu_buffer_rsrc_t wres = make_rsrc(reinterpret_cast<const uint8_t*>(packed) + first * row_w + k0 / 2,
-                                                  live ? (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2 : 0u);
-    const __amdgpu_buffer_rsrc_t sres = make_rsrc(scales + first * spr + k0 / G,
-                                                  live ? ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u : 0u);
+                                                  (uint32_t)(N - n0) * row_w - (uint32_t)k0 / 2);
+    const __amdgpu_buffer_rsrc_t sres =
+        make_rsrc(scales + first * spr + k0 / G, ((uint32_t)(N - n0) * spr - (uint32_t)k0 / G) * 2u);
     const bool in = (uint32_t)k0 + 32u * lchunk < (uint32_t)K;
     const uint32_t wo = offset_if(in, w_off), so = offset_if(in, s_off);
 #pragma unroll
