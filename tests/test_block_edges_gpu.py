@@ -212,3 +212,33 @@ def test_small_products_between_the_experts_kernels(w4, tokens, topk, size):
             bar[t] += ws * (np.abs(w2) @ (2.0 ** -20 * np.abs(h) + np.maximum(2.0 ** -23 * np.abs(h), 2.0 ** -28)
                                           + (inter + topk + 8) * 2.0 ** -24 * np.abs(h)))
     assert np.all(np.abs(y - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -25 + bar)
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("tokens", [5, 60, 300])
+def test_masked_router_into_the_experts(w4, tokens, renormalize):
+    """Tokens that the router leaves with fewer experts than slots, or none, go through the four calls, and (few tokens)
+    through moe_ffn, as through the formula with the slots left out."""
+    torch = torch_mod()
+    from gpu_util import assert_close
+    from test_moe_ffn_gpu import Layer
+    experts, topk, hidden = 12, 4, 256
+    layer = Layer(w4, experts, hidden, 128, 32, 87700 + tokens)
+    rng = layer.rng
+    logits = rng.standard_normal((tokens, experts)).astype(np.float32)
+    logits[rng.random(logits.shape) < 0.7] = -np.inf
+    logits[1] = -np.inf
+    x = dev(rng.standard_normal((tokens, hidden)).astype(np.float16))
+    ids, w = w4.moe_topk(dev(logits), topk, renormalize=renormalize)
+    assert bool((ids == -1).any(dim=1).any()) and bool((ids[1] == -1).all())
+    want, bar = layer.formula(host(x), host(ids), host(w))
+    gu, gs, dn, ds = layer.args
+    offs, tok, row = w4.moe_route(ids, experts)
+    h = w4.grouped_gemm_swiglu(x, gu, gs, offs, 32, pair_token=tok)
+    y = host(w4.moe_combine(w4.grouped_gemm(h, dn, ds, offs, 32), row, w))
+    assert np.all(y[1] == 0)
+    some = np.abs(want).sum(axis=1) > 0
+    assert_close(y[some], want[some], "four calls")
+    if tokens <= 64:
+        y = host(layer(x, ids, w)).astype(np.float64)
+        assert np.all(np.abs(y - want) <= bar) and np.all(y[1] == 0)
