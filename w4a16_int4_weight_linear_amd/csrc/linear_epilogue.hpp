@@ -30,8 +30,7 @@ __device__ inline float gelu_tanh_gate(float z) {
 // range from there on), found by linear programming against scipy's erfcx: 2^-22.8.  Evaluated in
 // fp32, the rounding of z^2 / 2 before the exponential grows with it: largest relative error (numpy's fp32 in
 // these steps, 2 million values a range) 2^-20.7 to |z| = 2, 2^-20.1 to 4, 2^-18.5 to 8, 2^-17.0 to 13, where Phi is
-// 1e-38; half a step of fp16 is 2^-11.  17 instructions; erfcf, which is within some fp32 units in the last
-// place throughout, takes some 60.
+// 1e-38; half a step of fp16 is 2^-11.  17 instructions; erfcf takes some 60.
 __device__ inline float normal_gate(float z, float& e) {
   e = __expf(-0.5f * z * z);
   const float t = reciprocal(__builtin_fmaf(0.3f, __builtin_fabsf(z), 1.0f));

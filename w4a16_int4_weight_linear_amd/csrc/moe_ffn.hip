@@ -28,10 +28,11 @@
 // tokens took 62 + 37 us instead of 56 + 38 (as they were then).  Weight loads bypass the caches' retention (kStream):
 // the first product 66 instead of 104 us, both as they were then.
 //
-// Measured (MI355X, operands from memory; 2048 x 512, group 32, 256 experts, 8 slots a token): 1 token 5.2 + 5.0 us
-// (launch and one trip to memory each), 8 tokens 15.3 + 10.3, 16 tokens 25 + 15.5 + 5, 32 tokens 37 + 23 + 5, 64
-// tokens 51 + 31.5 + 5 us: 391 MB of used experts' weights at 4.7 TB/s over both products, against 4.9 of a large
-// copy.  What is left is the fixed part (launch, sorting the pairs, the last work items) and the third kernel.
+// Measured (MI355X, operands from memory, medians; 2048 x 512, group 32, 256 experts, 8 slots a token): 1 token 5.4 + 4.9 us
+// (launch and one trip to memory each), 8 tokens 15.4 + 10.6, 16 tokens 25.3 + 17.8 + 4.8, 32 tokens 37.7 + 24.0 + 4.8, 64
+// tokens 51.2 + 32.0 + 4.8 us (31.2 to 36.5 by which experts are used): 391 MB of their weights at 4.4-4.7 TB/s over both
+// products, against 4.9 of a large copy.  What is left is the fixed part (launch, sorting the pairs, the last work items)
+// and the third kernel.
 //
 // h goes between the kernels as two fp16 parts, h 2^-8 = hi + lo 2^-11: off by at most 2^-23 |h|, or by 2^-28 where that
 // is more (|h| below 2^-5: lo is subnormal there), for |h| up to 2^24.  Rounded once to fp16 it would add as much error
@@ -259,7 +260,8 @@ __host__ __device__ inline int h_steps(int inter) { return (inter + kStepK - 1) 
 // ---- few pairs: each by itself ----
 // Up to this many: two launches and no sorting.  Direct against grouped: 32 pairs of experts that are nearly all
 // different 9.4 + 6.7 against 10.9 + 6.9 + 4.8 us, 64 pairs 15.3 + 10.3 against 17.2 + 10.9 + 4.9; of twelve experts 32 pairs 9.1
-// + 6.7 against 7.7 + 5.2 + 4.9, 64 pairs 14.0 + 9.7 against 9.3 + 5.7 + 4.9 (the host cannot know which).  Also what
+// + 6.7 against 7.7 + 5.2 + 4.9, 64 pairs 14.0 + 9.7 against 9.3 + 5.7 + 4.9: there the grouped form is faster by a sixth,
+// at different experts slower by a quarter, and the host, which chooses, does not see the ids.  Also what
 // moe_down_direct_kernel holds: an id per lane, a result per pair in LDS.
 constexpr int kDirectPairs = 64;
 constexpr int kBandRows = 4 * kWaves;            // gate/up rows of a workgroup: four per wave
